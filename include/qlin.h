@@ -312,6 +312,153 @@ qlin_status qlin_grouped_select_variant(qlin_format fmt, int groups, int N, int 
 qlin_status qlin_grouped_workspace_bytes(qlin_format fmt, int groups, int N, int K, int total_rows,
                                          int max_group_rows, const qlin_config *cfg, size_t *bytes);
 
+/* ------------------------------------------------- rows with their own weights
+ *
+ * Routing tokens to experts, the way into the grouped product and back out of
+ * it, and low-rank adapters beside a shared projection.  The pages name MoE
+ * layers as the next target ("Building a High-Performance and Portable vLLM
+ * Linear Backend with Helion", section "Future work", model-coverage
+ * paragraph); these calls surround qlin_grouped_gemm and qlin_linear.
+ */
+
+typedef enum {
+    QLIN_SCORE_SOFTMAX = 0, /* s = softmax over the token's open experts */
+    QLIN_SCORE_SIGMOID = 1  /* s = 1 / (1 + exp(-logit))                 */
+} qlin_score;
+
+typedef enum {
+    QLIN_GROUP_MAX = 0, /* an expert group is worth its best expert       */
+    QLIN_GROUP_TOP2 = 1 /* ... the sum of its two best experts            */
+} qlin_group_score;
+
+/* One router.
+ *   experts      E, 1..QLIN_MAX_EXPERTS
+ *   topk         experts per token, 1..min(E, QLIN_MAX_TOPK)
+ *   score        qlin_score
+ *   groups       consecutive expert groups of E / groups experts, 1..64,
+ *                dividing E; 1: the choice is not limited to groups
+ *   topk_groups  groups a token may choose from, 1..groups
+ *   group_score  qlin_group_score
+ *   renormalize  1: the weights of a token's experts are divided by their sum
+ *   scale        factor on the weights (finite)                             */
+typedef struct {
+    int32_t experts;
+    int32_t topk;
+    int32_t score;
+    int32_t groups;
+    int32_t topk_groups;
+    int32_t group_score;
+    int32_t renormalize;
+    float scale;
+} qlin_router;
+
+#define QLIN_MAX_EXPERTS 1024
+#define QLIN_MAX_TOPK 32
+
+/* Routing: which experts each token takes, with which weights, and the rows
+ * grouped by expert that qlin_grouped_gemm takes.
+ *   logits   [T, ld] of logit_type (QLIN_OUT_BF16 or QLIN_OUT_F32_ACC, as
+ *            qlin_linear writes them), ld >= experts
+ *   bias     fp32 [experts] or NULL: added to the scores for the choice
+ *            only (a load balance); the weights do not have it
+ *   ids      int32 [T][topk], best first
+ *   weights  fp32 [T][topk]
+ *   group_offsets  int32 [experts + 1]: expert e owns rows
+ *            [off[e], off[e + 1]); off[experts] rows are in use
+ *   rows     int32 [T * topk]: the token of each row, -1 past the rows in use
+ *   slots    int32 [T][topk]: the row of each (token, choice)
+ * The choice.  An expert whose logit is -inf or NaN is closed to the token;
+ * +inf counts as the largest finite fp32.  c = s + bias (an expert whose bias
+ * is NaN or -inf is never chosen).  With groups, the topk_groups groups worth
+ * most stay open (the worth is over c).  Then the topk largest c are chosen.
+ * Ties, of groups too, go to the lowest index.  The order is that of the
+ * logits where neither a bias nor QLIN_GROUP_TOP2 comes in, and of scores in
+ * 64 bits otherwise: it does not depend on the order of any sum.  Where fewer
+ * than topk experts are open, the remaining choices have id -1, weight 0,
+ * slot -1 and no row.
+ * The weights: scale x s, or scale x s / (the sum of the token's chosen s),
+ * 0 where that sum is 0.
+ * Rows are in expert order and, within an expert, in token order.
+ *   workspace  qlin_route_workspace_bytes(router, T) bytes (may be 0); needs
+ *              no initial value.  Calls that overlap in time must not share it.
+ * T may be 0: offsets are zeroed and nothing else is written.
+ * Errors: QLIN_ERR_INVALID_ARG (a null pointer, a router field out of range),
+ * QLIN_ERR_ALIGNMENT (ld < experts, pointers not aligned to their element),
+ * QLIN_ERR_SHAPE (T < 0, T x topk over 2^20), QLIN_ERR_WORKSPACE. */
+qlin_status qlin_route(const qlin_router *router, int T, const void *logits, int64_t ld,
+                       qlin_out_type logit_type, const float *bias, int32_t *ids, float *weights,
+                       int32_t *group_offsets, int32_t *rows, int32_t *slots, void *workspace,
+                       size_t ws_bytes, void *stream);
+qlin_status qlin_route_workspace_bytes(const qlin_router *router, int T, size_t *bytes);
+
+/* The way into the experts: every token is quantized once, as
+ * qlin_quantize_act does, and its codes and scales are stored at each of its
+ * rows: (xq, x_scales)[slots[t][j]] = quant(x[t]).
+ *   x          bf16 [T, ldx] (ldx >= K, ldx % 8 == 0)
+ *   slots      int32 [T][topk] from qlin_route; entries outside
+ *              [0, total_rows) are skipped
+ *   xq         [total_rows, K] codes, x_scales fp32 [total_rows] or
+ *              [total_rows][K/128] for QLIN_BLOCK_FP8; rows that no slot
+ *              names are left as they were
+ * Errors as qlin_quantize_act; QLIN_ERR_SHAPE for topk < 1, topk >
+ * QLIN_MAX_TOPK, T x topk over 2^20 or total_rows outside [0, 2^20]. */
+qlin_status qlin_dispatch_quantize(qlin_format fmt, int T, int topk, int K, const void *x, int64_t ldx,
+                                   const int32_t *slots, int total_rows, void *xq, float *x_scales,
+                                   void *stream);
+
+/* The way back: y[t] = add[t] + sum over j of weights[t][j] h[slots[t][j]].
+ *   h        [total_rows, ldh] of h_type (QLIN_OUT_BF16 or QLIN_OUT_F32_ACC)
+ *   slots    int32 [T][topk] from qlin_route; entries outside
+ *            [0, total_rows) add nothing, whatever their weight is
+ *   weights  fp32 [T][topk]
+ *   add      [T, ldadd] of y_type (a residual, a shared expert's output), or
+ *            NULL; may be y itself (then ldadd must be ldy)
+ *   y        [T, ldy] of y_type (QLIN_OUT_BF16 or QLIN_OUT_F32_ACC)
+ * The sum is in fp32, in the order of j, with add last, and rounded once.
+ * N % 16 == 0; leading dimensions are >= N and whole 16-byte units; ldadd is
+ * not looked at without add.  h must not overlap y.  T may be 0.
+ * Errors: QLIN_ERR_INVALID_ARG (a null pointer, an unknown type), QLIN_ERR_SHAPE
+ * (T, topk, N or total_rows out of range), QLIN_ERR_ALIGNMENT. */
+qlin_status qlin_combine(int T, int topk, int N, const void *h, int64_t ldh, qlin_out_type h_type,
+                         const int32_t *slots, const float *weights, int total_rows, const void *add,
+                         int64_t ldadd, void *y, int64_t ldy, qlin_out_type y_type, void *stream);
+
+#define QLIN_MAX_ADAPTERS 4096
+#define QLIN_MAX_RANK 256
+
+/* Low-rank adapters of many requests beside a shared projection:
+ *   y[m] = base[m] + scales[a] B_a (A_a x[m]),   a = ids[m].
+ *   x        bf16 [M, ldx] (ldx >= K, ldx % 8 == 0)
+ *   ids      int32 [M] on the device: the adapter of each row, in any order;
+ *            outside [0, adapters): none, y[m] = base[m]
+ *   A        bf16 [adapters][max_rank][K]
+ *   B        bf16 [adapters][N][max_rank]
+ *   ranks    int32 [adapters] or NULL (all max_rank): adapter a uses its
+ *            first ranks[a] rows of A and columns of B (clamped to
+ *            [0, max_rank]); what lies past them is not used, whatever it is
+ *   scales   fp32 [adapters] or NULL (1)
+ *   base     [M, ldb] of out_type (the shared projection's output), or NULL
+ *            (0); may be y itself (then ldb must be ldy)
+ *   y        [M, ldy] of out_type (QLIN_OUT_BF16 or QLIN_OUT_F32_ACC)
+ * A projection that is a slice of a wider one (q, k, v) takes base and y as
+ * views: column offsets in whole 16-byte units, ldb and ldy the wide one's.
+ * Sums are fp32; the product A_a x is kept to at least 16 bits (24 for
+ * QLIN_OUT_F32_ACC) of mantissa between the two products; y is rounded once.
+ * N % 16 == 0, K % 16 == 0, max_rank % 8 == 0 up to QLIN_MAX_RANK; leading
+ * dimensions are whole 16-byte units; ldb is not looked at without base.
+ *   workspace  qlin_lora_workspace_bytes(...) bytes; needs no initial value.
+ *              Calls that overlap in time must not share it.
+ * M may be 0.  A row's result depends on the call's sizes and on the row's
+ * own data, not on which adapters the other rows have.
+ * Errors: QLIN_ERR_INVALID_ARG (a null pointer, an unknown type), QLIN_ERR_SHAPE
+ * (a size out of range or not a multiple), QLIN_ERR_ALIGNMENT (a pointer or a
+ * leading dimension), QLIN_ERR_WORKSPACE. */
+qlin_status qlin_lora(int M, int N, int K, int adapters, int max_rank, const void *x, int64_t ldx,
+                      const int32_t *ids, const void *A, const void *B, const int32_t *ranks,
+                      const float *scales, const void *base, int64_t ldb, void *y, int64_t ldy,
+                      qlin_out_type out_type, void *workspace, size_t ws_bytes, void *stream);
+qlin_status qlin_lora_workspace_bytes(int M, int N, int K, int adapters, int max_rank, size_t *bytes);
+
 /* Selection table.  qlin_load_table parses a text table (replacing any loaded
  * one; path NULL = the table installed next to the library); the table is
  * immutable afterwards, so lookups are thread-safe.  qlin_set_strict(1)

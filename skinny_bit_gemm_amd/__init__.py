@@ -33,6 +33,8 @@ EXPORTS = (
     "qlin_graph_destroy", "qlin_status_str", "qlin_abi_version", "qlin_last_hip_error",
     "qlin_grouped_gemm", "qlin_grouped_select_variant", "qlin_grouped_workspace_bytes",
     "qlin_linear_scratch", "qlin_packed_weight_bytes", "qlin_pack_weight", "qlin_quantize_act_cfg",
+    "qlin_route", "qlin_route_workspace_bytes", "qlin_dispatch_quantize", "qlin_combine", "qlin_lora",
+    "qlin_lora_workspace_bytes",
 )
 # format flag: the weight codes are in the packed layout of qlin_pack_weight
 QLIN_PACKED_WEIGHTS = 0x100
@@ -71,6 +73,24 @@ class qlin_config(ctypes.Structure):
 def make_config(swap_ab=0, split_k=1, tile_m=16, tile_n=32, waves=4, k_waves=4, reduce=0,
                 act_path=0) -> qlin_config:
     return qlin_config(swap_ab, split_k, tile_m, tile_n, waves, k_waves, reduce, act_path)
+
+
+# qlin_router: how logits become scores, and what a group of experts is worth
+QLIN_SCORE_SOFTMAX, QLIN_SCORE_SIGMOID = 0, 1
+QLIN_GROUP_MAX, QLIN_GROUP_TOP2 = 0, 1
+QLIN_MAX_EXPERTS, QLIN_MAX_TOPK = 1024, 32
+QLIN_MAX_ADAPTERS, QLIN_MAX_RANK = 4096, 256
+
+
+class qlin_router(ctypes.Structure):
+    _fields_ = [("experts", ctypes.c_int32), ("topk", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32), ("group_score", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+def make_router(experts, topk, score=QLIN_SCORE_SOFTMAX, groups=1, topk_groups=1, group_score=QLIN_GROUP_MAX,
+                renormalize=1, scale=1.0) -> qlin_router:
+    return qlin_router(experts, topk, score, groups, topk_groups, group_score, renormalize, scale)
 
 
 _lib = None
@@ -113,6 +133,12 @@ def lib():
         L.qlin_grouped_select_variant.argtypes = [_I, _I, _I, _I, _I, ctypes.POINTER(qlin_config)]
         L.qlin_grouped_workspace_bytes.argtypes = [_I, _I, _I, _I, _I, _I, ctypes.POINTER(qlin_config),
                                                    ctypes.POINTER(_SZ)]
+        L.qlin_route.argtypes = [ctypes.POINTER(qlin_router), _I, _P, _I64, _I, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
+        L.qlin_route_workspace_bytes.argtypes = [ctypes.POINTER(qlin_router), _I, ctypes.POINTER(_SZ)]
+        L.qlin_dispatch_quantize.argtypes = [_I, _I, _I, _I, _P, _I64, _P, _I, _P, _P, _P]
+        L.qlin_combine.argtypes = [_I, _I, _I, _P, _I64, _I, _P, _P, _I, _P, _I64, _P, _I64, _I, _P]
+        L.qlin_lora.argtypes = [_I, _I, _I, _I, _I, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _P, _I64, _I, _P, _SZ, _P]
+        L.qlin_lora_workspace_bytes.argtypes = [_I, _I, _I, _I, _I, ctypes.POINTER(_SZ)]
         L.qlin_load_table.argtypes = [ctypes.c_char_p]
         L.qlin_set_strict.argtypes = [_I]
         L.qlin_table_entries.argtypes = []
@@ -146,6 +172,10 @@ def _stream(stream) -> int | None:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _nbytes(t) -> int:
+    return t.nbytes if t is not None and not isinstance(t, int) else 0
 
 
 def _check(st: int, what: str, raise_on_error: bool):
@@ -251,6 +281,54 @@ def qlin_grouped_workspace_bytes(fmt, groups, N, K, total_rows, max_group_rows, 
     st = lib().qlin_grouped_workspace_bytes(fmt, groups, N, K, total_rows, max_group_rows,
                                             ctypes.byref(cfg) if cfg is not None else None, ctypes.byref(out))
     _check(st, "qlin_grouped_workspace_bytes", True)
+    return int(out.value)
+
+
+def qlin_route(router, T, logits, ld, logit_type, bias, ids, weights, group_offsets, rows, slots, workspace=None,
+               ws_bytes=None, stream=None, raise_on_error=True):
+    if ws_bytes is None:
+        ws_bytes = _nbytes(workspace)
+    rptr = ctypes.byref(router) if router is not None else None
+    st = lib().qlin_route(rptr, T, _ptr(logits), ld, logit_type, _ptr(bias), _ptr(ids), _ptr(weights),
+                          _ptr(group_offsets), _ptr(rows), _ptr(slots), _ptr(workspace), ws_bytes, _stream(stream))
+    return _check(st, "qlin_route", raise_on_error)
+
+
+def qlin_route_workspace_bytes(router, T) -> int:
+    out = _SZ(0)
+    st = lib().qlin_route_workspace_bytes(ctypes.byref(router) if router is not None else None, T, ctypes.byref(out))
+    _check(st, "qlin_route_workspace_bytes", True)
+    return int(out.value)
+
+
+def qlin_dispatch_quantize(fmt, T, topk, K, x, ldx, slots, total_rows, xq, x_scales, stream=None,
+                           raise_on_error=True):
+    st = lib().qlin_dispatch_quantize(fmt, T, topk, K, _ptr(x), ldx, _ptr(slots), total_rows, _ptr(xq),
+                                      _ptr(x_scales), _stream(stream))
+    return _check(st, "qlin_dispatch_quantize", raise_on_error)
+
+
+def qlin_combine(T, topk, N, h, ldh, h_type, slots, weights, total_rows, add, ldadd, y, ldy, y_type=QLIN_OUT_BF16,
+                 stream=None, raise_on_error=True):
+    st = lib().qlin_combine(T, topk, N, _ptr(h), ldh, h_type, _ptr(slots), _ptr(weights), total_rows, _ptr(add),
+                            ldadd, _ptr(y), ldy, y_type, _stream(stream))
+    return _check(st, "qlin_combine", raise_on_error)
+
+
+def qlin_lora(M, N, K, adapters, max_rank, x, ldx, ids, A, B, ranks, scales, base, ldb, y, ldy,
+              out_type=QLIN_OUT_BF16, workspace=None, ws_bytes=None, stream=None, raise_on_error=True):
+    if ws_bytes is None:
+        ws_bytes = _nbytes(workspace)
+    st = lib().qlin_lora(M, N, K, adapters, max_rank, _ptr(x), ldx, _ptr(ids), _ptr(A), _ptr(B), _ptr(ranks),
+                         _ptr(scales), _ptr(base), ldb, _ptr(y), ldy, out_type, _ptr(workspace), ws_bytes,
+                         _stream(stream))
+    return _check(st, "qlin_lora", raise_on_error)
+
+
+def qlin_lora_workspace_bytes(M, N, K, adapters, max_rank) -> int:
+    out = _SZ(0)
+    st = lib().qlin_lora_workspace_bytes(M, N, K, adapters, max_rank, ctypes.byref(out))
+    _check(st, "qlin_lora_workspace_bytes", True)
     return int(out.value)
 
 

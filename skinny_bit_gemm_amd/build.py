@@ -22,7 +22,7 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-munsafe-fp-a
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
           "-Wall", "-Wno-unused-function", "-Wno-unused-command-line-argument"]
 SOURCES = ["qlin_gemm_fp8.hip", "qlin_gemm_i8.hip", "qlin_gemm_block.hip", "qlin_kernels.hip",
-           "qlin_api.cpp", "qlin_table.cpp"]
+           "qlin_route.hip", "qlin_lora.hip", "qlin_api.cpp", "qlin_table.cpp"]
 PROBE_SOURCES = ["qlin_probe.hip"]
 
 

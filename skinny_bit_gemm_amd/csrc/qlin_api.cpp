@@ -560,6 +560,214 @@ qlin_status qlin_pack_weight(int batch, int N, int K, const void *wq, void *wq_p
     return hip_status(launch_pack_weight(batch, N, K, wq, wq_packed, static_cast<hipStream_t>(stream)));
 }
 
+// ------------------------------------------------- rows with their own weights
+
+static qlin_status check_router(const qlin_router *r) {
+    if (!r) return QLIN_ERR_INVALID_ARG;
+    if (r->experts < 1 || r->experts > QLIN_MAX_EXPERTS) return QLIN_ERR_INVALID_ARG;
+    if (r->topk < 1 || r->topk > QLIN_MAX_TOPK || r->topk > r->experts) return QLIN_ERR_INVALID_ARG;
+    if (r->score != QLIN_SCORE_SOFTMAX && r->score != QLIN_SCORE_SIGMOID) return QLIN_ERR_INVALID_ARG;
+    if (r->groups < 1 || r->groups > 64 || r->experts % r->groups != 0) return QLIN_ERR_INVALID_ARG;
+    if (r->topk_groups < 1 || r->topk_groups > r->groups) return QLIN_ERR_INVALID_ARG;
+    if (r->group_score != QLIN_GROUP_MAX && r->group_score != QLIN_GROUP_TOP2) return QLIN_ERR_INVALID_ARG;
+    if (r->renormalize != 0 && r->renormalize != 1) return QLIN_ERR_INVALID_ARG;
+    if (!(r->scale - r->scale == 0.0f)) return QLIN_ERR_INVALID_ARG;   // inf or NaN
+    return QLIN_OK;
+}
+
+static bool row_type_ok(qlin_out_type t) { return t == QLIN_OUT_BF16 || t == QLIN_OUT_F32_ACC; }
+static int row_type_bytes(qlin_out_type t) { return t == QLIN_OUT_BF16 ? 2 : 4; }
+static bool aligned2(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+// a leading dimension of at least n elements, in whole 16-byte units
+static bool ld_ok(int64_t ld, int n, int bytes) { return ld >= n && ld % (16 / bytes) == 0; }
+
+static size_t route_ws(const qlin_router *r, int T) {
+    const int blocks = route_blocks(T);
+    return blocks > 1 ? align256((size_t)blocks * r->experts * 2) : 0;
+}
+
+static qlin_status check_tokens(int T, int topk) {
+    return T < 0 || topk < 1 || topk > QLIN_MAX_TOPK || (int64_t)T * topk > kMaxDim ? QLIN_ERR_SHAPE : QLIN_OK;
+}
+
+qlin_status qlin_route_workspace_bytes(const qlin_router *router, int T, size_t *bytes) {
+    if (!bytes) return QLIN_ERR_INVALID_ARG;
+    qlin_status st = check_router(router);
+    if (st != QLIN_OK) return st;
+    st = check_tokens(T, router->topk);
+    if (st != QLIN_OK) return st;
+    *bytes = route_ws(router, T);
+    return QLIN_OK;
+}
+
+qlin_status qlin_route(const qlin_router *router, int T, const void *logits, int64_t ld,
+                       qlin_out_type logit_type, const float *bias, int32_t *ids, float *weights,
+                       int32_t *group_offsets, int32_t *rows, int32_t *slots, void *workspace,
+                       size_t ws_bytes, void *stream) {
+    qlin_status st = check_router(router);
+    if (st != QLIN_OK) return st;
+    if (!row_type_ok(logit_type)) return QLIN_ERR_INVALID_ARG;
+    st = check_tokens(T, router->topk);
+    if (st != QLIN_OK) return st;
+    if (!logits || !ids || !weights || !group_offsets || !rows || !slots) return QLIN_ERR_INVALID_ARG;
+    if (ld < router->experts) return QLIN_ERR_ALIGNMENT;
+    if (!(logit_type == QLIN_OUT_BF16 ? aligned2(logits) : aligned4(logits)) || !aligned4(bias) || !aligned4(ids) ||
+        !aligned4(weights) || !aligned4(group_offsets) || !aligned4(rows) || !aligned4(slots))
+        return QLIN_ERR_ALIGNMENT;
+    const size_t need = route_ws(router, T);
+    if (need && (!workspace || ws_bytes < need)) return QLIN_ERR_WORKSPACE;
+    if (need && !aligned16(workspace)) return QLIN_ERR_ALIGNMENT;
+    RouteLaunch a = {};
+    a.logits = logits;
+    a.ld = ld;
+    a.logits_bf16 = logit_type == QLIN_OUT_BF16;
+    a.bias = bias;
+    a.T = T;
+    a.experts = router->experts;
+    a.topk = router->topk;
+    a.score = router->score;
+    a.groups = router->groups;
+    a.group_size = router->experts / router->groups;
+    a.group_recip = ((1u << 22) + a.group_size - 1) / a.group_size;
+    a.topk_groups = router->topk_groups;
+    a.group_top2 = router->groups > 1 && router->group_score == QLIN_GROUP_TOP2;
+    a.renormalize = router->renormalize;
+    a.scale = router->scale;
+    a.ids = ids;
+    a.weights = weights;
+    a.offsets = group_offsets;
+    a.rows = rows;
+    a.slots = slots;
+    a.hist = static_cast<uint16_t *>(workspace);
+    a.block_tokens = route_block_tokens(T);
+    return hip_status(launch_route(a, static_cast<hipStream_t>(stream)));
+}
+
+qlin_status qlin_dispatch_quantize(qlin_format fmt, int T, int topk, int K, const void *x, int64_t ldx,
+                                   const int32_t *slots, int total_rows, void *xq, float *x_scales,
+                                   void *stream) {
+    if (!fmt_ok(fmt)) return QLIN_ERR_INVALID_ARG;
+    const qlin_status st = check_tokens(T, topk);
+    if (st != QLIN_OK) return st;
+    if (K < 16 || K > kMaxDim || K % 16 != 0 || total_rows < 0 || total_rows > kMaxDim) return QLIN_ERR_SHAPE;
+    if (fmt == QLIN_BLOCK_FP8 && K % kGroup != 0) return QLIN_ERR_SHAPE;
+    if (ldx < K || ldx % 8 != 0) return QLIN_ERR_ALIGNMENT;
+    if (!x || !slots || !xq || !x_scales) return QLIN_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned4(slots) || !aligned16(xq) || !aligned4(x_scales)) return QLIN_ERR_ALIGNMENT;
+    if (T == 0 || total_rows == 0) return QLIN_OK;
+    DispatchLaunch a = {};
+    a.x = static_cast<const uint16_t *>(x);
+    a.ldx = ldx;
+    a.slots = slots;
+    a.xq = static_cast<uint8_t *>(xq);
+    a.xs = x_scales;
+    a.T = T;
+    a.topk = topk;
+    a.K = K;
+    a.total_rows = total_rows;
+    return hip_status(launch_dispatch(fmt, a, static_cast<hipStream_t>(stream)));
+}
+
+qlin_status qlin_combine(int T, int topk, int N, const void *h, int64_t ldh, qlin_out_type h_type,
+                         const int32_t *slots, const float *weights, int total_rows, const void *add,
+                         int64_t ldadd, void *y, int64_t ldy, qlin_out_type y_type, void *stream) {
+    if (!row_type_ok(h_type) || !row_type_ok(y_type)) return QLIN_ERR_INVALID_ARG;
+    const qlin_status st = check_tokens(T, topk);
+    if (st != QLIN_OK) return st;
+    if (N < 16 || N > kMaxDim || N % 16 != 0 || total_rows < 0 || total_rows > kMaxDim) return QLIN_ERR_SHAPE;
+    if (!h || !slots || !weights || !y) return QLIN_ERR_INVALID_ARG;
+    if (!ld_ok(ldh, N, row_type_bytes(h_type)) || !ld_ok(ldy, N, row_type_bytes(y_type))) return QLIN_ERR_ALIGNMENT;
+    if (add && !ld_ok(ldadd, N, row_type_bytes(y_type))) return QLIN_ERR_ALIGNMENT;
+    if (add == y && ldadd != ldy) return QLIN_ERR_INVALID_ARG;
+    if (!aligned16(h) || !aligned16(y) || !aligned16(add) || !aligned4(slots) || !aligned4(weights))
+        return QLIN_ERR_ALIGNMENT;
+    if (T == 0) return QLIN_OK;
+    CombineLaunch a = {};
+    a.h = h;
+    a.ldh = ldh;
+    a.slots = slots;
+    a.weights = weights;
+    a.add = add;
+    a.ldadd = ldadd;
+    a.y = y;
+    a.ldy = ldy;
+    a.T = T;
+    a.topk = topk;
+    a.N = N;
+    a.total_rows = total_rows;
+    return hip_status(launch_combine(h_type == QLIN_OUT_F32_ACC, y_type == QLIN_OUT_F32_ACC, a,
+                                     static_cast<hipStream_t>(stream)));
+}
+
+static qlin_status check_lora_shape(int M, int N, int K, int adapters, int max_rank) {
+    if (M < 0 || M > kMaxDim || N < 16 || N > kMaxDim || N % 16 != 0 || K < 16 || K > kMaxDim || K % 16 != 0)
+        return QLIN_ERR_SHAPE;
+    if (adapters < 1 || adapters > QLIN_MAX_ADAPTERS) return QLIN_ERR_SHAPE;
+    if (max_rank < 8 || max_rank > QLIN_MAX_RANK || max_rank % 8 != 0) return QLIN_ERR_SHAPE;
+    return QLIN_OK;
+}
+
+qlin_status qlin_lora_workspace_bytes(int M, int N, int K, int adapters, int max_rank, size_t *bytes) {
+    if (!bytes) return QLIN_ERR_INVALID_ARG;
+    const qlin_status st = check_lora_shape(M, N, K, adapters, max_rank);
+    if (st != QLIN_OK) return st;
+    LoraPlan p = {};
+    if (M > 0) lora_plan(M, N, K, adapters, max_rank, &p);
+    *bytes = p.ws_bytes;
+    return QLIN_OK;
+}
+
+qlin_status qlin_lora(int M, int N, int K, int adapters, int max_rank, const void *x, int64_t ldx,
+                      const int32_t *ids, const void *A, const void *B, const int32_t *ranks,
+                      const float *scales, const void *base, int64_t ldb, void *y, int64_t ldy,
+                      qlin_out_type out_type, void *workspace, size_t ws_bytes, void *stream) {
+    if (!row_type_ok(out_type)) return QLIN_ERR_INVALID_ARG;
+    const qlin_status st = check_lora_shape(M, N, K, adapters, max_rank);
+    if (st != QLIN_OK) return st;
+    if (!x || !ids || !A || !B || !y) return QLIN_ERR_INVALID_ARG;
+    const int bytes = row_type_bytes(out_type);
+    if (!ld_ok(ldx, K, 2) || !ld_ok(ldy, N, bytes) || (base && !ld_ok(ldb, N, bytes))) return QLIN_ERR_ALIGNMENT;
+    if (base == y && ldb != ldy) return QLIN_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned4(ids) || !aligned16(A) || !aligned16(B) || !aligned4(ranks) || !aligned4(scales) ||
+        !aligned16(base) || !aligned16(y))
+        return QLIN_ERR_ALIGNMENT;
+    if (M == 0) return QLIN_OK;
+    LoraPlan p = {};
+    lora_plan(M, N, K, adapters, max_rank, &p);
+    if (!workspace || ws_bytes < p.ws_bytes) return QLIN_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return QLIN_ERR_ALIGNMENT;
+    char *ws = static_cast<char *>(workspace);
+    LoraLaunch a = {};
+    a.x = static_cast<const uint16_t *>(x);
+    a.ldx = ldx;
+    a.ids = ids;
+    a.A = static_cast<const uint16_t *>(A);
+    a.B = static_cast<const uint16_t *>(B);
+    a.ranks = ranks;
+    a.scales = scales;
+    a.base = base;
+    a.ldb = ldb;
+    a.y = y;
+    a.ldy = ldy;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.adapters = adapters;
+    a.max_rank = max_rank;
+    a.splits = p.splits;
+    a.k_steps = p.k_steps;
+    a.v_stride = p.v_stride;
+    a.n_chunk = p.n_chunk;
+    a.v = reinterpret_cast<float *>(ws + p.v_at);
+    if (p.sorted) {
+        a.tiles = reinterpret_cast<int4 *>(ws + p.tiles_at);
+        a.tile_count = reinterpret_cast<int *>(ws + p.count_at);
+        a.perm = reinterpret_cast<int *>(ws + p.perm_at);
+        a.place = reinterpret_cast<int *>(ws + p.place_at);
+    }
+    return hip_status(launch_lora(p, out_type == QLIN_OUT_F32_ACC, a, static_cast<hipStream_t>(stream)));
+}
+
 struct qlin_graph_s {
     hipGraphExec_t exec;
 };

@@ -88,6 +88,75 @@ struct Plan {
 qlin_status make_plan(qlin_format fmt, int M, int N, int K, const qlin_config &cfg, bool fused,
                       Plan *plan, bool grouped = false);
 
+// A routing launch (qlin_route), resolved on the host.
+struct RouteLaunch {
+    const void *logits;
+    int64_t ld;
+    int logits_bf16;
+    const float *bias;
+    int T, experts, topk, score;
+    int groups, group_size, topk_groups, group_top2;
+    uint32_t group_recip;      // ceil(2^22 / group_size)
+    int renormalize;
+    float scale;
+    int *ids;
+    float *weights;
+    int *offsets, *rows, *slots;
+    uint16_t *hist;            // more than one block: rows per (block, expert)
+    int block_tokens;
+};
+
+struct DispatchLaunch {
+    const uint16_t *x;
+    int64_t ldx;
+    const int *slots;
+    uint8_t *xq;
+    float *xs;
+    int T, topk, K, total_rows;
+};
+
+struct CombineLaunch {
+    const void *h;
+    int64_t ldh;
+    const int *slots;
+    const float *weights;
+    const void *add;
+    int64_t ldadd;
+    void *y;
+    int64_t ldy;
+    int T, topk, N, total_rows;
+};
+
+// How qlin_lora runs for given sizes (qlin_lora.hip).
+struct LoraPlan {
+    int sorted;                // the rows are sorted by adapter first
+    int ct;                    // 16-row sub-tiles per row tile
+    int max_tiles;             // row tiles, at most
+    int rt, rank_chunks;       // shrink: 16-rank sub-tiles per workgroup, workgroups along the ranks
+    int splits, k_steps;       // shrink: K parts, 32-wide steps for each wave of a part
+    int v_stride;              // floats between rows of v
+    int n_chunk;               // expand: columns per workgroup
+    size_t v_at, tiles_at, count_at, perm_at, place_at, ws_bytes;
+};
+
+struct LoraLaunch {
+    const uint16_t *x;
+    int64_t ldx;
+    const int *ids;
+    const uint16_t *A, *B;
+    const int *ranks;
+    const float *scales;
+    const void *base;
+    int64_t ldb;
+    void *y;
+    int64_t ldy;
+    int M, N, K, adapters, max_rank;
+    int splits, k_steps, v_stride, n_chunk;
+    float *v;                  // [splits][M][v_stride]
+    int4 *tiles;               // sorted: (adapter, first place, rows, 0)
+    int *tile_count, *perm, *place;
+};
+
 // Host-side selection table (qlin_table.cpp).
 qlin_status table_lookup(qlin_format fmt, int M, int N, int K, qlin_config *out, bool *found);
 qlin_status table_nearest(qlin_format fmt, int M, int N, int K, qlin_config *out, bool *found);
@@ -110,6 +179,13 @@ hipError_t launch_pack_weight(int batch, int N, int K, const void *wq, void *out
 // staged in LDS; -1: direct, each wave loads its own activation fragments)
 hipError_t launch_gemm(int fmt, bool swap, int tile_m, int nr, int xc, const GemmLaunch &g,
                        size_t lds_bytes, hipStream_t s);
+int route_block_tokens(int T);
+int route_blocks(int T);
+hipError_t launch_route(const RouteLaunch &a, hipStream_t s);
+hipError_t launch_dispatch(int fmt, const DispatchLaunch &a, hipStream_t s);
+hipError_t launch_combine(bool h32, bool y32, const CombineLaunch &a, hipStream_t s);
+void lora_plan(int M, int N, int K, int adapters, int max_rank, LoraPlan *p);
+hipError_t launch_lora(const LoraPlan &p, bool f32, const LoraLaunch &a, hipStream_t s);
 bool gemm_variant_exists(int fmt, bool swap, int tile_m, int nr, int xc);
 // this device's static scratch array (kScratchBytes, zero between calls);
 // see qlin_linear_scratch
