@@ -583,7 +583,7 @@ static bool ld_ok(int64_t ld, int n, int bytes) { return ld >= n && ld % (16 / b
 
 static size_t route_ws(const qlin_router *r, int T) {
     const int blocks = route_blocks(T);
-    return blocks > 1 ? align256((size_t)blocks * r->experts * 2) : 0;
+    return blocks > 1 ? align256((size_t)blocks * route_hist_stride(r->experts) * 2) : 0;
 }
 
 static qlin_status check_tokens(int T, int topk) {
@@ -639,7 +639,9 @@ qlin_status qlin_route(const qlin_router *router, int T, const void *logits, int
     a.rows = rows;
     a.slots = slots;
     a.hist = static_cast<uint16_t *>(workspace);
+    a.hist_stride = route_hist_stride(router->experts);
     a.block_tokens = route_block_tokens(T);
+    a.blocks = route_blocks(T);
     return hip_status(launch_route(a, static_cast<hipStream_t>(stream)));
 }
 

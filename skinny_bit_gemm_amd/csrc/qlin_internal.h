@@ -102,8 +102,9 @@ struct RouteLaunch {
     int *ids;
     float *weights;
     int *offsets, *rows, *slots;
-    uint16_t *hist;            // more than one block: rows per (block, expert)
-    int block_tokens;
+    uint16_t *hist;            // more than one block: rows per (block, expert), zeros up to the stride
+    int hist_stride;
+    int blocks, block_tokens;
 };
 
 struct DispatchLaunch {
@@ -181,6 +182,7 @@ hipError_t launch_gemm(int fmt, bool swap, int tile_m, int nr, int xc, const Gem
                        size_t lds_bytes, hipStream_t s);
 int route_block_tokens(int T);
 int route_blocks(int T);
+inline int route_hist_stride(int experts) { return (experts + 7) & ~7; }
 hipError_t launch_route(const RouteLaunch &a, hipStream_t s);
 hipError_t launch_dispatch(int fmt, const DispatchLaunch &a, hipStream_t s);
 hipError_t launch_combine(bool h32, bool y32, const CombineLaunch &a, hipStream_t s);

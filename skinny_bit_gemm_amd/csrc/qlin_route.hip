@@ -13,18 +13,25 @@ namespace qlin {
 
 namespace {
 
-constexpr int kRouteWaves = 16;                   // waves of a routing workgroup
-constexpr int kRouteThreads = 64 * kRouteWaves;
+constexpr int kRouteTokens = 16;                  // tokens a routing workgroup holds at once
+constexpr int kRouteThreads = 64 * kRouteTokens;
 constexpr float kFltMax = 3.402823466e38f;
+constexpr int kRouteRowTokens = 1024;             // tokens from which each has 16 lanes
 
-// ------------------------------------------------------------ wave reductions
+// ---------------------------------------------- reductions over a token's lanes
+//
+// A token has LPT lanes: a wave (64) or a row of 16.  Every lane of the token
+// gets the result.
 
-// one DPP step of an unsigned maximum / a sum (see max_dpp)
+// one DPP step of a maximum, a minimum or a sum (see max_dpp)
 template <int CTRL, int ROW_MASK = 0xF>
-__device__ __forceinline__ uint32_t umax_dpp(uint32_t v) {
-    const uint32_t moved = (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, ROW_MASK, 0xF, false);
-    return v > moved ? v : moved;
+__device__ __forceinline__ uint32_t moved_dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, ROW_MASK, 0xF, false);
 }
+template <int CTRL, int ROW_MASK = 0xF>
+__device__ __forceinline__ uint32_t umax_dpp(uint32_t v) { return max(v, moved_dpp<CTRL, ROW_MASK>(v)); }
+template <int CTRL, int ROW_MASK = 0xF>
+__device__ __forceinline__ uint32_t umin_dpp(uint32_t v) { return min(v, moved_dpp<CTRL, ROW_MASK>(v)); }
 template <int CTRL, int ROW_MASK = 0xF>
 __device__ __forceinline__ float add_dpp(float v) {
     return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROW_MASK, 0xF, false));
@@ -35,36 +42,69 @@ __device__ __forceinline__ double add_dpp(double v) {
     const int hi = __builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, ROW_MASK, 0xF, false);
     return v + __hiloint2double(hi, lo);
 }
-__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+
+template <int LPT>
+__device__ __forceinline__ uint32_t token_max(uint32_t v) {
     v = umax_dpp<0xB1>(v);
     v = umax_dpp<0x4E>(v);
     v = umax_dpp<0x141>(v);
     v = umax_dpp<0x140>(v);
-    v = umax_dpp<0x142, 0xA>(v);
-    v = umax_dpp<0x143, 0xC>(v);
-    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+    if constexpr (LPT == 64) {
+        v = umax_dpp<0x142, 0xA>(v);
+        v = umax_dpp<0x143, 0xC>(v);
+        v = (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+    }
+    return v;
 }
-__device__ __forceinline__ uint64_t wave_umax(uint64_t v) {
-    const uint32_t hi = wave_umax((uint32_t)(v >> 32));
-    const uint32_t lo = wave_umax((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+template <int LPT>
+__device__ __forceinline__ uint64_t token_max(uint64_t v) {
+    const uint32_t hi = token_max<LPT>((uint32_t)(v >> 32));
+    const uint32_t lo = token_max<LPT>((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
     return ((uint64_t)hi << 32) | lo;
 }
+template <int LPT>
+__device__ __forceinline__ uint32_t token_min(uint32_t v) {
+    v = umin_dpp<0xB1>(v);
+    v = umin_dpp<0x4E>(v);
+    v = umin_dpp<0x141>(v);
+    v = umin_dpp<0x140>(v);
+    if constexpr (LPT == 64) {
+        v = umin_dpp<0x142, 0xA>(v);
+        v = umin_dpp<0x143, 0xC>(v);
+        v = (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+    }
+    return v;
+}
+template <int LPT>
+__device__ __forceinline__ float token_max(float v) {
+    if constexpr (LPT == 64) return wave_max(v);
+    else return row16_max(v);
+}
 template <typename F>
-__device__ __forceinline__ F wave_sum_lane63(F v) {
+__device__ __forceinline__ F row16_sum(F v) {
     v = add_dpp<0xB1>(v);
     v = add_dpp<0x4E>(v);
     v = add_dpp<0x141>(v);
-    v = add_dpp<0x140>(v);
-    v = add_dpp<0x142, 0xA>(v);
-    return add_dpp<0x143, 0xC>(v);
+    return add_dpp<0x140>(v);
 }
-__device__ __forceinline__ float wave_sum(float v) {
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wave_sum_lane63(v)), 63));
+template <int LPT>
+__device__ __forceinline__ float token_sum(float v) {
+    v = row16_sum(v);
+    if constexpr (LPT == 64) {
+        v = add_dpp<0x143, 0xC>(add_dpp<0x142, 0xA>(v));
+        v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+    }
+    return v;
 }
-__device__ __forceinline__ double wave_sum(double v) {
-    v = wave_sum_lane63(v);
-    return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), 63),
-                            __builtin_amdgcn_readlane(__double2loint(v), 63));
+template <int LPT>
+__device__ __forceinline__ double token_sum(double v) {
+    v = row16_sum(v);
+    if constexpr (LPT == 64) {
+        v = add_dpp<0x143, 0xC>(add_dpp<0x142, 0xA>(v));
+        v = __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), 63),
+                             __builtin_amdgcn_readlane(__double2loint(v), 63));
+    }
+    return v;
 }
 
 // ------------------------------------------------------------- ordered keys
@@ -86,34 +126,44 @@ __device__ __forceinline__ double unordered(uint64_t k) {
     return __longlong_as_double((long long)(k >> 63 ? k ^ 0x8000000000000000ull : ~k));
 }
 
-// Lowest expert whose key is `best` (expert e = lane + 64 j): ballots in
-// the order of j, then the lowest lane.
-template <int EPL, typename Key>
-__device__ __forceinline__ int first_with(const Key (&key)[EPL], Key best) {
-    int at = -1;
+// Lowest expert whose key is `best` (expert e = lane + LPT j).
+template <int LPT, int EPL, typename Key>
+__device__ __forceinline__ uint32_t first_with(const Key (&key)[EPL], Key best, int lane) {
+    if constexpr (LPT == 64) {   // ballots in the order of j, then the lowest lane
+        int at = 0;
 #pragma unroll
-    for (int j = EPL - 1; j >= 0; --j) {
-        const uint64_t b = __ballot(key[j] == best);
-        if (b) at = 64 * j + __ffsll((unsigned long long)b) - 1;
+        for (int j = EPL - 1; j >= 0; --j) {
+            const uint64_t b = __ballot(key[j] == best);
+            if (b) at = 64 * j + __ffsll((unsigned long long)b) - 1;
+        }
+        return at;
+    } else {
+        uint32_t at = 0xFFFF;
+#pragma unroll
+        for (int j = EPL - 1; j >= 0; --j) at = key[j] == best ? lane + LPT * j : at;
+        return token_min<LPT>(at);
     }
-    return at;
 }
 
-// One token, by one wave: lane j < topk ends with the j-th chosen expert (-1:
-// none) and its weight.  Lane l holds experts l, l + 64, ...
-template <int EPL, bool WIDE>
-__device__ __forceinline__ void route_token(const RouteLaunch &a, int t, int lane, int &my_id, float &my_w) {
+// One token, by LPT lanes: lane j < topk ends with the j-th chosen expert
+// (-1: none) and its weight (topk > LPT: not here).  Lane l holds experts l,
+// l + LPT, ...  Rows past the call's tokens (`live` false) go along, closed.
+template <int LPT, int EPL, bool WIDE>
+__device__ __forceinline__ void route_token(const RouteLaunch &a, int t, bool live, int lane, int &my_id, float &my_w) {
     using Key = std::conditional_t<WIDE, uint64_t, uint32_t>;
     float l[EPL];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-        const int e = lane + 64 * j;
+        const int e = lane + LPT * j;
         l[j] = -INFINITY;
-        if (e < a.experts) {
+        if (live && e < a.experts) {
             const int64_t at = (int64_t)t * a.ld + e;
             l[j] = a.logits_bf16 ? __uint_as_float((uint32_t) static_cast<const uint16_t *>(a.logits)[at] << 16)
                                  : static_cast<const float *>(a.logits)[at];
         }
+    }
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
         if (l[j] != l[j]) l[j] = -INFINITY;
         l[j] = fminf(l[j], kFltMax);
     }
@@ -121,7 +171,7 @@ __device__ __forceinline__ void route_token(const RouteLaunch &a, int t, int lan
     if (a.score == QLIN_SCORE_SOFTMAX) {
 #pragma unroll
         for (int j = 0; j < EPL; ++j) top = fmaxf(top, l[j]);
-        top = wave_max(top);
+        top = token_max<LPT>(top);
     }
     // the order of the choice
     Key key[EPL];
@@ -134,7 +184,7 @@ __device__ __forceinline__ void route_token(const RouteLaunch &a, int t, int lan
                 s[j] = l[j] > -INFINITY ? exp((double)l[j] - (double)top) : 0.0;
                 sum += s[j];
             }
-            sum = wave_sum(sum);
+            sum = token_sum<LPT>(sum);
 #pragma unroll
             for (int j = 0; j < EPL; ++j) s[j] /= sum;
         } else {
@@ -143,7 +193,7 @@ __device__ __forceinline__ void route_token(const RouteLaunch &a, int t, int lan
         }
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-            const int e = lane + 64 * j;
+            const int e = lane + LPT * j;
             const float b = a.bias && e < a.experts ? a.bias[e] : 0.0f;
             key[j] = l[j] > -INFINITY && b > -INFINITY ? ordered(s[j] + (double)b) : 0;
         }
@@ -152,44 +202,49 @@ __device__ __forceinline__ void route_token(const RouteLaunch &a, int t, int lan
         for (int j = 0; j < EPL; ++j) key[j] = l[j] > -INFINITY ? ordered(l[j]) : 0;
     }
     if (a.groups > 1) {
-        Key worth = 0;   // lane g: group g's
+        uint64_t kept = 0;
+        Key worth[64 / LPT] = {};   // group g's: lane g % LPT, number g / LPT
         for (int g = 0; g < a.groups; ++g) {
             Key in[EPL], best = 0;
 #pragma unroll
             for (int j = 0; j < EPL; ++j) {
-                const int e = lane + 64 * j - g * a.group_size;
+                const int e = lane + LPT * j - g * a.group_size;
                 in[j] = e >= 0 && e < a.group_size ? key[j] : 0;
                 best = in[j] > best ? in[j] : best;
             }
-            best = wave_umax(best);
+            best = token_max<LPT>(best);
             if constexpr (WIDE) {
-                if (a.group_top2 && best != 0) {
-                    const int at = first_with(in, best);
+                if (a.group_top2) {
+                    const uint32_t at = first_with<LPT>(in, best, lane);
                     Key second = 0;
 #pragma unroll
                     for (int j = 0; j < EPL; ++j) {
-                        if (at == lane + 64 * j) in[j] = 0;
+                        if (at == (uint32_t)(lane + LPT * j)) in[j] = 0;
                         second = in[j] > second ? in[j] : second;
                     }
-                    second = wave_umax(second);
-                    if (second != 0) best = ordered(unordered(best) + unordered(second));
+                    second = token_max<LPT>(second);
+                    if (best != 0 && second != 0) best = ordered(unordered(best) + unordered(second));
                 }
             }
-            if (lane == g) worth = best;
+#pragma unroll
+            for (int i = 0; i < 64 / LPT; ++i)
+                if (g == lane + LPT * i) worth[i] = best;
         }
-        uint64_t kept = 0;
-        for (int i = 0; i < a.topk_groups; ++i) {
-            const Key w[1] = {worth};
-            const Key best = wave_umax(worth);
-            if (best == 0) break;
-            const int g = first_with(w, best);
-            kept |= 1ull << g;
-            if (lane == g) worth = 0;
+        for (int n = 0; n < a.topk_groups; ++n) {
+            Key best = worth[0];
+#pragma unroll
+            for (int i = 1; i < 64 / LPT; ++i) best = worth[i] > best ? worth[i] : best;
+            best = token_max<LPT>(best);
+            const uint32_t g = first_with<LPT>(worth, best, lane);
+            if (best != 0) kept |= 1ull << (g & 63);
+#pragma unroll
+            for (int i = 0; i < 64 / LPT; ++i)
+                if (g == (uint32_t)(lane + LPT * i)) worth[i] = 0;
         }
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
             // e / group_size by its reciprocal: exact for e x group_size < 2^22
-            const uint32_t g = ((uint32_t)(lane + 64 * j) * a.group_recip) >> 22;
+            const uint32_t g = ((uint32_t)(lane + LPT * j) * a.group_recip) >> 22;
             if (!(kept >> (g & 63) & 1)) key[j] = 0;
         }
     }
@@ -199,19 +254,21 @@ __device__ __forceinline__ void route_token(const RouteLaunch &a, int t, int lan
         Key best = key[0];
 #pragma unroll
         for (int j = 1; j < EPL; ++j) best = key[j] > best ? key[j] : best;
-        best = wave_umax(best);
-        if (best == 0) break;
-        const int at = first_with(key, best);
-        float li = 0.0f;
+        best = token_max<LPT>(best);
+        if constexpr (LPT == 64)
+            if (best == 0) break;
+        const uint32_t at = first_with<LPT>(key, best, lane);
+        float li = -INFINITY;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-            if (at == lane + 64 * j) key[j] = 0;
-            if constexpr (WIDE) li = (at >> 6) == j ? l[j] : li;
+            const bool here = at == (uint32_t)(lane + LPT * j);
+            if constexpr (WIDE) li = here ? l[j] : li;
+            if (here) key[j] = 0;
         }
-        if constexpr (WIDE) li = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(li), at & 63));
+        if constexpr (WIDE) li = token_max<LPT>(li);
         else li = unordered(best);
-        if (lane == i) {
-            my_id = at;
+        if (lane == i && best != 0) {
+            my_id = (int)at;
             my_l = li;
         }
     }
@@ -221,7 +278,7 @@ __device__ __forceinline__ void route_token(const RouteLaunch &a, int t, int lan
     if (a.score == QLIN_SCORE_SOFTMAX) {
         // renormalized: the softmax over the chosen logits alone (the sum over
         // the others cancels), which does not underflow
-        const float m = a.renormalize ? wave_max(my_l) : top;
+        const float m = a.renormalize ? token_max<LPT>(my_l) : top;
         s = mine ? expf(my_l - m) : 0.0f;
         float sum = s;
         if (!a.renormalize) {
@@ -229,20 +286,20 @@ __device__ __forceinline__ void route_token(const RouteLaunch &a, int t, int lan
 #pragma unroll
             for (int j = 0; j < EPL; ++j) sum += l[j] > -INFINITY ? expf(l[j] - top) : 0.0f;
         }
-        sum = wave_sum(sum);
+        sum = token_sum<LPT>(sum);
         s = sum > 0.0f ? s / sum : 0.0f;
     } else {
         s = mine ? 1.0f / (1.0f + expf(-my_l)) : 0.0f;
         if (a.renormalize) {
-            const float sum = wave_sum(s);
+            const float sum = token_sum<LPT>(s);
             s = sum > 0.0f ? s / sum : 0.0f;
         }
     }
     my_w = mine ? s * a.scale : 0.0f;
 }
 
-// Exclusive sums over value[0 .. n) (n <= kRouteThreads, one per thread) into
-// off[0 .. n], by the whole workgroup.
+// Exclusive sums over value (one per thread, n <= kRouteThreads of them) into
+// off[0 .. n], by a workgroup of kRouteThreads.
 __device__ __forceinline__ void scan_to(uint32_t value, int n, uint32_t *off, uint32_t *wave_tot) {
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     uint32_t v = tid < n ? value : 0;
@@ -261,98 +318,122 @@ __device__ __forceinline__ void scan_to(uint32_t value, int n, uint32_t *off, ui
     __syncthreads();
 }
 
-// Routes block_tokens tokens, 16 at a time (one per wave).  Each expert has a
-// bit per token of the batch, so a pair's place among its expert's rows of
-// this block is a count of bits: token order, whatever order waves come in.
-//   one block:   scans the experts' counts and writes rows and slots
-//   more blocks: leaves each pair's place in slots and the experts' counts
-//                of this block in hist; place_kernel does the rest
-template <int EPL, bool WIDE>
-__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteLaunch a) {
-    __shared__ uint32_t cnt[QLIN_MAX_EXPERTS], bits[QLIN_MAX_EXPERTS], off[QLIN_MAX_EXPERTS + 1];
-    __shared__ uint32_t wave_tot[kRouteWaves];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    if (tid < a.experts) cnt[tid] = bits[tid] = 0;
+// Routes block_tokens tokens, 16 at a time.  Each expert has a bit per token
+// of the 16, so a pair's place among its expert's rows of this block is a
+// count of bits: token order, whatever order the waves come in.
+//   ONE (one workgroup for the call): scans the experts' counts and writes
+//   rows and slots; else leaves each pair's place in slots and the experts'
+//   counts of this block in hist, and place_kernel does the rest.
+template <int LPT, int EPL, bool WIDE, bool ONE>
+__global__ __launch_bounds__(kRouteTokens *LPT) void route_kernel(RouteLaunch a) {
+    constexpr int THREADS = kRouteTokens * LPT;
+    __shared__ uint32_t cnt[QLIN_MAX_EXPERTS], bits[QLIN_MAX_EXPERTS];
+    const int tid = threadIdx.x, lane = tid % LPT, w = tid / LPT;
+    for (int e = tid; e < a.experts; e += THREADS) cnt[e] = bits[e] = 0;
     __syncthreads();
     const int t0 = blockIdx.x * a.block_tokens;
     const int t1 = min(a.T, t0 + a.block_tokens);
-    for (int tb = t0; tb < t1; tb += kRouteWaves) {
+    for (int tb = t0; tb < t1; tb += kRouteTokens) {
         const int t = tb + w;
+        const bool live = t < t1;
         int id = -1;
         float wt = 0.0f;
-        if (t < t1) {
-            route_token<EPL, WIDE>(a, t, lane, id, wt);
-            if (lane < a.topk) {
-                a.ids[(int64_t)t * a.topk + lane] = id;
-                a.weights[(int64_t)t * a.topk + lane] = wt;
-                if (id >= 0) atomicOr(&bits[id], 1u << w);
-            }
+        if (LPT < 64 || live) route_token<LPT, EPL, WIDE>(a, t, live, lane, id, wt);
+        if (live && lane < a.topk) {
+            a.ids[(int64_t)t * a.topk + lane] = id;
+            a.weights[(int64_t)t * a.topk + lane] = wt;
+            if (id >= 0) atomicOr(&bits[id], 1u << w);
         }
         __syncthreads();
-        if (t < t1 && lane < a.topk)
+        if (live && lane < a.topk)
             a.slots[(int64_t)t * a.topk + lane] =
                 id >= 0 ? (int)(cnt[id] + __popc(bits[id] & ((1u << w) - 1))) : -1;
         __syncthreads();
-        if (tid < a.experts) {
-            cnt[tid] += __popc(bits[tid]);
-            bits[tid] = 0;
+        for (int e = tid; e < a.experts; e += THREADS) {
+            cnt[e] += __popc(bits[e]);
+            bits[e] = 0;
         }
         __syncthreads();
     }
-    if (gridDim.x > 1) {
-        if (tid < a.experts) a.hist[(int64_t)blockIdx.x * a.experts + tid] = (uint16_t)cnt[tid];
-        return;
+    if constexpr (!ONE) {
+        for (int e = tid; e < a.hist_stride; e += THREADS)
+            a.hist[(int64_t)blockIdx.x * a.hist_stride + e] = e < a.experts ? (uint16_t)cnt[e] : 0;
+    } else {
+        __shared__ uint32_t off[QLIN_MAX_EXPERTS + 1], wave_tot[kRouteTokens];
+        scan_to(tid < a.experts ? cnt[tid] : 0, a.experts, off, wave_tot);
+        for (int i = tid; i <= a.experts; i += THREADS) a.offsets[i] = (int)off[i];
+        for (int t = w; t < a.T; t += kRouteTokens) {
+            if (lane >= a.topk) continue;
+            const int64_t p = (int64_t)t * a.topk + lane;   // written by this thread above
+            const int id = a.ids[p];
+            if (id < 0) continue;
+            const int slot = (int)off[id] + a.slots[p];
+            a.slots[p] = slot;
+            a.rows[slot] = t;
+        }
+        for (int i = (int)off[a.experts] + tid; i < a.T * a.topk; i += THREADS) a.rows[i] = -1;
     }
-    scan_to(tid < a.experts ? cnt[tid] : 0, a.experts, off, wave_tot);
-    for (int i = tid; i <= a.experts; i += kRouteThreads) a.offsets[i] = (int)off[i];
-    for (int t = w; t < a.T; t += kRouteWaves) {
-        if (lane >= a.topk) continue;
-        const int64_t p = (int64_t)t * a.topk + lane;   // written by this thread above
-        const int id = a.ids[p];
-        if (id < 0) continue;
-        const int slot = (int)off[id] + a.slots[p];
-        a.slots[p] = slot;
-        a.rows[slot] = t;
-    }
-    for (int i = (int)off[a.experts] + tid; i < a.T * a.topk; i += kRouteThreads) a.rows[i] = -1;
 }
 
-// Rows and slots of one block's pairs: the expert's offset, its rows in
-// earlier blocks and the pair's place in its own block.  Every block sums the
-// blocks' counts for itself (two bytes for each expert and block, out of the
-// L2) instead of waiting for a third launch.
+// Rows and slots of the pairs of kPlaceBlocks routing blocks: the expert's
+// offset, its rows in earlier blocks and the pair's place in its own block.
+// Every workgroup sums the blocks' counts for itself (2 bytes for each expert
+// and block, out of the L2) instead of waiting for a third launch.
+constexpr int kPlaceBlocks = 16;
+
 __global__ __launch_bounds__(kRouteThreads) void place_kernel(RouteLaunch a) {
     __shared__ uint32_t pre[QLIN_MAX_EXPERTS], tot[QLIN_MAX_EXPERTS], off[QLIN_MAX_EXPERTS + 1];
-    __shared__ uint32_t wave_tot[kRouteWaves];
+    __shared__ uint16_t own[kPlaceBlocks][QLIN_MAX_EXPERTS];   // counts, then places, of this workgroup's blocks
+    __shared__ uint32_t wave_tot[kRouteTokens];
     const int tid = threadIdx.x;
     if (tid < a.experts) pre[tid] = tot[tid] = 0;
     __syncthreads();
-    int width = 64;
-    while (width < a.experts) width *= 2;
-    const int e = tid & (width - 1), segs = kRouteThreads / width;
-    if (e < a.experts) {
-        uint32_t p = 0, s = 0;
-        for (int b = tid / width; b < (int)gridDim.x; b += segs) {
-            const uint32_t c = a.hist[(int64_t)b * a.experts + e];
-            s += c;
-            p += b < (int)blockIdx.x ? c : 0;
+    const int b0 = blockIdx.x * kPlaceBlocks, b1 = min(a.blocks, b0 + kPlaceBlocks);
+    const int cols = a.hist_stride / 8, segs = kRouteThreads / cols;
+    const int col = tid % cols, seg = tid / cols;
+    if (seg < segs) {
+        uint32_t p[8] = {}, s[8] = {};
+        for (int b = seg; b < a.blocks; b += segs) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(a.hist + (int64_t)b * a.hist_stride + col * 8);
+            const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t c = i & 1 ? q[i / 2] >> 16 : q[i / 2] & 0xFFFFu;
+                s[i] += c;
+                p[i] += b < b0 ? c : 0;
+            }
+            if (b >= b0 && b < b1) *reinterpret_cast<uint4 *>(&own[b - b0][col * 8]) = v;
         }
-        atomicAdd(&pre[e], p);
-        atomicAdd(&tot[e], s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (col * 8 + i >= a.experts) break;
+            atomicAdd(&pre[col * 8 + i], p[i]);
+            atomicAdd(&tot[col * 8 + i], s[i]);
+        }
     }
     __syncthreads();
     scan_to(tid < a.experts ? tot[tid] : 0, a.experts, off, wave_tot);
     if (blockIdx.x == 0)
         for (int i = tid; i <= a.experts; i += kRouteThreads) a.offsets[i] = (int)off[i];
-    const int t0 = blockIdx.x * a.block_tokens;
-    const int pairs = (min(a.T, t0 + a.block_tokens) - t0) * a.topk;
+    if (tid < a.experts) {
+        uint32_t at = 0;
+        for (int b = 0; b < b1 - b0; ++b) {
+            const uint32_t c = own[b][tid];
+            own[b][tid] = (uint16_t)at;
+            at += c;
+        }
+    }
+    __syncthreads();
+    const int t0 = b0 * a.block_tokens;
+    const int pairs = (min(a.T, b1 * a.block_tokens) - t0) * a.topk;
     for (int i = tid; i < pairs; i += kRouteThreads) {
         const int64_t p = (int64_t)t0 * a.topk + i;
         const int id = a.ids[p];
         if (id < 0) continue;
-        const int slot = (int)(off[id] + pre[id]) + a.slots[p];
+        const int t = i / a.topk;
+        const int slot = (int)(off[id] + pre[id] + own[t / a.block_tokens][id]) + a.slots[p];
         a.slots[p] = slot;
-        a.rows[slot] = t0 + i / a.topk;
+        a.rows[slot] = t0 + t;
     }
     for (int i = (int)off[a.experts] + (int)blockIdx.x * kRouteThreads + tid; i < a.T * a.topk;
          i += (int)gridDim.x * kRouteThreads)
@@ -512,21 +593,36 @@ int route_block_tokens(int T) {
 }
 int route_blocks(int T) { return T <= 64 ? 1 : (T + route_block_tokens(T) - 1) / route_block_tokens(T); }
 
-hipError_t launch_route(const RouteLaunch &a, hipStream_t s) {
-    const dim3 grid(route_blocks(a.T)), block(kRouteThreads);
+template <int LPT, int EPL>
+static void launch_route_kernel(const RouteLaunch &a, hipStream_t s) {
+    const dim3 grid(a.blocks), block(kRouteTokens * LPT);
     const bool wide = a.bias != nullptr || a.group_top2;
-#define QLIN_ROUTE(EPL_)                                                                              \
-    if (wide) hipLaunchKernelGGL((route_kernel<EPL_, true>), grid, block, 0, s, a);                   \
-    else hipLaunchKernelGGL((route_kernel<EPL_, false>), grid, block, 0, s, a)
-    if (a.experts <= 64) { QLIN_ROUTE(1); }
-    else if (a.experts <= 128) { QLIN_ROUTE(2); }
-    else if (a.experts <= 256) { QLIN_ROUTE(4); }
-    else if (a.experts <= 512) { QLIN_ROUTE(8); }
-    else { QLIN_ROUTE(16); }
-#undef QLIN_ROUTE
+    if (a.blocks > 1) {
+        if (wide) hipLaunchKernelGGL((route_kernel<LPT, EPL, true, false>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((route_kernel<LPT, EPL, false, false>), grid, block, 0, s, a);
+    } else if constexpr (LPT == 64) {
+        if (wide) hipLaunchKernelGGL((route_kernel<LPT, EPL, true, true>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((route_kernel<LPT, EPL, false, true>), grid, block, 0, s, a);
+    }
+}
+
+hipError_t launch_route(const RouteLaunch &a, hipStream_t s) {
+    // 16 lanes per token where tokens are many: four tokens share each
+    // instruction of the reductions
+    if (a.T >= kRouteRowTokens && a.experts <= 256 && a.topk <= 16) {
+        if (a.experts <= 64) launch_route_kernel<16, 4>(a, s);
+        else if (a.experts <= 128) launch_route_kernel<16, 8>(a, s);
+        else launch_route_kernel<16, 16>(a, s);
+    } else {
+        if (a.experts <= 64) launch_route_kernel<64, 1>(a, s);
+        else if (a.experts <= 128) launch_route_kernel<64, 2>(a, s);
+        else if (a.experts <= 256) launch_route_kernel<64, 4>(a, s);
+        else if (a.experts <= 512) launch_route_kernel<64, 8>(a, s);
+        else launch_route_kernel<64, 16>(a, s);
+    }
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || grid.x == 1) return e;
-    hipLaunchKernelGGL(place_kernel, grid, block, 0, s, a);
+    if (e != hipSuccess || a.blocks == 1) return e;
+    hipLaunchKernelGGL(place_kernel, dim3((a.blocks + kPlaceBlocks - 1) / kPlaceBlocks), dim3(kRouteThreads), 0, s, a);
     return hipGetLastError();
 }
 
