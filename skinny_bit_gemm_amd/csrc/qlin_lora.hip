@@ -39,11 +39,16 @@ __device__ __forceinline__ int rank_of(const LoraLaunch &a, int adapter) {
     return a.ranks ? min(max(a.ranks[adapter], 0), a.max_rank) : a.max_rank;
 }
 
+constexpr int kShrinkWaves = 8, kShrinkWavesWide = 4;   // of a shrink workgroup, 16- and 64-row tiles
+
 // One tile: `count` rows of one adapter (adapters: rows without one).
 struct Tile {
     int adapter, count;
     int v0;   // row of v where the tile's first row is (-1: v has the call's row order)
 };
+
+// Rows up to which a workgroup finds its tile by ballots over the ids.
+constexpr int kDirectRows = 64;
 
 // Finds tile `ti` and its rows (member[0 .. 16 CT)); count 0: there is no
 // such tile.  Ends with a barrier when the tile exists.
@@ -59,29 +64,42 @@ __device__ __forceinline__ Tile find_tile(const LoraLaunch &a, int ti, int *memb
         t.count = d.z;
         if (tid < t.count) member[tid] = a.perm[d.y + tid];
     } else {
-        // the tile's first row is row ti, and every 16th of its adapter's
-        // rows is one
-        const int mine = lane < a.M ? adapter_of(a, a.ids[lane]) : -1;
-        const int lead = __builtin_amdgcn_readlane(mine, ti);
-        const uint64_t same = __ballot(mine == lead);
-        const int before = __popcll(same & ((1ull << ti) - 1));
+        // a tile starts at every 16th row of its adapter's rows, and is known
+        // by that row's number
+        const int lead = adapter_of(a, a.ids[ti]);
+        uint64_t same[kDirectRows / 64];
+        int before = 0, all = 0;
+#pragma unroll
+        for (int q = 0; q < kDirectRows / 64; ++q) {
+            const int m = q * 64 + lane;
+            same[q] = __ballot(m < a.M && adapter_of(a, a.ids[m < a.M ? m : 0]) == lead);
+            all += __popcll(same[q]);
+            before += __popcll(ti >= q * 64 + 64 ? same[q] : ti > q * 64 ? same[q] & ((1ull << (ti - q * 64)) - 1) : 0);
+        }
         if (before & 15) return t;
-        const int at = __popcll(same & ((1ull << lane) - 1)) - before;
         t.adapter = lead;
-        t.count = min(16, __popcll(same) - before);
-        if (tid < 64 && mine == lead && at >= 0 && at < 16) member[at] = lane;
+        t.count = min(16, all - before);
+        if (tid < 64) {
+            int at = -before;
+#pragma unroll
+            for (int q = 0; q < kDirectRows / 64; ++q) {
+                const int place = at + __popcll(same[q] & ((1ull << lane) - 1));
+                if ((same[q] >> lane & 1) && place >= 0 && place < 16) member[place] = q * 64 + lane;
+                at += __popcll(same[q]);
+            }
+        }
     }
     __syncthreads();
     return t;
 }
 
 // v (a part of K) for one tile and 16 RT ranks: D[rank][row] from A rows and
-// x rows, both read along K.  The four waves split the part's K steps and add
-// up through the LDS.
-template <int CT, int RT, bool SORTED>
-__global__ __launch_bounds__(256) void shrink_kernel(LoraLaunch a) {
+// x rows, both read along K.  The NW waves split the part's K steps and add
+// up through the LDS, 16 rows at a time.
+template <int CT, int RT, int NW, bool SORTED>
+__global__ __launch_bounds__(64 * NW) void shrink_kernel(LoraLaunch a) {
     __shared__ int member[16 * CT];
-    __shared__ v4f part[3][CT * RT][64];
+    __shared__ v4f part[NW][RT][64];
     const int split = blockIdx.x, rank0 = blockIdx.z * 16 * RT;
     const Tile t = find_tile<CT, SORTED>(a, blockIdx.y, member);
     if (t.count == 0 || rank0 >= rank_of(a, t.adapter)) return;
@@ -99,7 +117,7 @@ __global__ __launch_bounds__(256) void shrink_kernel(LoraLaunch a) {
         ap[r] = a.A + ((int64_t)t.adapter * a.max_rank + rank) * a.K + kg * 8;
     }
     v4f acc[CT][RT] = {};
-    const int s0 = (split * 4 + w) * a.k_steps;
+    const int s0 = (split * NW + w) * a.k_steps;
     const int s1 = min(s0 + a.k_steps, (a.K + 31) / 32);
 #pragma unroll 4
     for (int s = s0; s < s1; ++s) {
@@ -117,150 +135,195 @@ __global__ __launch_bounds__(256) void shrink_kernel(LoraLaunch a) {
 #pragma unroll
             for (int r = 0; r < RT; ++r) acc[c][r] = mfma_bf16(av[r], xv[c], acc[c][r]);
     }
-    if (w > 0) {
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-#pragma unroll
-            for (int r = 0; r < RT; ++r) part[w - 1][c * RT + r][lane] = acc[c][r];
-    }
-    __syncthreads();
-    if (w > 0) return;
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
+        if (c * 16 >= t.count) break;
+        if (c > 0) __syncthreads();
+#pragma unroll
+        for (int r = 0; r < RT; ++r) part[w][r][lane] = acc[c][r];
+        __syncthreads();
         const int i = c * 16 + c16;
-        if (i >= t.count) continue;
-        const int64_t row = t.v0 >= 0 ? t.v0 + i : member[i];
-        float *v = a.v + ((int64_t)split * a.M + row) * a.v_stride + rank0 + kg * 4;
+        for (int r = w; r < RT; r += NW) {
+            v4f s = part[0][r][lane];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            v4f s = acc[c][r];
-            for (int q = 0; q < 3; ++q) s += part[q][c * RT + r][lane];
-            if (rank0 + r * 16 < a.v_stride) *reinterpret_cast<v4f *>(v + r * 16) = s;
+            for (int q = 1; q < NW; ++q) s += part[q][r][lane];
+            if (i >= t.count || rank0 + r * 16 >= a.v_stride) continue;
+            const int64_t row = t.v0 >= 0 ? t.v0 + i : member[i];
+            *reinterpret_cast<v4f *>(a.v + ((int64_t)split * a.M + row) * a.v_stride + rank0 + r * 16 + kg * 4) = s;
         }
     }
 }
 
-// The sum of v's slices for one row and the ranks kg * 8 + 0 .. 7 of a step
-// of 32, times the adapter's scale, as TERMS bf16 numbers that add up to it:
-// each takes 8 more bits of the mantissa, so that the second product loses
-// nothing that its fp32 sums would keep (TERMS 3) or less than the bf16
-// rounding of y would show (TERMS 2).  Ranks past the adapter's are zero.
-template <int TERMS>
-__device__ __forceinline__ void load_v(const LoraLaunch &a, int64_t row, int rank, int ranks, float scale,
-                                       uint4 (&out)[TERMS]) {
-    float f[8] = {};
-    const float *p = a.v + row * a.v_stride + rank;
-    if (rank < ranks) {
-        for (int s = 0; s < a.splits; ++s) {
-            const float4 u = *reinterpret_cast<const float4 *>(p), v = *reinterpret_cast<const float4 *>(p + 4);
-            f[0] += u.x; f[1] += u.y; f[2] += u.z; f[3] += u.w;
-            f[4] += v.x; f[5] += v.y; f[6] += v.z; f[7] += v.w;
-            p += (int64_t)a.M * a.v_stride;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = rank + i < ranks ? f[i] * scale : 0.0f;
-#pragma unroll
-    for (int q = 0; q < TERMS; ++q) {
-        uint32_t o[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            o[i] = bf16_pair(f[2 * i], f[2 * i + 1]);
-            f[2 * i] -= bf16_lo(o[i]);
-            f[2 * i + 1] -= bf16_hi(o[i]);
-        }
-        out[q] = make_uint4(o[0], o[1], o[2], o[3]);
-    }
-}
-
-// y of one tile for column runs of 64 per wave.  D[column][row] from B rows
-// and v.  The rows of a wave's four column tiles are dealt so that each lane
-// ends with 16 consecutive columns of its row.
+// y of one tile for n_chunk columns; each of the four waves has a quarter of
+// them, 32 at a time.  D[column][row] from B rows and v.
+//
+// First the tile's v: the slices are added up, the adapter's scale is applied
+// and the sum is written to the LDS as TERMS bf16 numbers that add up to it.
+// Each takes 8 more bits of the mantissa, so that the second product loses
+// nothing that its fp32 sums would keep (TERMS 3, fp32 y) or less than the
+// bf16 rounding of y shows (TERMS 2).  Ranks past the adapter's are zero.
+//
+// RK: 32-rank steps (0: more than two, B read as it is needed).  The next
+// columns' B rows and base are on their way while these are multiplied.  The
+// columns of a wave's two tiles are dealt so that each lane ends with 16
+// consecutive bytes of its row.
 template <int CT, int RK, bool F32, bool SORTED>
 __global__ __launch_bounds__(256) void expand_kernel(LoraLaunch a) {
-    constexpr int TERMS = F32 ? 3 : 2;
-    __shared__ int member[16 * CT];
+    constexpr int TERMS = F32 ? 3 : 2, ROWS = 16 * CT;
+    extern __shared__ __align__(16) uint16_t vs[];   // [TERMS][ROWS][stride]
+    __shared__ int member[ROWS];
     const Tile t = find_tile<CT, SORTED>(a, blockIdx.y, member);
     if (t.count == 0) return;
     const int ranks = rank_of(a, t.adapter);
     if (ranks == 0 && a.base == a.y) return;   // these rows are already there
-    const float scale = a.scales && t.adapter < a.adapters ? a.scales[t.adapter] : 1.0f;
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int c16 = lane & 15, kg = lane >> 4;
-    const int chunks = (ranks + 32 * RK - 1) / (32 * RK);
-    int row[CT];
-    uint4 vf[CT][RK][TERMS];
-    auto load_chunk = [&](int ch) {
+    const int steps = RK > 0 ? RK : (ranks + 31) / 32, stride = steps * 32 + 8;
+    const float scale = a.scales && t.adapter < a.adapters ? a.scales[t.adapter] : 1.0f;
+
+    for (int i = tid; i < ROWS * steps * 8; i += 256) {   // four ranks of a row
+        const int row = i / (steps * 8), rank = (i - row * steps * 8) * 4;
+        v4f f = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (row < t.count && rank < ranks) {
+            const float *p = a.v + (int64_t)(t.v0 >= 0 ? t.v0 + row : member[row]) * a.v_stride + rank;
+            for (int s = 0; s < a.splits; ++s) f += *reinterpret_cast<const v4f *>(p + (int64_t)s * a.M * a.v_stride);
+        }
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-            const int i = c * 16 + c16 < t.count ? c * 16 + c16 : 0;
-            const int64_t at = t.v0 >= 0 ? t.v0 + i : member[i];
+        for (int j = 0; j < 4; ++j) f[j] = rank + j < ranks ? f[j] * scale : 0.0f;
 #pragma unroll
-            for (int q = 0; q < RK; ++q)
-                load_v<TERMS>(a, at, (ch * RK + q) * 32 + kg * 8, ranks, scale, vf[c][q]);
+        for (int e = 0; e < TERMS; ++e) {
+            const uint32_t lo = bf16_pair(f[0], f[1]), hi = bf16_pair(f[2], f[3]);
+            *reinterpret_cast<uint2 *>(vs + ((int64_t)e * ROWS + row) * stride + rank) = make_uint2(lo, hi);
+            f[0] -= bf16_lo(lo);
+            f[1] -= bf16_hi(lo);
+            f[2] -= bf16_lo(hi);
+            f[3] -= bf16_hi(hi);
+        }
+    }
+    __syncthreads();
+
+    int64_t yrow[CT], brow[CT];
+    bool in_tile[CT];
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+        in_tile[c] = c * 16 + c16 < t.count;
+        const int64_t m = member[in_tile[c] ? c * 16 + c16 : 0];
+        yrow[c] = m * a.ldy;
+        brow[c] = m * a.ldb;
+    }
+    const int quarter = a.n_chunk / 4;
+    const int n_begin = blockIdx.x * a.n_chunk + w * quarter, n_end = min(a.N, n_begin + quarter);
+    // D's row 4 kg + i of tile j is column col(j) + i, and the lane that loads
+    // that row of B is c16 = 4 kg + i
+    auto col = [&](int j, int g) { return F32 ? j * 16 + g * 4 : g * 8 + j * 4; };
+    const uint16_t *bp[2];   // this lane's B row of tile j, at the wave's first column
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        bp[j] = a.B + ((int64_t)t.adapter * a.N + col(j, c16 >> 2) + (c16 & 3)) * a.max_rank + kg * 8;
+    auto load_b = [&](int n, int q, uint4 (&b)[2]) {
+        const int rank = q * 32 + kg * 8;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            b[j] = make_uint4(0, 0, 0, 0);
+            if (rank < ranks && n + col(j, c16 >> 2) + (c16 & 3) < a.N)
+                b[j] = *reinterpret_cast<const uint4 *>(bp[j] + (int64_t)n * a.max_rank + q * 32);
         }
     };
+    // ranks past the adapter's: whatever B holds there is cleared
+    auto clear_past = [&](int q, uint4 (&b)[2]) {
+        if ((q + 1) * 32 <= ranks) return;
+        const int rank = q * 32 + kg * 8;
+        uint32_t keep[4];
 #pragma unroll
-    for (int c = 0; c < CT; ++c) row[c] = c * 16 + c16 < t.count ? member[c * 16 + c16] : -1;
-    if (chunks == 1) load_chunk(0);
-    const int n_end = min(a.N, (int)(blockIdx.x + 1) * a.n_chunk);
-    for (int n0 = blockIdx.x * a.n_chunk + w * 64; n0 < n_end; n0 += 256) {
-        v4f acc[CT][4] = {};
-        for (int ch = 0; ch < chunks; ++ch) {
-            if (chunks > 1) load_chunk(ch);
-            uint4 bv[4][RK];
+        for (int i = 0; i < 4; ++i)
+            keep[i] = (rank + 2 * i < ranks ? 0xFFFFu : 0u) | (rank + 2 * i + 1 < ranks ? 0xFFFF0000u : 0u);
 #pragma unroll
-            for (int q = 0; q < RK; ++q) {
-                const int rank = (ch * RK + q) * 32 + kg * 8;
-                // ranks past the adapter's: whatever B holds there is cleared
-                uint32_t keep[4];
+        for (int j = 0; j < 2; ++j)
+            b[j] = make_uint4(b[j].x & keep[0], b[j].y & keep[1], b[j].z & keep[2], b[j].w & keep[3]);
+    };
+    constexpr int PARTS = F32 ? 2 : 1;   // 16-byte pieces of a lane's columns
+    auto load_base = [&](int n, uint4 (&o)[CT][PARTS]) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    keep[i] = (rank + 2 * i < ranks ? 0xFFFFu : 0u) | (rank + 2 * i + 1 < ranks ? 0xFFFF0000u : 0u);
+        for (int c = 0; c < CT; ++c)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int n = min(n0 + (c16 >> 2) * 16 + j * 4 + (c16 & 3), a.N - 1);
-                    uint4 b = make_uint4(0, 0, 0, 0);
-                    if (rank < ranks)
-                        b = *reinterpret_cast<const uint4 *>(a.B + ((int64_t)t.adapter * a.N + n) * a.max_rank + rank);
-                    bv[j][q] = make_uint4(b.x & keep[0], b.y & keep[1], b.z & keep[2], b.w & keep[3]);
+            for (int h = 0; h < PARTS; ++h) {
+                const int at = n + col(h, kg);
+                o[c][h] = make_uint4(0, 0, 0, 0);
+                if (a.base && in_tile[c] && at < n_end) {
+                    if constexpr (F32)
+                        o[c][h] = *reinterpret_cast<const uint4 *>(static_cast<const float *>(a.base) + brow[c] + at);
+                    else
+                        o[c][h] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.base) + brow[c] + at);
                 }
             }
+    };
+    constexpr int HELD = RK > 0 ? RK : 1;
+    uint4 b_next[HELD][2], base_next[CT][PARTS];
+    if constexpr (RK > 0)
+#pragma unroll
+        for (int q = 0; q < RK; ++q) load_b(n_begin, q, b_next[q]);
+    load_base(n_begin, base_next);
+    for (int n = n_begin; n < n_end; n += 32) {
+        v4f acc[CT][2] = {};
+        uint4 b_now[HELD][2], base_now[CT][PARTS];
+        if constexpr (RK > 0) {
 #pragma unroll
             for (int q = 0; q < RK; ++q)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int c = 0; c < CT; ++c)
-#pragma unroll
-                        for (int e = TERMS - 1; e >= 0; --e) acc[c][j] = mfma_bf16(bv[j][q], vf[c][q][e], acc[c][j]);
+                for (int j = 0; j < 2; ++j) b_now[q][j] = b_next[q][j];
         }
-        const int n = n0 + kg * 16;
-        if (n >= n_end) continue;   // N and n_chunk are multiples of 16
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-            if (row[c] < 0) continue;
-            const int64_t at = (int64_t)row[c] * a.ldy + n, bt = (int64_t)row[c] * a.ldb + n;
-            if constexpr (F32) {
+        for (int c = 0; c < CT; ++c)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v4f o = acc[c][j];
-                    if (a.base) o += *reinterpret_cast<const v4f *>(static_cast<const float *>(a.base) + bt + 4 * j);
-                    *reinterpret_cast<v4f *>(static_cast<float *>(a.y) + at + 4 * j) = o;
-                }
+            for (int h = 0; h < PARTS; ++h) base_now[c][h] = base_next[c][h];
+        if (n + 32 < n_end) {
+            if constexpr (RK > 0)
+#pragma unroll
+                for (int q = 0; q < RK; ++q) load_b(n + 32, q, b_next[q]);
+            load_base(n + 32, base_next);
+        }
+        for (int q = 0; q < steps; ++q) {
+            uint4 b[2];
+            if constexpr (RK == 0) {
+                load_b(n, q, b);
             } else {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint4 b = make_uint4(0, 0, 0, 0);
-                    if (a.base)
-                        b = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.base) + bt + 8 * h);
-                    const v4f p = acc[c][2 * h], q = acc[c][2 * h + 1];
-                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.y) + at + 8 * h) =
-                        make_uint4(bf16_pair(bf16_lo(b.x) + p[0], bf16_hi(b.x) + p[1]),
-                                   bf16_pair(bf16_lo(b.y) + p[2], bf16_hi(b.y) + p[3]),
-                                   bf16_pair(bf16_lo(b.z) + q[0], bf16_hi(b.z) + q[1]),
-                                   bf16_pair(bf16_lo(b.w) + q[2], bf16_hi(b.w) + q[3]));
+                for (int j = 0; j < 2; ++j) b[j] = b_now[RK == 1 ? 0 : q][j];
+            }
+            clear_past(q, b);
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+#pragma unroll
+                for (int e = TERMS - 1; e >= 0; --e) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(
+                        vs + ((int64_t)e * ROWS + c * 16 + c16) * stride + q * 32 + kg * 8);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) acc[c][j] = mfma_bf16(b[j], v, acc[c][j]);
                 }
+            if constexpr (RK > 0)
+                if (q + 1 == RK) break;
+        }
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+            if (!in_tile[c]) continue;
+            if constexpr (F32) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int at = n + col(h, kg);
+                    if (at < n_end)
+                        *reinterpret_cast<v4f *>(static_cast<float *>(a.y) + yrow[c] + at) =
+                            acc[c][h] + __builtin_bit_cast(v4f, base_now[c][h]);
+                }
+            } else {
+                const int at = n + col(0, kg);
+                const uint4 o = base_now[c][0];
+                const v4f p = acc[c][0], q = acc[c][1];
+                if (at < n_end)
+                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.y) + yrow[c] + at) =
+                        make_uint4(bf16_pair(bf16_lo(o.x) + p[0], bf16_hi(o.x) + p[1]),
+                                   bf16_pair(bf16_lo(o.y) + p[2], bf16_hi(o.y) + p[3]),
+                                   bf16_pair(bf16_lo(o.z) + q[0], bf16_hi(o.z) + q[1]),
+                                   bf16_pair(bf16_lo(o.w) + q[2], bf16_hi(o.w) + q[3]));
             }
         }
     }
@@ -347,29 +410,28 @@ __global__ __launch_bounds__(1024) void group_kernel(LoraLaunch a, int tile_rows
 
 // ---------------------------------------------------------------- planning
 
-// Rows up to which a workgroup finds its tile by a ballot over the ids.
-constexpr int kLoraDirectRows = 64;
-
 void lora_plan(int M, int N, int K, int adapters, int max_rank, LoraPlan *p) {
-    p->sorted = M > kLoraDirectRows;
+    p->sorted = M > kDirectRows;
     p->ct = M >= 1024 ? 4 : 1;
     const int tile_rows = 16 * p->ct;
     p->max_tiles = p->sorted ? (M + tile_rows - 1) / tile_rows + (adapters + 1 < M ? adapters + 1 : M) : M;
     p->rt = max_rank <= 16 ? 1 : max_rank <= 32 ? 2 : 4;
     p->rank_chunks = (max_rank + 16 * p->rt - 1) / (16 * p->rt);
     p->v_stride = (max_rank + 15) / 16 * 16;
-    // K parts: enough workgroups to fill the GPU twice, with two steps of 32
-    // or more for each of a workgroup's four waves
-    const int steps = (K + 31) / 32;
-    const int tiles = (M + tile_rows - 1) / tile_rows;
-    int splits = 512 / ((p->sorted ? tiles : M) * p->rank_chunks);
-    splits = splits > 16 ? 16 : splits < 1 ? 1 : splits;
-    if (splits > steps / 8) splits = steps / 8 > 0 ? steps / 8 : 1;
-    p->k_steps = (steps + 4 * splits - 1) / (4 * splits);
-    p->splits = (steps + 4 * p->k_steps - 1) / (4 * p->k_steps);
-    // columns per expand workgroup
+    // K parts: one or two workgroups for each compute unit, at most four parts
+    // (the expand kernel reads them all for each of its column runs), two
+    // steps of 32 or more for each wave
+    const int steps = (K + 31) / 32, waves = p->ct == 1 ? kShrinkWaves : kShrinkWavesWide;
+    const int tiles = p->sorted ? (M + tile_rows - 1) / tile_rows : M;
+    int splits = 2 * kComputeUnits / (tiles * p->rank_chunks);
+    splits = splits > 4 ? 4 : splits < 1 ? 1 : splits;
+    if (splits > steps / (2 * waves)) splits = steps / (2 * waves) > 0 ? steps / (2 * waves) : 1;
+    p->k_steps = (steps + waves * splits - 1) / (waves * splits);
+    p->splits = (steps + waves * p->k_steps - 1) / (waves * p->k_steps);
+    // columns per expand workgroup: runs as long as leave four workgroups for
+    // each compute unit
     int n_chunk = 256;
-    while ((int64_t)((N + n_chunk - 1) / n_chunk) * tiles > 2048 && n_chunk < 4096) n_chunk *= 2;
+    while (n_chunk < 4096 && (int64_t)((N + 2 * n_chunk - 1) / (2 * n_chunk)) * tiles >= 4 * kComputeUnits) n_chunk *= 2;
     p->n_chunk = n_chunk;
     auto align = [](size_t v) { return (v + 255) & ~size_t(255); };
     size_t at = 0;
@@ -389,50 +451,43 @@ void lora_plan(int M, int N, int K, int adapters, int max_rank, LoraPlan *p) {
 }
 
 template <int CT, int RT>
-static void launch_shrink(const LoraPlan &p, const LoraLaunch &a, const dim3 &grid, hipStream_t s) {
-    if (p.sorted) hipLaunchKernelGGL((shrink_kernel<CT, RT, true>), grid, dim3(256), 0, s, a);
-    else if constexpr (CT == 1) hipLaunchKernelGGL((shrink_kernel<CT, RT, false>), grid, dim3(256), 0, s, a);
+static void launch_shrink(const LoraPlan &p, const LoraLaunch &a, hipStream_t s) {
+    constexpr int NW = CT == 1 ? kShrinkWaves : kShrinkWavesWide;
+    const dim3 grid(p.splits, p.max_tiles, p.rank_chunks), block(64 * NW);
+    if (p.sorted) hipLaunchKernelGGL((shrink_kernel<CT, RT, NW, true>), grid, block, 0, s, a);
+    else if constexpr (CT == 1) hipLaunchKernelGGL((shrink_kernel<CT, RT, NW, false>), grid, block, 0, s, a);
 }
 
-template <int CT, int RK>
-static void launch_expand(const LoraPlan &p, bool f32, const LoraLaunch &a, const dim3 &grid, hipStream_t s) {
-    if (p.sorted) {
-        if (f32) hipLaunchKernelGGL((expand_kernel<CT, RK, true, true>), grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((expand_kernel<CT, RK, false, true>), grid, dim3(256), 0, s, a);
-    } else if constexpr (CT == 1) {
-        if (f32) hipLaunchKernelGGL((expand_kernel<CT, RK, true, false>), grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((expand_kernel<CT, RK, false, false>), grid, dim3(256), 0, s, a);
-    }
+template <int CT, int RK, bool F32>
+static void launch_expand(const LoraPlan &p, const LoraLaunch &a, hipStream_t s) {
+    const dim3 grid((a.N + p.n_chunk - 1) / p.n_chunk, p.max_tiles), block(256);
+    const int steps = RK > 0 ? RK : (a.max_rank + 31) / 32;
+    const size_t lds = (size_t)(F32 ? 3 : 2) * 16 * CT * (steps * 32 + 8) * 2;
+    if (p.sorted) hipLaunchKernelGGL((expand_kernel<CT, RK, F32, true>), grid, block, lds, s, a);
+    else if constexpr (CT == 1) hipLaunchKernelGGL((expand_kernel<CT, RK, F32, false>), grid, block, lds, s, a);
+}
+
+template <int CT>
+static hipError_t launch_products(const LoraPlan &p, bool f32, const LoraLaunch &a, hipStream_t s) {
+    if (p.rt == 1) launch_shrink<CT, 1>(p, a, s);
+    else if (p.rt == 2) launch_shrink<CT, 2>(p, a, s);
+    else launch_shrink<CT, 4>(p, a, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int steps = (a.max_rank + 31) / 32;
+    if (steps == 1) f32 ? launch_expand<CT, 1, true>(p, a, s) : launch_expand<CT, 1, false>(p, a, s);
+    else if (steps == 2) f32 ? launch_expand<CT, 2, true>(p, a, s) : launch_expand<CT, 2, false>(p, a, s);
+    else f32 ? launch_expand<CT, 0, true>(p, a, s) : launch_expand<CT, 0, false>(p, a, s);
+    return hipGetLastError();
 }
 
 hipError_t launch_lora(const LoraPlan &p, bool f32, const LoraLaunch &a, hipStream_t s) {
-    hipError_t e;
     if (p.sorted) {
         hipLaunchKernelGGL(group_kernel, dim3(1), dim3(1024), 0, s, a, 16 * p.ct);
-        e = hipGetLastError();
+        const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    const dim3 sg(p.splits, p.max_tiles, p.rank_chunks);
-    if (p.ct == 1) {
-        if (p.rt == 1) launch_shrink<1, 1>(p, a, sg, s);
-        else if (p.rt == 2) launch_shrink<1, 2>(p, a, sg, s);
-        else launch_shrink<1, 4>(p, a, sg, s);
-    } else {
-        if (p.rt == 1) launch_shrink<4, 1>(p, a, sg, s);
-        else if (p.rt == 2) launch_shrink<4, 2>(p, a, sg, s);
-        else launch_shrink<4, 4>(p, a, sg, s);
-    }
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const dim3 eg((a.N + p.n_chunk - 1) / p.n_chunk, p.max_tiles);
-    if (p.ct == 1) {
-        if (p.rt <= 2) launch_expand<1, 1>(p, f32, a, eg, s);
-        else launch_expand<1, 2>(p, f32, a, eg, s);
-    } else {
-        if (p.rt <= 2) launch_expand<4, 1>(p, f32, a, eg, s);
-        else launch_expand<4, 2>(p, f32, a, eg, s);
-    }
-    return hipGetLastError();
+    return p.ct == 1 ? launch_products<1>(p, f32, a, s) : launch_products<4>(p, f32, a, s);
 }
 
 }  // namespace qlin

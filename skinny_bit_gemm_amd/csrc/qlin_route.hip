@@ -393,6 +393,7 @@ __global__ __launch_bounds__(kRouteThreads) void place_kernel(RouteLaunch a) {
     const int col = tid % cols, seg = tid / cols;
     if (seg < segs) {
         uint32_t p[8] = {}, s[8] = {};
+    #pragma unroll 8
         for (int b = seg; b < a.blocks; b += segs) {
             const uint4 v = *reinterpret_cast<const uint4 *>(a.hist + (int64_t)b * a.hist_stride + col * 8);
             const uint32_t q[4] = {v.x, v.y, v.z, v.w};
