@@ -714,7 +714,7 @@ qlin_status qlin_lora_workspace_bytes(int M, int N, int K, int adapters, int max
     const qlin_status st = check_lora_shape(M, N, K, adapters, max_rank);
     if (st != QLIN_OK) return st;
     LoraPlan p = {};
-    if (M > 0) lora_plan(M, N, K, adapters, max_rank, &p);
+    if (M > 0) lora_plan(M, N, K, adapters, max_rank, false, &p);   // the type does not change the size
     *bytes = p.ws_bytes;
     return QLIN_OK;
 }
@@ -735,7 +735,7 @@ qlin_status qlin_lora(int M, int N, int K, int adapters, int max_rank, const voi
         return QLIN_ERR_ALIGNMENT;
     if (M == 0) return QLIN_OK;
     LoraPlan p = {};
-    lora_plan(M, N, K, adapters, max_rank, &p);
+    lora_plan(M, N, K, adapters, max_rank, out_type == QLIN_OUT_F32_ACC, &p);
     if (!workspace || ws_bytes < p.ws_bytes) return QLIN_ERR_WORKSPACE;
     if (!aligned16(workspace)) return QLIN_ERR_ALIGNMENT;
     char *ws = static_cast<char *>(workspace);
@@ -760,6 +760,7 @@ qlin_status qlin_lora(int M, int N, int K, int adapters, int max_rank, const voi
     a.k_steps = p.k_steps;
     a.v_stride = p.v_stride;
     a.n_chunk = p.n_chunk;
+    a.sub_tiles = p.sub_tiles;
     a.v = reinterpret_cast<float *>(ws + p.v_at);
     if (p.sorted) {
         a.tiles = reinterpret_cast<int4 *>(ws + p.tiles_at);

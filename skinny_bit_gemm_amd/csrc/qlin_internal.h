@@ -131,8 +131,9 @@ struct CombineLaunch {
 // How qlin_lora runs for given sizes (qlin_lora.hip).
 struct LoraPlan {
     int sorted;                // the rows are sorted by adapter first
-    int ct;                    // 16-row sub-tiles per row tile
+    int wide;                  // row tiles of 64 rows instead of 16
     int max_tiles;             // row tiles, at most
+    int shrink_ct, sub_tiles;  // 16-row sub-tiles per shrink workgroup, shrink workgroups per row tile
     int rt, rank_chunks;       // shrink: 16-rank sub-tiles per workgroup, workgroups along the ranks
     int splits, k_steps;       // shrink: K parts, 32-wide steps for each wave of a part
     int v_stride;              // floats between rows of v
@@ -153,6 +154,7 @@ struct LoraLaunch {
     int64_t ldy;
     int M, N, K, adapters, max_rank;
     int splits, k_steps, v_stride, n_chunk;
+    int sub_tiles;             // shrink workgroups per row tile
     float *v;                  // [splits][M][v_stride]
     int4 *tiles;               // sorted: (adapter, first place, rows, 0)
     int *tile_count, *perm, *place;
@@ -186,7 +188,7 @@ inline int route_hist_stride(int experts) { return (experts + 7) & ~7; }
 hipError_t launch_route(const RouteLaunch &a, hipStream_t s);
 hipError_t launch_dispatch(int fmt, const DispatchLaunch &a, hipStream_t s);
 hipError_t launch_combine(bool h32, bool y32, const CombineLaunch &a, hipStream_t s);
-void lora_plan(int M, int N, int K, int adapters, int max_rank, LoraPlan *p);
+void lora_plan(int M, int N, int K, int adapters, int max_rank, bool f32, LoraPlan *p);
 hipError_t launch_lora(const LoraPlan &p, bool f32, const LoraLaunch &a, hipStream_t s);
 bool gemm_variant_exists(int fmt, bool swap, int tile_m, int nr, int xc);
 // this device's static scratch array (kScratchBytes, zero between calls);

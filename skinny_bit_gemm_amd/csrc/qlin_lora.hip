@@ -9,6 +9,8 @@
 //   expand  adds the slices up and y = base + s B_a v for a run of columns.
 // Up to 64 rows, a workgroup finds its tile from the ids with one ballot;
 // past that, group_kernel sorts the rows by adapter first.
+#include <algorithm>
+
 #include "qlin_device.h"
 
 namespace qlin {
@@ -17,6 +19,7 @@ namespace {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ v4f mfma_bf16(uint4 a, uint4 b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0,
@@ -39,7 +42,9 @@ __device__ __forceinline__ int rank_of(const LoraLaunch &a, int adapter) {
     return a.ranks ? min(max(a.ranks[adapter], 0), a.max_rank) : a.max_rank;
 }
 
-constexpr int kShrinkWaves = 8, kShrinkWavesWide = 4;   // of a shrink workgroup, 16- and 64-row tiles
+constexpr int shrink_waves(int ct) { return ct == 4 ? 4 : 8; }   // of a shrink workgroup of 16 ct rows
+
+constexpr int kWideRows = 64;   // rows of a wide tile
 
 // One tile: `count` rows of one adapter (adapters: rows without one).
 struct Tile {
@@ -50,19 +55,21 @@ struct Tile {
 // Rows up to which a workgroup finds its tile by ballots over the ids.
 constexpr int kDirectRows = 64;
 
-// Finds tile `ti` and its rows (member[0 .. 16 CT)); count 0: there is no
-// such tile.  Ends with a barrier when the tile exists.
+// Finds part `sub` (16 CT rows) of tile `ti` and its rows (member[0 .. 16 CT));
+// count 0: there is no such part.  Ends with a barrier when there is.
 template <int CT, bool SORTED>
-__device__ __forceinline__ Tile find_tile(const LoraLaunch &a, int ti, int *member) {
+__device__ __forceinline__ Tile find_tile(const LoraLaunch &a, int ti, int sub, int *member) {
     Tile t = {0, 0, -1};
     const int tid = threadIdx.x, lane = tid & 63;
     if constexpr (SORTED) {
         if (ti >= a.tile_count[0]) return t;
         const int4 d = a.tiles[ti];
+        const int first = sub * 16 * CT;
+        if (first >= d.z) return t;
         t.adapter = d.x;
-        t.v0 = d.y;
-        t.count = d.z;
-        if (tid < t.count) member[tid] = a.perm[d.y + tid];
+        t.v0 = d.y + first;
+        t.count = min(d.z - first, 16 * CT);
+        if (tid < t.count) member[tid] = a.perm[t.v0 + tid];
     } else {
         // a tile starts at every 16th row of its adapter's rows, and is known
         // by that row's number
@@ -101,7 +108,7 @@ __global__ __launch_bounds__(64 * NW) void shrink_kernel(LoraLaunch a) {
     __shared__ int member[16 * CT];
     __shared__ v4f part[NW][RT][64];
     const int split = blockIdx.x, rank0 = blockIdx.z * 16 * RT;
-    const Tile t = find_tile<CT, SORTED>(a, blockIdx.y, member);
+    const Tile t = find_tile<CT, SORTED>(a, blockIdx.y / a.sub_tiles, blockIdx.y % a.sub_tiles, member);
     if (t.count == 0 || rank0 >= rank_of(a, t.adapter)) return;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int c16 = lane & 15, kg = lane >> 4;
@@ -154,63 +161,75 @@ __global__ __launch_bounds__(64 * NW) void shrink_kernel(LoraLaunch a) {
     }
 }
 
-// y of one tile for n_chunk columns; each of the four waves has a quarter of
-// them, 32 at a time.  D[column][row] from B rows and v.
-//
-// First the tile's v: the slices are added up, the adapter's scale is applied
-// and the sum is written to the LDS as TERMS bf16 numbers that add up to it.
-// Each takes 8 more bits of the mantissa, so that the second product loses
-// nothing that its fp32 sums would keep (TERMS 3, fp32 y) or less than the
-// bf16 rounding of y shows (TERMS 2).  Ranks past the adapter's are zero.
+// Four numbers as TERMS bf16 numbers each that add up to them: each takes 8
+// more bits of the mantissa.
+template <int TERMS>
+__device__ __forceinline__ void split4(v4f f, uint2 (&out)[TERMS]) {
+#pragma unroll
+    for (int e = 0; e < TERMS; ++e) {
+        out[e] = make_uint2(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]));
+        f[0] -= bf16_lo(out[e].x);
+        f[1] -= bf16_hi(out[e].x);
+        f[2] -= bf16_lo(out[e].y);
+        f[3] -= bf16_hi(out[e].y);
+    }
+}
+
+// Eight bf16 columns: base + what the products give, each rounded once.
+__device__ __forceinline__ uint4 add_pairs(uint4 b, float f0, float f1, float f2, float f3, float f4, float f5, float f6,
+                                           float f7) {
+    return make_uint4(bf16_pair(bf16_lo(b.x) + f0, bf16_hi(b.x) + f1), bf16_pair(bf16_lo(b.y) + f2, bf16_hi(b.y) + f3),
+                      bf16_pair(bf16_lo(b.z) + f4, bf16_hi(b.z) + f5), bf16_pair(bf16_lo(b.w) + f6, bf16_hi(b.w) + f7));
+}
+
+// A tile's v into the LDS (vs[TERMS][ROWS][32 steps + 8]) by 256 threads: the
+// slices are added up, the adapter's scale is applied and the sum is kept as
+// TERMS bf16 numbers that add up to it, so that the second product loses
+// nothing that its fp32 sums would keep (3, for fp32 y) or less than the bf16
+// rounding of y shows (2).  Ranks past the adapter's are zero.
+template <int ROWS, int TERMS>
+__device__ __forceinline__ void fill_v(const LoraLaunch &a, const Tile &t, const int *member, int ranks, int steps,
+                                       uint16_t *vs) {
+    const int tid = threadIdx.x, stride = steps * 32 + 8;
+    const float scale = a.scales && t.adapter < a.adapters ? a.scales[t.adapter] : 1.0f;
+    for (int row = tid >> 4; row < ROWS; row += 16)   // 16 threads a row, four ranks each
+        for (int rank = (tid & 15) * 4; rank < steps * 32; rank += 64) {
+            v4f f = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (row < t.count && rank < ranks) {
+                const float *p = a.v + (int64_t)(t.v0 >= 0 ? t.v0 + row : member[row]) * a.v_stride + rank;
+                for (int s = 0; s < a.splits; ++s) f += *reinterpret_cast<const v4f *>(p + (int64_t)s * a.M * a.v_stride);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = rank + j < ranks ? f[j] * scale : 0.0f;
+            uint2 o[TERMS];
+            split4<TERMS>(f, o);
+#pragma unroll
+            for (int e = 0; e < TERMS; ++e) *reinterpret_cast<uint2 *>(vs + (e * ROWS + row) * stride + rank) = o[e];
+        }
+}
+
+// y of one tile of up to 16 rows for n_chunk columns; each of the four waves
+// has a quarter of them, 32 at a time.  D[column][row] from B rows and v.
 //
 // RK: 32-rank steps (0: more than two, B read as it is needed).  The next
 // columns' B rows and base are on their way while these are multiplied.  The
 // columns of a wave's two tiles are dealt so that each lane ends with 16
 // consecutive bytes of its row.
-template <int CT, int RK, bool F32, bool SORTED>
-__global__ __launch_bounds__(256) void expand_kernel(LoraLaunch a) {
-    constexpr int TERMS = F32 ? 3 : 2, ROWS = 16 * CT;
-    extern __shared__ __align__(16) uint16_t vs[];   // [TERMS][ROWS][stride]
-    __shared__ int member[ROWS];
-    const Tile t = find_tile<CT, SORTED>(a, blockIdx.y, member);
+template <int RK, bool F32, bool SORTED>
+__global__ __launch_bounds__(256, 4) void expand_kernel(LoraLaunch a) {
+    constexpr int TERMS = F32 ? 3 : 2;
+    extern __shared__ __align__(16) uint16_t vs[];   // [TERMS][16][stride]
+    __shared__ int member[16];
+    const Tile t = find_tile<1, SORTED>(a, blockIdx.y, 0, member);
     if (t.count == 0) return;
     const int ranks = rank_of(a, t.adapter);
     if (ranks == 0 && a.base == a.y) return;   // these rows are already there
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int c16 = lane & 15, kg = lane >> 4;
     const int steps = RK > 0 ? RK : (ranks + 31) / 32, stride = steps * 32 + 8;
-    const float scale = a.scales && t.adapter < a.adapters ? a.scales[t.adapter] : 1.0f;
 
-    for (int i = tid; i < ROWS * steps * 8; i += 256) {   // four ranks of a row
-        const int row = i / (steps * 8), rank = (i - row * steps * 8) * 4;
-        v4f f = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (row < t.count && rank < ranks) {
-            const float *p = a.v + (int64_t)(t.v0 >= 0 ? t.v0 + row : member[row]) * a.v_stride + rank;
-            for (int s = 0; s < a.splits; ++s) f += *reinterpret_cast<const v4f *>(p + (int64_t)s * a.M * a.v_stride);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] = rank + j < ranks ? f[j] * scale : 0.0f;
-#pragma unroll
-        for (int e = 0; e < TERMS; ++e) {
-            const uint32_t lo = bf16_pair(f[0], f[1]), hi = bf16_pair(f[2], f[3]);
-            *reinterpret_cast<uint2 *>(vs + ((int64_t)e * ROWS + row) * stride + rank) = make_uint2(lo, hi);
-            f[0] -= bf16_lo(lo);
-            f[1] -= bf16_hi(lo);
-            f[2] -= bf16_lo(hi);
-            f[3] -= bf16_hi(hi);
-        }
-    }
-    __syncthreads();
-
-    int64_t yrow[CT], brow[CT];
-    bool in_tile[CT];
-#pragma unroll
-    for (int c = 0; c < CT; ++c) {
-        in_tile[c] = c * 16 + c16 < t.count;
-        const int64_t m = member[in_tile[c] ? c * 16 + c16 : 0];
-        yrow[c] = m * a.ldy;
-        brow[c] = m * a.ldb;
-    }
+    const bool in_tile = c16 < t.count;
+    const int64_t m = member[in_tile ? c16 : 0], yrow = m * a.ldy, brow = m * a.ldb;
     const int quarter = a.n_chunk / 4;
     const int n_begin = blockIdx.x * a.n_chunk + w * quarter, n_end = min(a.N, n_begin + quarter);
     // D's row 4 kg + i of tile j is column col(j) + i, and the lane that loads
@@ -242,30 +261,32 @@ __global__ __launch_bounds__(256) void expand_kernel(LoraLaunch a) {
             b[j] = make_uint4(b[j].x & keep[0], b[j].y & keep[1], b[j].z & keep[2], b[j].w & keep[3]);
     };
     constexpr int PARTS = F32 ? 2 : 1;   // 16-byte pieces of a lane's columns
-    auto load_base = [&](int n, uint4 (&o)[CT][PARTS]) {
+    auto load_base = [&](int n, uint4 (&o)[PARTS]) {
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
-#pragma unroll
-            for (int h = 0; h < PARTS; ++h) {
-                const int at = n + col(h, kg);
-                o[c][h] = make_uint4(0, 0, 0, 0);
-                if (a.base && in_tile[c] && at < n_end) {
-                    if constexpr (F32)
-                        o[c][h] = *reinterpret_cast<const uint4 *>(static_cast<const float *>(a.base) + brow[c] + at);
-                    else
-                        o[c][h] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.base) + brow[c] + at);
-                }
+        for (int h = 0; h < PARTS; ++h) {
+            const int at = n + col(h, kg);
+            o[h] = make_uint4(0, 0, 0, 0);
+            if (a.base && in_tile && at < n_end) {
+                if constexpr (F32)
+                    o[h] = *reinterpret_cast<const uint4 *>(static_cast<const float *>(a.base) + brow + at);
+                else
+                    o[h] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.base) + brow + at);
             }
+        }
     };
     constexpr int HELD = RK > 0 ? RK : 1;
-    uint4 b_next[HELD][2], base_next[CT][PARTS];
+    uint4 b_next[HELD][2], base_next[PARTS];
     if constexpr (RK > 0)
 #pragma unroll
         for (int q = 0; q < RK; ++q) load_b(n_begin, q, b_next[q]);
     load_base(n_begin, base_next);
+
+    fill_v<16, TERMS>(a, t, member, ranks, steps, vs);
+    __syncthreads();
+
     for (int n = n_begin; n < n_end; n += 32) {
-        v4f acc[CT][2] = {};
-        uint4 b_now[HELD][2], base_now[CT][PARTS];
+        v4f acc[2] = {};
+        uint4 b_now[HELD][2], base_now[PARTS];
         if constexpr (RK > 0) {
 #pragma unroll
             for (int q = 0; q < RK; ++q)
@@ -273,9 +294,7 @@ __global__ __launch_bounds__(256) void expand_kernel(LoraLaunch a) {
                 for (int j = 0; j < 2; ++j) b_now[q][j] = b_next[q][j];
         }
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
-#pragma unroll
-            for (int h = 0; h < PARTS; ++h) base_now[c][h] = base_next[c][h];
+        for (int h = 0; h < PARTS; ++h) base_now[h] = base_next[h];
         if (n + 32 < n_end) {
             if constexpr (RK > 0)
 #pragma unroll
@@ -292,39 +311,186 @@ __global__ __launch_bounds__(256) void expand_kernel(LoraLaunch a) {
             }
             clear_past(q, b);
 #pragma unroll
-            for (int c = 0; c < CT; ++c)
+            for (int e = TERMS - 1; e >= 0; --e) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(vs + (e * 16 + c16) * stride + q * 32 + kg * 8);
 #pragma unroll
-                for (int e = TERMS - 1; e >= 0; --e) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(
-                        vs + ((int64_t)e * ROWS + c * 16 + c16) * stride + q * 32 + kg * 8);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) acc[c][j] = mfma_bf16(b[j], v, acc[c][j]);
-                }
+                for (int j = 0; j < 2; ++j) acc[j] = mfma_bf16(b[j], v, acc[j]);
+            }
             if constexpr (RK > 0)
                 if (q + 1 == RK) break;
         }
+        if (!in_tile) continue;
+        if constexpr (F32) {
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-            if (!in_tile[c]) continue;
-            if constexpr (F32) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int at = n + col(h, kg);
-                    if (at < n_end)
-                        *reinterpret_cast<v4f *>(static_cast<float *>(a.y) + yrow[c] + at) =
-                            acc[c][h] + __builtin_bit_cast(v4f, base_now[c][h]);
-                }
-            } else {
-                const int at = n + col(0, kg);
-                const uint4 o = base_now[c][0];
-                const v4f p = acc[c][0], q = acc[c][1];
+            for (int h = 0; h < 2; ++h) {
+                const int at = n + col(h, kg);
                 if (at < n_end)
-                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.y) + yrow[c] + at) =
-                        make_uint4(bf16_pair(bf16_lo(o.x) + p[0], bf16_hi(o.x) + p[1]),
-                                   bf16_pair(bf16_lo(o.y) + p[2], bf16_hi(o.y) + p[3]),
-                                   bf16_pair(bf16_lo(o.z) + q[0], bf16_hi(o.z) + q[1]),
-                                   bf16_pair(bf16_lo(o.w) + q[2], bf16_hi(o.w) + q[3]));
+                    *reinterpret_cast<v4f *>(static_cast<float *>(a.y) + yrow + at) =
+                        acc[h] + __builtin_bit_cast(v4f, base_now[h]);
             }
+        } else {
+            const int at = n + col(0, kg);
+            if (at < n_end)
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.y) + yrow + at) =
+                    add_pairs(base_now[0], acc[0][0], acc[0][1], acc[0][2], acc[0][3], acc[1][0], acc[1][1], acc[1][2],
+                              acc[1][3]);
+        }
+    }
+}
+
+// y of one tile of up to 64 rows (16 a wave) for n_chunk columns, COLS at a
+// time.  D[row][column] from v and B rows.
+//
+// What bounds it is the way to memory, and that is a matter of how neighbouring
+// lanes lie.  A fragment of the matrix cores has them in different rows: read
+// or written like that, every lane is an access of its own, 16 bytes a clock
+// for a compute unit.  So B goes through the LDS, loaded as it lies in memory
+// a stage ahead, once for 64 rows; and a lane has NJ consecutive columns (tile
+// j has the columns NJ c + j), so that 16 lanes load and store 256 consecutive
+// bytes of a row of y, with the non-temporal policy (the next call's shrink
+// then does not wait for y's lines to leave the caches: 27 -> 21 us).  4096
+// rows, 10240 columns, rank 64: 44 us against 62 with B read by each wave and
+// half lines of y at a time, 55 with 128 bytes of a row.
+//   PASS  8-rank chunks of B in a stage: 4 (max_rank <= 32) or 8
+//   ONE   a stage holds all ranks (max_rank <= 8 PASS): v stays in registers
+template <int PASS, bool ONE, bool F32>
+__global__ __launch_bounds__(256) void expand_wide_kernel(LoraLaunch a) {
+    constexpr int TERMS = F32 ? 3 : 2, ROWS = kWideRows, NJ = F32 ? 4 : 8, COLS = 16 * NJ;
+    constexpr int LOADS = COLS * PASS / 256;              // 16-byte loads of a thread for a stage
+    __shared__ uint4 bs[COLS * (PASS + 1)];               // [tile j, lane's column][chunk], rows one chunk apart
+    extern __shared__ __align__(16) uint16_t vs[];        // [TERMS][ROWS][stride]
+    __shared__ int member[ROWS];
+    const Tile t = find_tile<ROWS / 16, true>(a, blockIdx.y, 0, member);
+    if (t.count == 0) return;
+    const int ranks = rank_of(a, t.adapter);
+    if (ranks == 0 && a.base == a.y) return;   // these rows are already there
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const int c16 = lane & 15, kg = lane >> 4;
+    const int steps = (a.max_rank + 31) / 32, stride = steps * 32 + 8;
+    const int n_begin = blockIdx.x * a.n_chunk, n_end = min(a.N, n_begin + a.n_chunk);
+    const int held = min(a.max_rank / 8, PASS);           // chunks of a B row in a stage
+    const int passes = ONE ? (ranks > 0 ? 1 : 0) : (ranks + PASS * 8 - 1) / (PASS * 8);
+
+    // chunk p of a stage is column p / held (by its reciprocal: exact for
+    // p < 2^13), place p % held; it goes to the LDS row of its tile and lane
+    const uint32_t recip = 65536u / held + 1;
+    int to[LOADS], from[LOADS], place[LOADS];
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+        const int p = i * 256 + tid, col = (int)(p * recip >> 16);
+        place[i] = p - col * held;
+        to[i] = ((col % NJ) * 16 + col / NJ) * (PASS + 1) + place[i];
+        from[i] = col * a.max_rank + place[i] * 8;
+        if (col >= COLS) place[i] = 1 << 20;   // past the stage
+    }
+    const uint16_t *const b_rows = a.B + (int64_t)t.adapter * a.N * a.max_rank;
+    uint4 next[LOADS];
+    auto load_b = [&](int n, int pass) {
+        const uint16_t *p = b_rows + (int64_t)n * a.max_rank + pass * PASS * 8;
+        if (held == PASS && n + COLS <= n_end && (pass + 1) * PASS * 8 <= ranks) {
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) next[i] = *reinterpret_cast<const uint4 *>(p + from[i]);
+            return;
+        }
+        const int end = (n_end - n) * a.max_rank - pass * PASS * 8;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            next[i] = make_uint4(0, 0, 0, 0);
+            if ((pass * PASS + place[i]) * 8 < ranks && from[i] < end) next[i] = *reinterpret_cast<const uint4 *>(p + from[i]);
+        }
+    };
+    auto put_b = [&]() {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            if (place[i] < held) bs[to[i]] = next[i];
+    };
+    load_b(n_begin, 0);
+
+    fill_v<ROWS, TERMS>(a, t, member, ranks, steps, vs);
+    put_b();
+    __syncthreads();
+
+    const int row0 = w * 16;
+    const bool idle = row0 >= t.count;
+    const v4u *const base0 = static_cast<const v4u *>(a.base);
+    v4u *const y0 = static_cast<v4u *>(a.y);
+    constexpr int PER = F32 ? 4 : 8;   // columns of 16 bytes
+    int64_t base_at[4], y_at[4];
+    bool live[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = row0 + kg * 4 + i;
+        live[i] = r < t.count;
+        const int64_t m = member[live[i] ? r : 0];
+        base_at[i] = (m * a.ldb + n_begin) / PER + c16;
+        y_at[i] = (m * a.ldy + n_begin) / PER + c16;
+    }
+    uint4 vf[PASS / 4][TERMS];
+    auto load_v = [&](int pass) {
+#pragma unroll
+        for (int q = 0; q < PASS / 4; ++q)
+#pragma unroll
+            for (int e = 0; e < TERMS; ++e)
+                vf[q][e] = pass * PASS * 8 + q * 32 < ranks
+                               ? *reinterpret_cast<const uint4 *>(vs + (e * ROWS + row0 + c16) * stride + pass * PASS * 8 +
+                                                                  q * 32 + kg * 8)
+                               : make_uint4(0, 0, 0, 0);
+    };
+    if constexpr (ONE) load_v(0);
+    for (int n = n_begin; n < n_end; n += COLS) {
+        const bool in = n + c16 * PER < n_end;   // n_end is a multiple of 16
+        v4u base[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            base[i] = v4u{0, 0, 0, 0};
+            if (a.base && in && live[i]) base[i] = __builtin_nontemporal_load(base0 + base_at[i]);
+            base_at[i] += COLS / PER;
+        }
+        v4f acc[NJ] = {};
+        for (int pass = 0; pass < passes; ++pass) {
+            const bool more = pass + 1 < passes || n + COLS < n_end;
+            if (pass + 1 < passes) load_b(n, pass + 1);
+            else if (n + COLS < n_end) load_b(n + COLS, 0);
+            if constexpr (!ONE) load_v(pass);
+#pragma unroll
+            for (int q = 0; q < PASS / 4; ++q) {
+                const int rank0 = pass * PASS * 8 + q * 32, rank = rank0 + kg * 8;
+                if (rank0 >= ranks || idle) break;
+                uint4 bq[NJ];
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+                    bq[j] = bs[(j * 16 + c16) * (PASS + 1) + q * 4 + kg];
+                if (rank0 + 32 > ranks) {   // as expand_kernel's clear_past
+                    uint32_t keep[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        keep[i] = (rank + 2 * i < ranks ? 0xFFFFu : 0u) | (rank + 2 * i + 1 < ranks ? 0xFFFF0000u : 0u);
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j)
+                        bq[j] = make_uint4(bq[j].x & keep[0], bq[j].y & keep[1], bq[j].z & keep[2], bq[j].w & keep[3]);
+                }
+#pragma unroll
+                for (int e = TERMS - 1; e >= 0; --e)
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) acc[j] = mfma_bf16(vf[q][e], bq[j], acc[j]);
+            }
+            if (more) {
+                __syncthreads();
+                put_b();
+                __syncthreads();
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v4u o;
+            if constexpr (F32) {
+                o = __builtin_bit_cast(v4u, v4f{acc[0][i], acc[1][i], acc[2][i], acc[3][i]} + __builtin_bit_cast(v4f, base[i]));
+            } else {
+                o = __builtin_bit_cast(v4u, add_pairs(__builtin_bit_cast(uint4, base[i]), acc[0][i], acc[1][i], acc[2][i],
+                                                      acc[3][i], acc[4][i], acc[5][i], acc[6][i], acc[7][i]));
+            }
+            if (in && live[i]) __builtin_nontemporal_store(o, y0 + y_at[i]);
+            y_at[i] += COLS / PER;
         }
     }
 }
@@ -410,28 +576,40 @@ __global__ __launch_bounds__(1024) void group_kernel(LoraLaunch a, int tile_rows
 
 // ---------------------------------------------------------------- planning
 
-void lora_plan(int M, int N, int K, int adapters, int max_rank, LoraPlan *p) {
+constexpr int kWideFrom = 1024;   // rows from which tiles are wide
+
+void lora_plan(int M, int N, int K, int adapters, int max_rank, bool f32, LoraPlan *p) {
     p->sorted = M > kDirectRows;
-    p->ct = M >= 1024 ? 4 : 1;
-    const int tile_rows = 16 * p->ct;
-    p->max_tiles = p->sorted ? (M + tile_rows - 1) / tile_rows + (adapters + 1 < M ? adapters + 1 : M) : M;
+    p->wide = M >= kWideFrom;
+    const int tile_rows = p->wide ? kWideRows : 16;
+    p->max_tiles = p->sorted ? (M + tile_rows - 1) / tile_rows + std::min(adapters + 1, M) : M;
     p->rt = max_rank <= 16 ? 1 : max_rank <= 32 ? 2 : 4;
     p->rank_chunks = (max_rank + 16 * p->rt - 1) / (16 * p->rt);
     p->v_stride = (max_rank + 15) / 16 * 16;
     // K parts: one or two workgroups for each compute unit, at most four parts
     // (the expand kernel reads them all for each of its column runs), two
     // steps of 32 or more for each wave
-    const int steps = (K + 31) / 32, waves = p->ct == 1 ? kShrinkWaves : kShrinkWavesWide;
-    const int tiles = p->sorted ? (M + tile_rows - 1) / tile_rows : M;
-    int splits = 2 * kComputeUnits / (tiles * p->rank_chunks);
-    splits = splits > 4 ? 4 : splits < 1 ? 1 : splits;
-    if (splits > steps / (2 * waves)) splits = steps / (2 * waves) > 0 ? steps / (2 * waves) : 1;
+    p->shrink_ct = !p->wide ? 1 : p->rt == 1 ? 1 : p->rt == 2 ? 2 : 4;
+    p->sub_tiles = tile_rows / (16 * p->shrink_ct);
+    const int steps = (K + 31) / 32, waves = shrink_waves(p->shrink_ct);
+    const int groups = std::min(adapters, M);
+    // about how many tiles there are: full ones, or one for each adapter
+    const int tiles = std::max((M + tile_rows - 1) / tile_rows, groups);
+    const int shrink_tiles = std::max((M + 16 * p->shrink_ct - 1) / (16 * p->shrink_ct), groups);
+    int splits = 2 * kComputeUnits / (shrink_tiles * p->rank_chunks);
+    const int cap = p->wide ? 2 : 4;
+    splits = std::min(std::max(splits, 1), cap);
+    splits = std::max(std::min(splits, steps / (2 * waves)), 1);
     p->k_steps = (steps + waves * splits - 1) / (waves * splits);
     p->splits = (steps + waves * p->k_steps - 1) / (waves * p->k_steps);
-    // columns per expand workgroup: runs as long as leave four workgroups for
-    // each compute unit
+    // columns per expand workgroup: four stages, or runs as long as leave four
+    // workgroups for each compute unit
     int n_chunk = 256;
-    while (n_chunk < 4096 && (int64_t)((N + 2 * n_chunk - 1) / (2 * n_chunk)) * tiles >= 4 * kComputeUnits) n_chunk *= 2;
+    if (p->wide) {
+        n_chunk = f32 ? 256 : 512;
+    } else {
+        while (n_chunk < 4096 && (int64_t)((N + 2 * n_chunk - 1) / (2 * n_chunk)) * tiles >= 4 * kComputeUnits) n_chunk *= 2;
+    }
     p->n_chunk = n_chunk;
     auto align = [](size_t v) { return (v + 255) & ~size_t(255); };
     size_t at = 0;
@@ -452,42 +630,56 @@ void lora_plan(int M, int N, int K, int adapters, int max_rank, LoraPlan *p) {
 
 template <int CT, int RT>
 static void launch_shrink(const LoraPlan &p, const LoraLaunch &a, hipStream_t s) {
-    constexpr int NW = CT == 1 ? kShrinkWaves : kShrinkWavesWide;
-    const dim3 grid(p.splits, p.max_tiles, p.rank_chunks), block(64 * NW);
+    constexpr int NW = shrink_waves(CT);
+    const dim3 grid(p.splits, p.max_tiles * a.sub_tiles, p.rank_chunks), block(64 * NW);
     if (p.sorted) hipLaunchKernelGGL((shrink_kernel<CT, RT, NW, true>), grid, block, 0, s, a);
     else if constexpr (CT == 1) hipLaunchKernelGGL((shrink_kernel<CT, RT, NW, false>), grid, block, 0, s, a);
 }
 
-template <int CT, int RK, bool F32>
+template <int RK, bool F32>
 static void launch_expand(const LoraPlan &p, const LoraLaunch &a, hipStream_t s) {
     const dim3 grid((a.N + p.n_chunk - 1) / p.n_chunk, p.max_tiles), block(256);
     const int steps = RK > 0 ? RK : (a.max_rank + 31) / 32;
-    const size_t lds = (size_t)(F32 ? 3 : 2) * 16 * CT * (steps * 32 + 8) * 2;
-    if (p.sorted) hipLaunchKernelGGL((expand_kernel<CT, RK, F32, true>), grid, block, lds, s, a);
-    else if constexpr (CT == 1) hipLaunchKernelGGL((expand_kernel<CT, RK, F32, false>), grid, block, lds, s, a);
+    const size_t lds = (size_t)(F32 ? 3 : 2) * 16 * (steps * 32 + 8) * 2;
+    if (p.sorted) hipLaunchKernelGGL((expand_kernel<RK, F32, true>), grid, block, lds, s, a);
+    else hipLaunchKernelGGL((expand_kernel<RK, F32, false>), grid, block, lds, s, a);
 }
 
-template <int CT>
-static hipError_t launch_products(const LoraPlan &p, bool f32, const LoraLaunch &a, hipStream_t s) {
-    if (p.rt == 1) launch_shrink<CT, 1>(p, a, s);
-    else if (p.rt == 2) launch_shrink<CT, 2>(p, a, s);
-    else launch_shrink<CT, 4>(p, a, s);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const int steps = (a.max_rank + 31) / 32;
-    if (steps == 1) f32 ? launch_expand<CT, 1, true>(p, a, s) : launch_expand<CT, 1, false>(p, a, s);
-    else if (steps == 2) f32 ? launch_expand<CT, 2, true>(p, a, s) : launch_expand<CT, 2, false>(p, a, s);
-    else f32 ? launch_expand<CT, 0, true>(p, a, s) : launch_expand<CT, 0, false>(p, a, s);
-    return hipGetLastError();
+template <int PASS, bool ONE, bool F32>
+static void launch_expand_wide(const LoraPlan &p, const LoraLaunch &a, hipStream_t s) {
+    const dim3 grid((a.N + p.n_chunk - 1) / p.n_chunk, p.max_tiles), block(256);
+    const size_t lds = (size_t)(F32 ? 3 : 2) * kWideRows * ((a.max_rank + 31) / 32 * 32 + 8) * 2;
+    hipLaunchKernelGGL((expand_wide_kernel<PASS, ONE, F32>), grid, block, lds, s, a);
+}
+
+template <bool F32>
+static void launch_expand_any(const LoraPlan &p, const LoraLaunch &a, hipStream_t s) {
+    if (p.wide) {
+        if (a.max_rank <= 32) launch_expand_wide<4, true, F32>(p, a, s);
+        else if (a.max_rank <= 64) launch_expand_wide<8, true, F32>(p, a, s);
+        else launch_expand_wide<8, false, F32>(p, a, s);
+    } else {
+        if (a.max_rank <= 32) launch_expand<1, F32>(p, a, s);
+        else if (a.max_rank <= 64) launch_expand<2, F32>(p, a, s);
+        else launch_expand<0, F32>(p, a, s);
+    }
 }
 
 hipError_t launch_lora(const LoraPlan &p, bool f32, const LoraLaunch &a, hipStream_t s) {
+    hipError_t e = hipSuccess;
     if (p.sorted) {
-        hipLaunchKernelGGL(group_kernel, dim3(1), dim3(1024), 0, s, a, 16 * p.ct);
-        const hipError_t e = hipGetLastError();
+        hipLaunchKernelGGL(group_kernel, dim3(1), dim3(1024), 0, s, a, p.wide ? kWideRows : 16);
+        e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    return p.ct == 1 ? launch_products<1>(p, f32, a, s) : launch_products<4>(p, f32, a, s);
+    if (p.rt == 1) p.shrink_ct == 1 ? launch_shrink<1, 1>(p, a, s) : launch_shrink<1, 1>(p, a, s);
+    else if (p.rt == 2) p.shrink_ct == 1 ? launch_shrink<1, 2>(p, a, s) : launch_shrink<2, 2>(p, a, s);
+    else p.shrink_ct == 1 ? launch_shrink<1, 4>(p, a, s) : launch_shrink<4, 4>(p, a, s);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (f32) launch_expand_any<true>(p, a, s);
+    else launch_expand_any<false>(p, a, s);
+    return hipGetLastError();
 }
 
 }  // namespace qlin
