@@ -581,9 +581,8 @@ static bool aligned2(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 1
 // a leading dimension of at least n elements, in whole 16-byte units
 static bool ld_ok(int64_t ld, int n, int bytes) { return ld >= n && ld % (16 / bytes) == 0; }
 
-static size_t route_ws(const qlin_router *r, int T) {
-    const int blocks = route_blocks(T);
-    return blocks > 1 ? align256((size_t)blocks * route_hist_stride(r->experts) * 2) : 0;
+static size_t route_ws(const RoutePlan &p, const qlin_router *r) {
+    return p.once ? 0 : align256((size_t)p.blocks * route_hist_stride(r->experts) * 2);
 }
 
 static qlin_status check_tokens(int T, int topk) {
@@ -596,7 +595,7 @@ qlin_status qlin_route_workspace_bytes(const qlin_router *router, int T, size_t 
     if (st != QLIN_OK) return st;
     st = check_tokens(T, router->topk);
     if (st != QLIN_OK) return st;
-    *bytes = route_ws(router, T);
+    *bytes = route_ws(route_plan(*router, T), router);
     return QLIN_OK;
 }
 
@@ -614,7 +613,8 @@ qlin_status qlin_route(const qlin_router *router, int T, const void *logits, int
     if (!(logit_type == QLIN_OUT_BF16 ? aligned2(logits) : aligned4(logits)) || !aligned4(bias) || !aligned4(ids) ||
         !aligned4(weights) || !aligned4(group_offsets) || !aligned4(rows) || !aligned4(slots))
         return QLIN_ERR_ALIGNMENT;
-    const size_t need = route_ws(router, T);
+    const RoutePlan p = route_plan(*router, T);
+    const size_t need = route_ws(p, router);
     if (need && (!workspace || ws_bytes < need)) return QLIN_ERR_WORKSPACE;
     if (need && !aligned16(workspace)) return QLIN_ERR_ALIGNMENT;
     RouteLaunch a = {};
@@ -640,9 +640,9 @@ qlin_status qlin_route(const qlin_router *router, int T, const void *logits, int
     a.slots = slots;
     a.hist = static_cast<uint16_t *>(workspace);
     a.hist_stride = route_hist_stride(router->experts);
-    a.block_tokens = route_block_tokens(T);
-    a.blocks = route_blocks(T);
-    return hip_status(launch_route(a, static_cast<hipStream_t>(stream)));
+    a.block_tokens = p.block_tokens;
+    a.blocks = p.blocks;
+    return hip_status(launch_route(p, a, static_cast<hipStream_t>(stream)));
 }
 
 qlin_status qlin_dispatch_quantize(qlin_format fmt, int T, int topk, int K, const void *x, int64_t ldx,

@@ -88,6 +88,12 @@ struct Plan {
 qlin_status make_plan(qlin_format fmt, int M, int N, int K, const qlin_config &cfg, bool fused,
                       Plan *plan, bool grouped = false);
 
+// How qlin_route runs for a number of tokens (qlin_route.hip).
+struct RoutePlan {
+    int rows, once;
+    int blocks, block_tokens;
+};
+
 // A routing launch (qlin_route), resolved on the host.
 struct RouteLaunch {
     const void *logits;
@@ -182,10 +188,9 @@ hipError_t launch_pack_weight(int batch, int N, int K, const void *wq, void *out
 // staged in LDS; -1: direct, each wave loads its own activation fragments)
 hipError_t launch_gemm(int fmt, bool swap, int tile_m, int nr, int xc, const GemmLaunch &g,
                        size_t lds_bytes, hipStream_t s);
-int route_block_tokens(int T);
-int route_blocks(int T);
 inline int route_hist_stride(int experts) { return (experts + 7) & ~7; }
-hipError_t launch_route(const RouteLaunch &a, hipStream_t s);
+RoutePlan route_plan(const qlin_router &r, int T);
+hipError_t launch_route(const RoutePlan &p, const RouteLaunch &a, hipStream_t s);
 hipError_t launch_dispatch(int fmt, const DispatchLaunch &a, hipStream_t s);
 hipError_t launch_combine(bool h32, bool y32, const CombineLaunch &a, hipStream_t s);
 void lora_plan(int M, int N, int K, int adapters, int max_rank, bool f32, LoraPlan *p);

@@ -5,6 +5,7 @@
 // The pages name MoE layers as the next target ("Building a High-Performance
 // and Portable vLLM Linear Backend with Helion", section "Future work",
 // model-coverage paragraph).
+#include <algorithm>
 #include <type_traits>
 
 #include "qlin_device.h"
@@ -13,10 +14,8 @@ namespace qlin {
 
 namespace {
 
-constexpr int kRouteTokens = 16;                  // tokens a routing workgroup holds at once
-constexpr int kRouteThreads = 64 * kRouteTokens;
+constexpr int kPlaceThreads = 1024;
 constexpr float kFltMax = 3.402823466e38f;
-constexpr int kRouteRowTokens = 1024;             // tokens from which each has 16 lanes
 
 // ---------------------------------------------- reductions over a token's lanes
 //
@@ -28,6 +27,8 @@ template <int CTRL, int ROW_MASK = 0xF>
 __device__ __forceinline__ uint32_t moved_dpp(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, ROW_MASK, 0xF, false);
 }
+template <int CTRL>
+__device__ __forceinline__ float moved_dpp(float v) { return __uint_as_float(moved_dpp<CTRL, 0xF>(__float_as_uint(v))); }
 template <int CTRL, int ROW_MASK = 0xF>
 __device__ __forceinline__ uint32_t umax_dpp(uint32_t v) { return max(v, moved_dpp<CTRL, ROW_MASK>(v)); }
 template <int CTRL, int ROW_MASK = 0xF>
@@ -145,13 +146,38 @@ __device__ __forceinline__ uint32_t first_with(const Key (&key)[EPL], Key best, 
     }
 }
 
-// One token, by LPT lanes: lane j < topk ends with the j-th chosen expert
-// (-1: none) and its weight (topk > LPT: not here).  Lane l holds experts l,
-// l + LPT, ...  Rows past the call's tokens (`live` false) go along, closed.
-template <int LPT, int EPL, bool WIDE>
-__device__ __forceinline__ void route_token(const RouteLaunch &a, int t, bool live, int lane, int &my_id, float &my_w) {
-    using Key = std::conditional_t<WIDE, uint64_t, uint32_t>;
-    float l[EPL];
+// The weight of the token's choice that this lane holds (my_id, logit my_l).
+template <int LPT, int EPL>
+__device__ __forceinline__ float weight_of(const RouteLaunch &a, const float (&l)[EPL], float top, int my_id, float my_l) {
+    const bool mine = my_id >= 0;
+    float s;
+    if (a.score == QLIN_SCORE_SOFTMAX) {
+        // renormalized: the softmax over the chosen logits alone (the sum over
+        // the others cancels), which does not underflow
+        const float m = a.renormalize ? token_max<LPT>(my_l) : top;
+        s = mine ? expf(my_l - m) : 0.0f;
+        float sum = s;
+        if (!a.renormalize) {
+            sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) sum += l[j] > -INFINITY ? expf(l[j] - top) : 0.0f;
+        }
+        sum = token_sum<LPT>(sum);
+        s = sum > 0.0f ? s / sum : 0.0f;
+    } else {
+        s = mine ? 1.0f / (1.0f + expf(-my_l)) : 0.0f;
+        if (a.renormalize) {
+            const float sum = token_sum<LPT>(s);
+            s = sum > 0.0f ? s / sum : 0.0f;
+        }
+    }
+    return mine ? s * a.scale : 0.0f;
+}
+
+// A token's logits: lane l holds experts l, l + LPT, ...; -inf where closed.
+// Tokens past the call's (`live` false) are closed throughout.
+template <int LPT, int EPL>
+__device__ __forceinline__ void load_logits(const RouteLaunch &a, int t, bool live, int lane, float (&l)[EPL]) {
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
         const int e = lane + LPT * j;
@@ -167,6 +193,15 @@ __device__ __forceinline__ void route_token(const RouteLaunch &a, int t, bool li
         if (l[j] != l[j]) l[j] = -INFINITY;
         l[j] = fminf(l[j], kFltMax);
     }
+}
+
+// One token, by LPT lanes: lane j < topk ends with the j-th chosen expert
+// (-1: none) and its weight.  Lane l holds experts l, l + LPT, ...
+template <int LPT, int EPL, bool WIDE>
+__device__ __forceinline__ void route_token(const RouteLaunch &a, int t, int lane, int &my_id, float &my_w) {
+    using Key = std::conditional_t<WIDE, uint64_t, uint32_t>;
+    float l[EPL];
+    load_logits<LPT>(a, t, true, lane, l);
     float top = -INFINITY;
     if (a.score == QLIN_SCORE_SOFTMAX) {
 #pragma unroll
@@ -272,34 +307,144 @@ __device__ __forceinline__ void route_token(const RouteLaunch &a, int t, bool li
             my_l = li;
         }
     }
-    // weights: lane j holds the j-th choice
-    const bool mine = my_id >= 0;
-    float s;
-    if (a.score == QLIN_SCORE_SOFTMAX) {
-        // renormalized: the softmax over the chosen logits alone (the sum over
-        // the others cancels), which does not underflow
-        const float m = a.renormalize ? token_max<LPT>(my_l) : top;
-        s = mine ? expf(my_l - m) : 0.0f;
-        float sum = s;
-        if (!a.renormalize) {
-            sum = 0.0f;
-#pragma unroll
-            for (int j = 0; j < EPL; ++j) sum += l[j] > -INFINITY ? expf(l[j] - top) : 0.0f;
-        }
-        sum = token_sum<LPT>(sum);
-        s = sum > 0.0f ? s / sum : 0.0f;
-    } else {
-        s = mine ? 1.0f / (1.0f + expf(-my_l)) : 0.0f;
-        if (a.renormalize) {
-            const float sum = token_sum<LPT>(s);
-            s = sum > 0.0f ? s / sum : 0.0f;
-        }
-    }
-    my_w = mine ? s * a.scale : 0.0f;
+    my_w = weight_of<LPT, EPL>(a, l, top, my_id, my_l);
 }
 
-// Exclusive sums over value (one per thread, n <= kRouteThreads of them) into
-// off[0 .. n], by a workgroup of kRouteThreads.
+// One DPP step's partner of a double.
+template <int CTRL>
+__device__ __forceinline__ double moved_dpp(double v) {
+    return __hiloint2double((int)moved_dpp<CTRL, 0xF>((uint32_t)__double2hiint(v)),
+                            (int)moved_dpp<CTRL, 0xF>((uint32_t)__double2loint(v)));
+}
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ double smaller(double a, double b) { return fmin(a, b); }
+template <typename C>
+__device__ __forceinline__ C row_max(C v) {
+    v = larger(v, moved_dpp<0xB1>(v));
+    v = larger(v, moved_dpp<0x4E>(v));
+    v = larger(v, moved_dpp<0x141>(v));
+    return larger(v, moved_dpp<0x140>(v));
+}
+
+// 1 / d for d >= 1: two Newton steps from the hardware's estimate (within
+// 2^-20 of itself or better, so within 2^-52 after them); 0 for infinity
+__device__ __forceinline__ double recip(double d) {
+    double y = __builtin_amdgcn_rcp(d);
+    y = __builtin_fma(y, __builtin_fma(-d, y, 1.0), y);
+    y = __builtin_fma(y, __builtin_fma(-d, y, 1.0), y);
+    return d < INFINITY ? y : 0.0;
+}
+
+// One token by a row of 16 lanes, where four tokens share each instruction of
+// the reductions (groups of a multiple of 16 experts, at most 16 of them).  The
+// scores are compared as numbers, in 64 bits (WIDE) where their sums need it:
+// a double's maximum is one instruction.
+template <int EPL, bool WIDE>
+__device__ __forceinline__ void route_row(const RouteLaunch &a, int t, bool live, int lane, int &my_id, float &my_w) {
+    using C = std::conditional_t<WIDE, double, float>;
+    constexpr C kClosed = -INFINITY;
+    float l[EPL];
+    C c[EPL];
+    load_logits<16>(a, t, live, lane, l);
+    float top = -INFINITY;
+    if (a.score == QLIN_SCORE_SOFTMAX) {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) top = fmaxf(top, l[j]);
+        top = row16_max(top);
+    }
+    if constexpr (WIDE) {
+        if (a.score == QLIN_SCORE_SOFTMAX) {
+            double sum = 0.0;
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) {
+                c[j] = l[j] > -INFINITY ? exp((double)l[j] - (double)top) : 0.0;
+                sum += c[j];
+            }
+            const double y = 1.0 / row16_sum(sum);
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) c[j] *= y;
+        } else {
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) c[j] = recip(1.0 + exp(-(double)l[j]));
+        }
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            const int e = lane + 16 * j;
+            const float b = a.bias && e < a.experts ? a.bias[e] : 0.0f;
+            c[j] = l[j] > -INFINITY && b > -INFINITY ? c[j] + (double)b : kClosed;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) c[j] = l[j];
+    }
+    if (a.groups > 1) {
+        const int per = a.group_size >> 4;   // numbers j of a group
+        C worth = kClosed, m1 = kClosed, m2 = kClosed;   // worth: lane g, group g's
+        int g = 0, left = per;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            m2 = larger(m2, smaller(m1, c[j]));
+            m1 = larger(m1, c[j]);
+            if (--left == 0) {   // the two largest of the group, over the row
+                auto merge = [&](C o1, C o2) {
+                    m2 = larger(smaller(m1, o1), larger(m2, o2));
+                    m1 = larger(m1, o1);
+                };
+                merge(moved_dpp<0xB1>(m1), moved_dpp<0xB1>(m2));
+                merge(moved_dpp<0x4E>(m1), moved_dpp<0x4E>(m2));
+                merge(moved_dpp<0x141>(m1), moved_dpp<0x141>(m2));
+                merge(moved_dpp<0x140>(m1), moved_dpp<0x140>(m2));
+                const C both = a.group_top2 && m2 > kClosed ? m1 + m2 : m1;
+                worth = lane == g ? both : worth;
+                m1 = m2 = kClosed;
+                ++g;
+                left = per;
+            }
+        }
+        uint32_t kept = 0;
+        for (int n = 0; n < a.topk_groups; ++n) {
+            const C best = row_max(worth);
+            const uint32_t at = token_min<16>(worth == best ? (uint32_t)lane : 99u);
+            if (best > kClosed) kept |= 1u << at;
+            if ((uint32_t)lane == at) worth = kClosed;
+        }
+        g = 0;
+        left = per;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            if (!(kept >> g & 1)) c[j] = kClosed;
+            if (--left == 0) {
+                ++g;
+                left = per;
+            }
+        }
+    }
+    my_id = -1;
+    for (int i = 0; i < a.topk; ++i) {
+        C best = c[0];
+#pragma unroll
+        for (int j = 1; j < EPL; ++j) best = larger(best, c[j]);
+        best = row_max(best);
+        const uint32_t at = first_with<16>(c, best, lane);
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            if (at == (uint32_t)(lane + 16 * j)) c[j] = kClosed;
+        if (lane == i && best > kClosed) my_id = (int)at;
+    }
+    float my_l = -INFINITY;
+    if (my_id >= 0) {
+        const int64_t at = (int64_t)t * a.ld + my_id;
+        my_l = a.logits_bf16 ? __uint_as_float((uint32_t) static_cast<const uint16_t *>(a.logits)[at] << 16)
+                             : static_cast<const float *>(a.logits)[at];
+        my_l = fminf(my_l, kFltMax);
+    }
+    my_w = weight_of<16, EPL>(a, l, top, my_id, my_l);
+}
+
+// Exclusive sums over value (one per thread, n <= the workgroup's threads)
+// into off[0 .. n].
 __device__ __forceinline__ void scan_to(uint32_t value, int n, uint32_t *off, uint32_t *wave_tot) {
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     uint32_t v = tid < n ? value : 0;
@@ -318,27 +463,36 @@ __device__ __forceinline__ void scan_to(uint32_t value, int n, uint32_t *off, ui
     __syncthreads();
 }
 
-// Routes block_tokens tokens, 16 at a time.  Each expert has a bit per token
-// of the 16, so a pair's place among its expert's rows of this block is a
-// count of bits: token order, whatever order the waves come in.
-//   ONE (one workgroup for the call): scans the experts' counts and writes
-//   rows and slots; else leaves each pair's place in slots and the experts'
-//   counts of this block in hist, and place_kernel does the rest.
-template <int LPT, int EPL, bool WIDE, bool ONE>
-__global__ __launch_bounds__(kRouteTokens *LPT) void route_kernel(RouteLaunch a) {
-    constexpr int THREADS = kRouteTokens * LPT;
+template <int LPT, int EPL, bool WIDE>
+__device__ __forceinline__ void route_any(const RouteLaunch &a, int t, bool live, int lane, int &id, float &w) {
+    if constexpr (LPT == 16) {
+        if (__any(live)) route_row<EPL, WIDE>(a, t, live, lane, id, w);
+    } else {
+        if (live) route_token<LPT, EPL, WIDE>(a, t, lane, id, w);
+    }
+}
+
+// Routes block_tokens tokens, TOKENS at a time.  Each expert has a bit per
+// token of these, so a pair's place among its expert's rows of this block is a
+// count of bits: token order, whatever order the waves come in.  Leaves each
+// pair's place in slots and the experts' counts of this block in hist;
+// place_kernel does the rest.
+template <int LPT, int EPL, bool WIDE, int TOKENS>
+__global__ __launch_bounds__(TOKENS *LPT) void route_kernel(RouteLaunch a) {
+    static_assert(TOKENS <= 32, "a bit per token");
+    constexpr int THREADS = TOKENS * LPT;
     __shared__ uint32_t cnt[QLIN_MAX_EXPERTS], bits[QLIN_MAX_EXPERTS];
     const int tid = threadIdx.x, lane = tid % LPT, w = tid / LPT;
     for (int e = tid; e < a.experts; e += THREADS) cnt[e] = bits[e] = 0;
     __syncthreads();
     const int t0 = blockIdx.x * a.block_tokens;
     const int t1 = min(a.T, t0 + a.block_tokens);
-    for (int tb = t0; tb < t1; tb += kRouteTokens) {
+    for (int tb = t0; tb < t1; tb += TOKENS) {
         const int t = tb + w;
         const bool live = t < t1;
         int id = -1;
         float wt = 0.0f;
-        if (LPT < 64 || live) route_token<LPT, EPL, WIDE>(a, t, live, lane, id, wt);
+        route_any<LPT, EPL, WIDE>(a, t, live, lane, id, wt);
         if (live && lane < a.topk) {
             a.ids[(int64_t)t * a.topk + lane] = id;
             a.weights[(int64_t)t * a.topk + lane] = wt;
@@ -355,41 +509,57 @@ __global__ __launch_bounds__(kRouteTokens *LPT) void route_kernel(RouteLaunch a)
         }
         __syncthreads();
     }
-    if constexpr (!ONE) {
-        for (int e = tid; e < a.hist_stride; e += THREADS)
-            a.hist[(int64_t)blockIdx.x * a.hist_stride + e] = e < a.experts ? (uint16_t)cnt[e] : 0;
-    } else {
-        __shared__ uint32_t off[QLIN_MAX_EXPERTS + 1], wave_tot[kRouteTokens];
-        scan_to(tid < a.experts ? cnt[tid] : 0, a.experts, off, wave_tot);
-        for (int i = tid; i <= a.experts; i += THREADS) a.offsets[i] = (int)off[i];
-        for (int t = w; t < a.T; t += kRouteTokens) {
-            if (lane >= a.topk) continue;
-            const int64_t p = (int64_t)t * a.topk + lane;   // written by this thread above
-            const int id = a.ids[p];
-            if (id < 0) continue;
-            const int slot = (int)off[id] + a.slots[p];
-            a.slots[p] = slot;
+    for (int e = tid; e < a.hist_stride; e += THREADS)
+        a.hist[(int64_t)blockIdx.x * a.hist_stride + e] = e < a.experts ? (uint16_t)cnt[e] : 0;
+}
+
+// All of the call's tokens (at most 64) at once, by one workgroup: one launch.
+// As route_kernel, with the sums over the experts added.
+template <int LPT, int EPL, bool WIDE>
+__global__ __launch_bounds__(1024) void route_once_kernel(RouteLaunch a) {
+    __shared__ uint32_t bits[2][QLIN_MAX_EXPERTS], off[QLIN_MAX_EXPERTS + 1], wave_tot[16];
+    const int tid = threadIdx.x, lane = tid % LPT, t = tid / LPT, threads = blockDim.x;
+    for (int e = tid; e < a.experts; e += threads) bits[0][e] = bits[1][e] = 0;
+    const bool live = t < a.T;
+    int id = -1;
+    float wt = 0.0f;
+    route_any<LPT, EPL, WIDE>(a, t, live, lane, id, wt);
+    __syncthreads();
+    if (live && lane < a.topk) {
+        a.ids[t * a.topk + lane] = id;
+        a.weights[t * a.topk + lane] = wt;
+        if (id >= 0) atomicOr(&bits[t >> 5][id], 1u << (t & 31));
+    }
+    __syncthreads();
+    scan_to(tid < a.experts ? __popc(bits[0][tid]) + __popc(bits[1][tid]) : 0, a.experts, off, wave_tot);
+    if (live && lane < a.topk) {
+        int slot = -1;
+        if (id >= 0) {
+            const uint32_t below = (1u << (t & 31)) - 1;
+            slot = (int)(off[id] + (t < 32 ? __popc(bits[0][id] & below) : __popc(bits[0][id]) + __popc(bits[1][id] & below)));
             a.rows[slot] = t;
         }
-        for (int i = (int)off[a.experts] + tid; i < a.T * a.topk; i += THREADS) a.rows[i] = -1;
+        a.slots[t * a.topk + lane] = slot;
     }
+    for (int i = tid; i <= a.experts; i += threads) a.offsets[i] = (int)off[i];
+    for (int i = (int)off[a.experts] + tid; i < a.T * a.topk; i += threads) a.rows[i] = -1;
 }
 
 // Rows and slots of the pairs of kPlaceBlocks routing blocks: the expert's
 // offset, its rows in earlier blocks and the pair's place in its own block.
 // Every workgroup sums the blocks' counts for itself (2 bytes for each expert
 // and block, out of the L2) instead of waiting for a third launch.
-constexpr int kPlaceBlocks = 16;
+constexpr int kPlaceBlocks = 8;
 
-__global__ __launch_bounds__(kRouteThreads) void place_kernel(RouteLaunch a) {
+__global__ __launch_bounds__(kPlaceThreads) void place_kernel(RouteLaunch a) {
     __shared__ uint32_t pre[QLIN_MAX_EXPERTS], tot[QLIN_MAX_EXPERTS], off[QLIN_MAX_EXPERTS + 1];
     __shared__ uint16_t own[kPlaceBlocks][QLIN_MAX_EXPERTS];   // counts, then places, of this workgroup's blocks
-    __shared__ uint32_t wave_tot[kRouteTokens];
+    __shared__ uint32_t wave_tot[16];
     const int tid = threadIdx.x;
-    if (tid < a.experts) pre[tid] = tot[tid] = 0;
+    if (tid < a.hist_stride) pre[tid] = tot[tid] = 0;
     __syncthreads();
     const int b0 = blockIdx.x * kPlaceBlocks, b1 = min(a.blocks, b0 + kPlaceBlocks);
-    const int cols = a.hist_stride / 8, segs = kRouteThreads / cols;
+    const int cols = a.hist_stride / 8, segs = kPlaceThreads / cols;
     const int col = tid % cols, seg = tid / cols;
     if (seg < segs) {
         uint32_t p[8] = {}, s[8] = {};
@@ -405,17 +575,18 @@ __global__ __launch_bounds__(kRouteThreads) void place_kernel(RouteLaunch a) {
             }
             if (b >= b0 && b < b1) *reinterpret_cast<uint4 *>(&own[b - b0][col * 8]) = v;
         }
+        // expert 8 col + i lies at i x cols + col: neighbouring lanes add in
+        // neighbouring banks
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (col * 8 + i >= a.experts) break;
-            atomicAdd(&pre[col * 8 + i], p[i]);
-            atomicAdd(&tot[col * 8 + i], s[i]);
+            atomicAdd(&pre[i * cols + col], p[i]);
+            atomicAdd(&tot[i * cols + col], s[i]);
         }
     }
     __syncthreads();
-    scan_to(tid < a.experts ? tot[tid] : 0, a.experts, off, wave_tot);
+    scan_to(tid < a.experts ? tot[(tid & 7) * cols + (tid >> 3)] : 0, a.experts, off, wave_tot);
     if (blockIdx.x == 0)
-        for (int i = tid; i <= a.experts; i += kRouteThreads) a.offsets[i] = (int)off[i];
+        for (int i = tid; i <= a.experts; i += kPlaceThreads) a.offsets[i] = (int)off[i];
     if (tid < a.experts) {
         uint32_t at = 0;
         for (int b = 0; b < b1 - b0; ++b) {
@@ -427,17 +598,17 @@ __global__ __launch_bounds__(kRouteThreads) void place_kernel(RouteLaunch a) {
     __syncthreads();
     const int t0 = b0 * a.block_tokens;
     const int pairs = (min(a.T, b1 * a.block_tokens) - t0) * a.topk;
-    for (int i = tid; i < pairs; i += kRouteThreads) {
+    for (int i = tid; i < pairs; i += kPlaceThreads) {
         const int64_t p = (int64_t)t0 * a.topk + i;
         const int id = a.ids[p];
         if (id < 0) continue;
         const int t = i / a.topk;
-        const int slot = (int)(off[id] + pre[id] + own[t / a.block_tokens][id]) + a.slots[p];
+        const int slot = (int)(off[id] + pre[(id & 7) * cols + (id >> 3)] + own[t / a.block_tokens][id]) + a.slots[p];
         a.slots[p] = slot;
         a.rows[slot] = t0 + t;
     }
-    for (int i = (int)off[a.experts] + (int)blockIdx.x * kRouteThreads + tid; i < a.T * a.topk;
-         i += (int)gridDim.x * kRouteThreads)
+    for (int i = (int)off[a.experts] + (int)blockIdx.x * kPlaceThreads + tid; i < a.T * a.topk;
+         i += (int)gridDim.x * kPlaceThreads)
         a.rows[i] = -1;
 }
 
@@ -585,45 +756,61 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineLaunch a) {
 
 // --------------------------------------------------------------- launchers
 
-// Tokens per routing workgroup: all of them up to 64 (one launch, four
-// batches of 16), else 16, or more so that there are at most 512 blocks to
-// sum over.
-int route_block_tokens(int T) {
-    if (T <= 64) return 64;
-    return 16 * ((T + 16 * 512 - 1) / (16 * 512));
+// How a call runs.
+//   rows   16 lanes per token (route_row) instead of a wave: from 17 tokens
+//          on, where four tokens share an instruction (128 experts, 64 tokens:
+//          7.6 us against 10.4 in two launches; 256 in 8 groups, 128 tokens: 21
+//          against 25), and for a wave that would have a single number in a
+//          lane or a group at a time (256 in 8 groups, 16 tokens: 11 us against
+//          19; 128 experts, 1 token: 4.7 against 3.9)
+//   once   one launch for all tokens: 64 of them with 16 lanes each, 16 with
+//          a wave each
+//   else   blocks of block_tokens tokens and a second launch; at most 512
+//          blocks to sum over
+RoutePlan route_plan(const qlin_router &r, int T) {
+    RoutePlan p = {};
+    const int group = r.experts / r.groups;
+    const bool fits = r.experts <= 256 && r.topk <= 16 && (r.groups == 1 || (r.groups <= 16 && group % 16 == 0));
+    p.rows = fits && (T > 16 || r.experts <= 64 || r.groups > 1);
+    p.once = T <= (p.rows ? 64 : 16);
+    const int tokens = p.rows ? 32 : 16;
+    p.block_tokens = tokens * ((T + tokens * 512 - 1) / (tokens * 512));
+    p.blocks = p.once ? 1 : (T + p.block_tokens - 1) / p.block_tokens;
+    return p;
 }
-int route_blocks(int T) { return T <= 64 ? 1 : (T + route_block_tokens(T) - 1) / route_block_tokens(T); }
 
 template <int LPT, int EPL>
-static void launch_route_kernel(const RouteLaunch &a, hipStream_t s) {
-    const dim3 grid(a.blocks), block(kRouteTokens * LPT);
+static void launch_route_kernel(const RouteLaunch &a, bool once, hipStream_t s) {
     const bool wide = a.bias != nullptr || a.group_top2;
-    if (a.blocks > 1) {
-        if (wide) hipLaunchKernelGGL((route_kernel<LPT, EPL, true, false>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((route_kernel<LPT, EPL, false, false>), grid, block, 0, s, a);
-    } else if constexpr (LPT == 64) {
-        if (wide) hipLaunchKernelGGL((route_kernel<LPT, EPL, true, true>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((route_kernel<LPT, EPL, false, true>), grid, block, 0, s, a);
+    if (once) {
+        // as many threads as the tokens and the sums over the experts need
+        const int need = std::max(a.T * LPT, a.experts);
+        const dim3 block((std::max(need, 64) + 63) / 64 * 64);
+        if (wide) hipLaunchKernelGGL((route_once_kernel<LPT, EPL, true>), dim3(1), block, 0, s, a);
+        else hipLaunchKernelGGL((route_once_kernel<LPT, EPL, false>), dim3(1), block, 0, s, a);
+    } else {
+        constexpr int TOKENS = LPT == 16 ? 32 : 16;
+        const dim3 grid(a.blocks), block(TOKENS * LPT);
+        if (wide) hipLaunchKernelGGL((route_kernel<LPT, EPL, true, TOKENS>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((route_kernel<LPT, EPL, false, TOKENS>), grid, block, 0, s, a);
     }
 }
 
-hipError_t launch_route(const RouteLaunch &a, hipStream_t s) {
-    // 16 lanes per token where tokens are many: four tokens share each
-    // instruction of the reductions
-    if (a.T >= kRouteRowTokens && a.experts <= 256 && a.topk <= 16) {
-        if (a.experts <= 64) launch_route_kernel<16, 4>(a, s);
-        else if (a.experts <= 128) launch_route_kernel<16, 8>(a, s);
-        else launch_route_kernel<16, 16>(a, s);
+hipError_t launch_route(const RoutePlan &p, const RouteLaunch &a, hipStream_t s) {
+    if (p.rows) {
+        if (a.experts <= 64) launch_route_kernel<16, 4>(a, p.once, s);
+        else if (a.experts <= 128) launch_route_kernel<16, 8>(a, p.once, s);
+        else launch_route_kernel<16, 16>(a, p.once, s);
     } else {
-        if (a.experts <= 64) launch_route_kernel<64, 1>(a, s);
-        else if (a.experts <= 128) launch_route_kernel<64, 2>(a, s);
-        else if (a.experts <= 256) launch_route_kernel<64, 4>(a, s);
-        else if (a.experts <= 512) launch_route_kernel<64, 8>(a, s);
-        else launch_route_kernel<64, 16>(a, s);
+        if (a.experts <= 64) launch_route_kernel<64, 1>(a, p.once, s);
+        else if (a.experts <= 128) launch_route_kernel<64, 2>(a, p.once, s);
+        else if (a.experts <= 256) launch_route_kernel<64, 4>(a, p.once, s);
+        else if (a.experts <= 512) launch_route_kernel<64, 8>(a, p.once, s);
+        else launch_route_kernel<64, 16>(a, p.once, s);
     }
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.blocks == 1) return e;
-    hipLaunchKernelGGL(place_kernel, dim3((a.blocks + kPlaceBlocks - 1) / kPlaceBlocks), dim3(kRouteThreads), 0, s, a);
+    if (e != hipSuccess || p.once) return e;
+    hipLaunchKernelGGL(place_kernel, dim3((a.blocks + kPlaceBlocks - 1) / kPlaceBlocks), dim3(kPlaceThreads), 0, s, a);
     return hipGetLastError();
 }
 

@@ -163,6 +163,22 @@ def test_route_many_tokens():
     assert got[2][4] - got[2][3] == 20011
 
 
+@pytest.mark.parametrize("E,groups,kept", [(40, 1, 1), (64, 4, 2), (96, 6, 4), (128, 1, 1), (160, 10, 3), (200, 1, 1),
+                                           (256, 8, 4), (256, 16, 5), (256, 1, 1), (72, 8, 4)])
+@pytest.mark.parametrize("score", [SOFT, SIG], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("steered", [False, True], ids=["plain", "bias"])
+def test_route_prompts(E, groups, kept, score, steered):
+    """Prompts of over a thousand tokens, bf16 ties, masked experts, tokens with nothing open."""
+    bias = np.round(np.random.default_rng(E).normal(0, 0.05, E), 3).astype(np.float32) if steered else None
+    for T, bf16, masked, top2 in ((1029, True, 0.2, 1), (1500, False, 0.9, 0)):
+        l = logits_for(T, E, 31, bf16, masked)
+        l[T // 3], l[T - 1], l[5, ::2] = -INF, -INF, NAN
+        if steered:
+            bias[3], bias[E - 1] = -INF, NAN
+        check_route(l, bf16, bias, topk=7, score=score, groups=groups, topk_groups=kept, group_score=top2,
+                    renormalize=1 - top2)
+
+
 def test_route_no_tokens():
     off = guarded((65,), torch.int32, -7)
     other = guarded((16,), torch.int32, -7)
