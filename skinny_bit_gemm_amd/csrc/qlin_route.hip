@@ -556,24 +556,44 @@ __global__ __launch_bounds__(kPlaceThreads) void place_kernel(RouteLaunch a) {
     __shared__ uint16_t own[kPlaceBlocks][QLIN_MAX_EXPERTS];   // counts, then places, of this workgroup's blocks
     __shared__ uint32_t wave_tot[16];
     const int tid = threadIdx.x;
+    const int b0 = blockIdx.x * kPlaceBlocks, b1 = min(a.blocks, b0 + kPlaceBlocks);
+    const int t0 = b0 * a.block_tokens;
+    const int pairs = (min(a.T, b1 * a.block_tokens) - t0) * a.topk;
+    // the first pairs are on their way while the counts are summed
+    constexpr int kAhead = 2;
+    int ahead_id[kAhead], ahead_place[kAhead];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+        const int i = q * kPlaceThreads + tid;
+        ahead_id[q] = i < pairs ? a.ids[(int64_t)t0 * a.topk + i] : -1;
+        ahead_place[q] = i < pairs ? a.slots[(int64_t)t0 * a.topk + i] : 0;
+    }
     if (tid < a.hist_stride) pre[tid] = tot[tid] = 0;
     __syncthreads();
-    const int b0 = blockIdx.x * kPlaceBlocks, b1 = min(a.blocks, b0 + kPlaceBlocks);
     const int cols = a.hist_stride / 8, segs = kPlaceThreads / cols;
     const int col = tid % cols, seg = tid / cols;
     if (seg < segs) {
         uint32_t p[8] = {}, s[8] = {};
-    #pragma unroll 8
-        for (int b = seg; b < a.blocks; b += segs) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(a.hist + (int64_t)b * a.hist_stride + col * 8);
-            const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+        for (int first = seg; first < a.blocks; first += 8 * segs) {
+            uint4 v[8];   // eight loads on their way at a time
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t c = i & 1 ? q[i / 2] >> 16 : q[i / 2] & 0xFFFFu;
-                s[i] += c;
-                p[i] += b < b0 ? c : 0;
+            for (int u = 0; u < 8; ++u) {
+                const int b = first + u * segs;
+                v[u] = make_uint4(0, 0, 0, 0);
+                if (b < a.blocks) v[u] = *reinterpret_cast<const uint4 *>(a.hist + (int64_t)b * a.hist_stride + col * 8);
             }
-            if (b >= b0 && b < b1) *reinterpret_cast<uint4 *>(&own[b - b0][col * 8]) = v;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int b = first + u * segs;
+                const uint32_t q[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t c = i & 1 ? q[i / 2] >> 16 : q[i / 2] & 0xFFFFu;
+                    s[i] += c;
+                    p[i] += b < b0 ? c : 0;
+                }
+                if (b >= b0 && b < b1) *reinterpret_cast<uint4 *>(&own[b - b0][col * 8]) = v[u];
+            }
         }
         // expert 8 col + i lies at i x cols + col: neighbouring lanes add in
         // neighbouring banks
@@ -596,23 +616,32 @@ __global__ __launch_bounds__(kPlaceThreads) void place_kernel(RouteLaunch a) {
         }
     }
     __syncthreads();
-    const int t0 = b0 * a.block_tokens;
-    const int pairs = (min(a.T, b1 * a.block_tokens) - t0) * a.topk;
-    for (int i = tid; i < pairs; i += kPlaceThreads) {
-        const int64_t p = (int64_t)t0 * a.topk + i;
-        const int id = a.ids[p];
-        if (id < 0) continue;
+    auto put = [&](int i, int id, int place) {
+        if (id < 0) return;
         const int t = i / a.topk;
-        const int slot = (int)(off[id] + pre[(id & 7) * cols + (id >> 3)] + own[t / a.block_tokens][id]) + a.slots[p];
-        a.slots[p] = slot;
+        const int slot = (int)(off[id] + pre[(id & 7) * cols + (id >> 3)] + own[t / a.block_tokens][id]) + place;
+        a.slots[(int64_t)t0 * a.topk + i] = slot;
         a.rows[slot] = t0 + t;
-    }
+    };
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) put(q * kPlaceThreads + tid, ahead_id[q], ahead_place[q]);
+    for (int i = kAhead * kPlaceThreads + tid; i < pairs; i += kPlaceThreads)
+        put(i, a.ids[(int64_t)t0 * a.topk + i], a.slots[(int64_t)t0 * a.topk + i]);
     for (int i = (int)off[a.experts] + (int)blockIdx.x * kPlaceThreads + tid; i < a.T * a.topk;
          i += (int)gridDim.x * kPlaceThreads)
         a.rows[i] = -1;
 }
 
 // ------------------------------------------------------------------ dispatch
+
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+
+// Eight codes of a row.  Non-temporal: topk rows are written for each that is
+// read, 15.1 us against 17.0 for 4096 tokens of 2048 to 8 rows each.
+__device__ __forceinline__ void store_codes(uint8_t *to, uint2 q) {
+    __builtin_nontemporal_store(v2u{q.x, q.y}, reinterpret_cast<v2u *>(to));
+}
 
 // One token per workgroup: the row is read once, quantized as
 // quant_token_kernel does, and its codes go to each of the token's rows.
@@ -648,7 +677,7 @@ __global__ __launch_bounds__(256) void dispatch_token_kernel(DispatchLaunch a) {
         for (int j = 0; j < a.topk; ++j) {
             const int slot = slots[j];
             if ((unsigned)slot < (unsigned)a.total_rows)
-                *reinterpret_cast<uint2 *>(a.xq + (int64_t)slot * a.K + c * 8) = q;
+                store_codes(a.xq + (int64_t)slot * a.K + c * 8, q);
         }
     };
     if constexpr (CPT > 0) {
@@ -680,7 +709,7 @@ __global__ __launch_bounds__(256) void dispatch_group_kernel(DispatchLaunch a) {
     for (int i = 0; i < a.topk; ++i) {
         const int slot = a.slots[(int64_t)t * a.topk + i];
         if ((unsigned)slot >= (unsigned)a.total_rows) continue;
-        *reinterpret_cast<uint2 *>(a.xq + (int64_t)slot * a.K + g * kGroup + j * 8) = q;
+        store_codes(a.xq + (int64_t)slot * a.K + g * kGroup + j * 8, q);
         if (j == 0) a.xs[(int64_t)slot * G + g] = s;
     }
 }
@@ -697,16 +726,19 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, p);
 }
 
-// eight elements at p as fp32, and back
+// Eight elements at p as fp32, and back.  Every one of them is read or written
+// once: with the non-temporal policy on both, 4096 tokens of 2048 from 8 bf16
+// rows each and a residual take 27.5 us against 35 (6.1 TB/s).
 template <bool F32>
 __device__ __forceinline__ void load8(const void *base, int64_t at, float (&f)[8]) {
     if constexpr (F32) {
-        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + at);
-        const float4 u = p[0], v = p[1];
+        const v4f *p = reinterpret_cast<const v4f *>(static_cast<const float *>(base) + at);
+        const v4f u = __builtin_nontemporal_load(p), v = __builtin_nontemporal_load(p + 1);
         f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w;
         f[4] = v.x; f[5] = v.y; f[6] = v.z; f[7] = v.w;
     } else {
-        const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + at);
+        const v4u u =
+            __builtin_nontemporal_load(reinterpret_cast<const v4u *>(static_cast<const uint16_t *>(base) + at));
         const uint32_t q[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -718,12 +750,12 @@ __device__ __forceinline__ void load8(const void *base, int64_t at, float (&f)[8
 template <bool F32>
 __device__ __forceinline__ void store8(void *base, int64_t at, const float (&f)[8]) {
     if constexpr (F32) {
-        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(base) + at);
-        p[0] = make_float4(f[0], f[1], f[2], f[3]);
-        p[1] = make_float4(f[4], f[5], f[6], f[7]);
+        v4f *p = reinterpret_cast<v4f *>(static_cast<float *>(base) + at);
+        __builtin_nontemporal_store(v4f{f[0], f[1], f[2], f[3]}, p);
+        __builtin_nontemporal_store(v4f{f[4], f[5], f[6], f[7]}, p + 1);
     } else {
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + at) =
-            make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+        const v4u o = {bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7])};
+        __builtin_nontemporal_store(o, reinterpret_cast<v4u *>(static_cast<uint16_t *>(base) + at));
     }
 }
 
