@@ -136,6 +136,7 @@ struct CombineLaunch {
 
 // How qlin_lora runs for given sizes (qlin_lora.hip).
 struct LoraPlan {
+    int few;                   // one launch, each row by itself
     int sorted;                // the rows are sorted by adapter first
     int wide;                  // row tiles of 64 rows instead of 16
     int max_tiles;             // row tiles, at most

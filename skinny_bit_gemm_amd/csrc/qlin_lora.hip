@@ -495,10 +495,93 @@ __global__ __launch_bounds__(256) void expand_wide_kernel(LoraLaunch a) {
     }
 }
 
+// A lane's partner in a DPP step.
+template <int CTRL, int ROW_MASK = 0xF>
+__device__ __forceinline__ float moved(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROW_MASK, 0xF, false));
+}
+// The wave's sum, in lane 63 (steps as in wave_max).
+__device__ __forceinline__ float wave_add(float v) {
+    v += moved<0xB1>(v);
+    v += moved<0x4E>(v);
+    v += moved<0x141>(v);
+    v += moved<0x140>(v);
+    v += moved<0x142, 0xA>(v);
+    return v + moved<0x143, 0xC>(v);
+}
+// sum + p . q of eight bf16 each
+__device__ __forceinline__ float dot8(uint4 p, uint4 q, float sum) {
+    const uint32_t u[4] = {p.x, p.y, p.z, p.w}, v[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        sum = __builtin_fmaf(bf16_lo(u[i]), bf16_lo(v[i]), sum);
+        sum = __builtin_fmaf(bf16_hi(u[i]), bf16_hi(v[i]), sum);
+    }
+    return sum;
+}
+
+// Both products for one row in one launch, on the vector ALUs: for a few
+// single tokens the second launch costs more than reading the row's A again in
+// every workgroup.  v stays in fp32.
+//
+// Wave w takes the ranks w, w + 8, ...: the lanes lie along K, so A comes in
+// 1 KiB of consecutive bytes a load.  Then P lanes take a column, 8 ranks
+// each.  B and base are on their way meanwhile.
+template <int P, bool F32>
+__global__ __launch_bounds__(512) void few_rows_kernel(LoraLaunch a) {
+    __shared__ float v[8 * P];
+    constexpr int PER = 512 / P;   // columns of a workgroup
+    const int m = blockIdx.y, tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const int adapter = adapter_of(a, a.ids[m]), ranks = rank_of(a, adapter);
+    const int n = blockIdx.x * PER + tid / P, rank0 = tid % P * 8;
+    const int64_t at = (int64_t)m * a.ldy + n;
+    const bool first = tid % P == 0 && n < a.N;
+    uint4 b = make_uint4(0, 0, 0, 0);
+    if (n < a.N && rank0 < ranks)
+        b = *reinterpret_cast<const uint4 *>(a.B + ((int64_t)adapter * a.N + n) * a.max_rank + rank0);
+    float base = 0.0f;
+    if (first && a.base) {
+        const int64_t from = (int64_t)m * a.ldb + n;
+        if constexpr (F32) base = static_cast<const float *>(a.base)[from];
+        else base = __uint_as_float((uint32_t) static_cast<const uint16_t *>(a.base)[from] << 16);
+    }
+    const float scale = a.scales && adapter < a.adapters ? a.scales[adapter] : 1.0f;
+    const uint16_t *x = a.x + (int64_t)m * a.ldx;
+    for (int r = w; r < 8 * P; r += 8) {
+        float sum = 0.0f;
+        if (r < ranks) {
+            const uint16_t *row = a.A + ((int64_t)adapter * a.max_rank + r) * a.K;
+#pragma unroll 4
+            for (int k = lane * 8; k < a.K; k += 512) {
+                const uint4 p = *reinterpret_cast<const uint4 *>(row + k), q = *reinterpret_cast<const uint4 *>(x + k);
+                sum = dot8(p, q, sum);
+            }
+        }
+        sum = wave_add(sum);
+        if (lane == 63) v[r] = sum * scale;
+    }
+    __syncthreads();
+    float y = 0.0f;
+    const uint32_t q[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {   // ranks past the adapter's: whatever B holds there is not used
+        const float f = i & 1 ? bf16_hi(q[i / 2]) : bf16_lo(q[i / 2]);
+        y = rank0 + i < ranks ? __builtin_fmaf(f, v[rank0 + i], y) : y;
+    }
+    if constexpr (P > 1) y = y + moved<0xB1>(y);
+    if constexpr (P > 2) y = y + moved<0x4E>(y);
+    if constexpr (P > 4) y = y + moved<0x141>(y);
+    if (!first) return;
+    if constexpr (F32) static_cast<float *>(a.y)[at] = base + y;
+    else static_cast<uint16_t *>(a.y)[at] = (uint16_t)bf16_pair(base + y, 0.0f);
+}
+
 // Sorts the rows by adapter (rows without one last) into perm, and cuts each
 // adapter's rows into tiles.  One workgroup.  The order of an adapter's rows
 // depends on which wave counts first; every row's result is the same in any
 // place of any tile.
+constexpr int kHeldRows = 4;
+
 __global__ __launch_bounds__(1024) void group_kernel(LoraLaunch a, int tile_rows) {
     __shared__ uint32_t cnt[QLIN_MAX_ADAPTERS + 1];
     __shared__ uint32_t tot[2][16];
@@ -508,26 +591,37 @@ __global__ __launch_bounds__(1024) void group_kernel(LoraLaunch a, int tile_rows
     __syncthreads();
     // each row's place among its adapter's rows: within the wave by ballots
     // (one round for each adapter that the wave sees), across waves by one
-    // atomic of the round's first lane
-    for (int m0 = w * 64; m0 < a.M; m0 += 1024) {
-        const int m = m0 + lane;
-        const int id = m < a.M ? adapter_of(a, a.ids[m]) : -1;
-        uint64_t todo = __ballot(m < a.M);
-        int place = 0, lead = 0, count = 0;
+    // atomic of the round's first lane; a thread's first rows stay in registers
+    int ids[kHeldRows], places[kHeldRows];
+    auto count = [&](int id, bool live) {
+        uint64_t todo = __ballot(live);
+        int place = 0, lead = 0, rows = 0;
         while (todo) {
             const int l = __ffsll((unsigned long long)todo) - 1;
             const uint64_t same = __ballot(id == __builtin_amdgcn_readlane(id, l));
             if (same >> lane & 1) {
                 place = __popcll(same & ((1ull << lane) - 1));
-                count = __popcll(same);
+                rows = __popcll(same);
                 lead = l;
             }
             todo &= ~same;
         }
         int before = 0;
-        if (m < a.M && place == 0) before = (int)atomicAdd(&cnt[id], (uint32_t)count);
-        before = __shfl(before, lead);
-        if (m < a.M) a.place[m] = before + place;
+        if (live && place == 0) before = (int)atomicAdd(&cnt[id], (uint32_t)rows);
+        return __shfl(before, lead) + place;
+    };
+#pragma unroll
+    for (int q = 0; q < kHeldRows; ++q) {
+        const int m = q * 1024 + tid;
+        ids[q] = m < a.M ? adapter_of(a, a.ids[m]) : -1;
+    }
+#pragma unroll
+    for (int q = 0; q < kHeldRows; ++q)
+        if (q * 1024 + w * 64 < a.M) places[q] = count(ids[q], ids[q] >= 0);
+    for (int m0 = kHeldRows * 1024 + w * 64; m0 < a.M; m0 += 1024) {
+        const int m = m0 + lane;
+        const int place = count(m < a.M ? adapter_of(a, a.ids[m]) : -1, m < a.M);
+        if (m < a.M) a.place[m] = place;
     }
     __syncthreads();
     // exclusive sums of the rows and of the tiles, a run of adapters per thread
@@ -566,10 +660,10 @@ __global__ __launch_bounds__(1024) void group_kernel(LoraLaunch a, int tile_rows
     }
     if (tid == 1023) a.tile_count[0] = (int)q;   // the last run ends after every tile
     __syncthreads();
-    for (int m0 = w * 64; m0 < a.M; m0 += 1024) {
-        const int m = m0 + lane;
-        if (m < a.M) a.perm[cnt[adapter_of(a, a.ids[m])] + a.place[m]] = m;
-    }
+#pragma unroll
+    for (int q = 0; q < kHeldRows; ++q)
+        if (ids[q] >= 0) a.perm[cnt[ids[q]] + places[q]] = q * 1024 + tid;
+    for (int m = kHeldRows * 1024 + tid; m < a.M; m += 1024) a.perm[cnt[adapter_of(a, a.ids[m])] + a.place[m]] = m;
 }
 
 }  // namespace
@@ -578,7 +672,22 @@ __global__ __launch_bounds__(1024) void group_kernel(LoraLaunch a, int tile_rows
 
 constexpr int kWideFrom = 1024;   // rows from which tiles are wide
 
+// One launch for both products: where a row's A is small, so that reading it
+// in every workgroup costs less than a second launch.  In elements of A: a
+// row's, all rows', and what all workgroups read together.  Inside these
+// bounds 4.1 us against 7.3 (rank 16, 4096 x 2048, 1 row), 6.0 against 8.7
+// (rank 16, 10240 x 5120, 4 rows), 8.5 against 9.7 (rank 64, 4096 x 2048, 2);
+// outside 10.4 against 8.7 (rank 16, 10240 x 5120, 8 rows), 9.7 against 8.4
+// (rank 32, 4096 x 2048, 16).
+static bool few_rows(int M, int N, int K, int max_rank) {
+    if (M > 16 || max_rank > 64) return false;
+    const int lanes = max_rank <= 8 ? 1 : max_rank <= 16 ? 2 : max_rank <= 32 ? 4 : 8;   // of a column
+    const int64_t one = (int64_t)K * max_rank, groups = (int64_t)M * ((N + 512 / lanes - 1) / (512 / lanes));
+    return one <= 1 << 17 && M * one <= 1 << 19 && groups * one <= 1 << 24;
+}
+
 void lora_plan(int M, int N, int K, int adapters, int max_rank, bool f32, LoraPlan *p) {
+    p->few = few_rows(M, N, K, max_rank);
     p->sorted = M > kDirectRows;
     p->wide = M >= kWideFrom;
     const int tile_rows = p->wide ? kWideRows : 16;
@@ -665,8 +774,22 @@ static void launch_expand_any(const LoraPlan &p, const LoraLaunch &a, hipStream_
     }
 }
 
+template <int P>
+static void launch_few_rows(bool f32, const LoraLaunch &a, hipStream_t s) {
+    const dim3 grid((a.N + 512 / P - 1) / (512 / P), a.M), block(512);
+    if (f32) hipLaunchKernelGGL((few_rows_kernel<P, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((few_rows_kernel<P, false>), grid, block, 0, s, a);
+}
+
 hipError_t launch_lora(const LoraPlan &p, bool f32, const LoraLaunch &a, hipStream_t s) {
     hipError_t e = hipSuccess;
+    if (p.few) {
+        if (a.max_rank <= 8) launch_few_rows<1>(f32, a, s);
+        else if (a.max_rank <= 16) launch_few_rows<2>(f32, a, s);
+        else if (a.max_rank <= 32) launch_few_rows<4>(f32, a, s);
+        else launch_few_rows<8>(f32, a, s);
+        return hipGetLastError();
+    }
     if (p.sorted) {
         hipLaunchKernelGGL(group_kernel, dim3(1), dim3(1024), 0, s, a, p.wide ? kWideRows : 16);
         e = hipGetLastError();
