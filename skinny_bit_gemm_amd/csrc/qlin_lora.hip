@@ -34,6 +34,21 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, p);
 }
 
+// A fragment of the matrix cores has lane 16 c + r hold chunk c (16 bytes, 8
+// numbers of the common axis) of row r.  Loaded like that, neighbouring lanes
+// lie in different rows and each is an access of its own: 64 clocks of a
+// compute unit's address unit for a wave's KiB.  So lane 4 r + c loads it,
+// four lanes for 64 consecutive bytes (16 clocks), and the lanes change
+// places.
+__device__ __forceinline__ uint4 to_fragment(uint4 v, int from) {
+    return make_uint4((uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v.x),
+                      (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v.y),
+                      (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v.z),
+                      (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v.w));
+}
+// the lane whose chunk becomes this lane's, in bytes
+__device__ __forceinline__ int fragment_source(int lane) { return ((lane & 15) * 4 + (lane >> 4)) * 4; }
+
 __device__ __forceinline__ int adapter_of(const LoraLaunch &a, int id) {
     return (unsigned)id < (unsigned)a.adapters ? id : a.adapters;
 }
@@ -112,16 +127,18 @@ __global__ __launch_bounds__(64 * NW) void shrink_kernel(LoraLaunch a) {
     if (t.count == 0 || rank0 >= rank_of(a, t.adapter)) return;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int c16 = lane & 15, kg = lane >> 4;
+    // this lane's part of the loads: row lane / 4, chunk lane % 4
+    const int from = fragment_source(lane), lrow = lane >> 2, lk = (lane & 3) * 8;
     const uint16_t *xp[CT], *ap[RT];
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
-        const int i = c * 16 + c16;
-        xp[c] = a.x + (int64_t)member[i < t.count ? i : 0] * a.ldx + kg * 8;
+        const int i = c * 16 + lrow;
+        xp[c] = a.x + (int64_t)member[i < t.count ? i : 0] * a.ldx + lk;
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-        const int rank = min(rank0 + r * 16 + c16, a.max_rank - 1);
-        ap[r] = a.A + ((int64_t)t.adapter * a.max_rank + rank) * a.K + kg * 8;
+        const int rank = min(rank0 + r * 16 + lrow, a.max_rank - 1);
+        ap[r] = a.A + ((int64_t)t.adapter * a.max_rank + rank) * a.K + lk;
     }
     v4f acc[CT][RT] = {};
     const int s0 = (split * NW + w) * a.k_steps;
@@ -129,7 +146,7 @@ __global__ __launch_bounds__(64 * NW) void shrink_kernel(LoraLaunch a) {
 #pragma unroll 4
     for (int s = s0; s < s1; ++s) {
         const int k = s * 32;
-        const bool in = k + kg * 8 < a.K;   // K is a multiple of 16
+        const bool in = k + lk < a.K;   // K is a multiple of 16
         uint4 av[RT], xv[CT];
 #pragma unroll
         for (int r = 0; r < RT; ++r)
@@ -137,6 +154,10 @@ __global__ __launch_bounds__(64 * NW) void shrink_kernel(LoraLaunch a) {
 #pragma unroll
         for (int c = 0; c < CT; ++c)
             xv[c] = in ? *reinterpret_cast<const uint4 *>(xp[c] + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) av[r] = to_fragment(av[r], from);
+#pragma unroll
+        for (int c = 0; c < CT; ++c) xv[c] = to_fragment(xv[c], from);
 #pragma unroll
         for (int c = 0; c < CT; ++c)
 #pragma unroll
@@ -232,19 +253,19 @@ __global__ __launch_bounds__(256, 4) void expand_kernel(LoraLaunch a) {
     const int64_t m = member[in_tile ? c16 : 0], yrow = m * a.ldy, brow = m * a.ldb;
     const int quarter = a.n_chunk / 4;
     const int n_begin = blockIdx.x * a.n_chunk + w * quarter, n_end = min(a.N, n_begin + quarter);
-    // D's row 4 kg + i of tile j is column col(j) + i, and the lane that loads
-    // that row of B is c16 = 4 kg + i
+    // D's row 4 kg + i of tile j is column col(j, kg) + i, and so is row 4 kg + i
+    // of its fragment of B
     auto col = [&](int j, int g) { return F32 ? j * 16 + g * 4 : g * 8 + j * 4; };
-    const uint16_t *bp[2];   // this lane's B row of tile j, at the wave's first column
+    const int from = fragment_source(lane), lrow = lane >> 2, lrank = (lane & 3) * 8;
+    const uint16_t *bp[2];   // the B row of tile j that this lane loads from, at the call's first column
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-        bp[j] = a.B + ((int64_t)t.adapter * a.N + col(j, c16 >> 2) + (c16 & 3)) * a.max_rank + kg * 8;
+        bp[j] = a.B + ((int64_t)t.adapter * a.N + col(j, lrow >> 2) + (lrow & 3)) * a.max_rank + lrank;
     auto load_b = [&](int n, int q, uint4 (&b)[2]) {
-        const int rank = q * 32 + kg * 8;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             b[j] = make_uint4(0, 0, 0, 0);
-            if (rank < ranks && n + col(j, c16 >> 2) + (c16 & 3) < a.N)
+            if (q * 32 + lrank < ranks && n + col(j, lrow >> 2) + (lrow & 3) < a.N)
                 b[j] = *reinterpret_cast<const uint4 *>(bp[j] + (int64_t)n * a.max_rank + q * 32);
         }
     };
@@ -309,6 +330,8 @@ __global__ __launch_bounds__(256, 4) void expand_kernel(LoraLaunch a) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) b[j] = b_now[RK == 1 ? 0 : q][j];
             }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) b[j] = to_fragment(b[j], from);
             clear_past(q, b);
 #pragma unroll
             for (int e = TERMS - 1; e >= 0; --e) {
