@@ -57,7 +57,7 @@ __device__ __forceinline__ int rank_of(const LoraLaunch &a, int adapter) {
     return a.ranks ? min(max(a.ranks[adapter], 0), a.max_rank) : a.max_rank;
 }
 
-constexpr int shrink_waves(int ct) { return ct == 4 ? 4 : 8; }   // of a shrink workgroup of 16 ct rows
+constexpr int kShrinkWaves = 8;   // of a shrink workgroup
 
 constexpr int kWideRows = 64;   // rows of a wide tile
 
@@ -718,12 +718,13 @@ void lora_plan(int M, int N, int K, int adapters, int max_rank, bool f32, LoraPl
     p->rt = max_rank <= 16 ? 1 : max_rank <= 32 ? 2 : 4;
     p->rank_chunks = (max_rank + 16 * p->rt - 1) / (16 * p->rt);
     p->v_stride = (max_rank + 15) / 16 * 16;
-    // K parts: one or two workgroups for each compute unit, at most four parts
-    // (the expand kernel reads them all for each of its column runs), two
-    // steps of 32 or more for each wave
-    p->shrink_ct = !p->wide ? 1 : p->rt == 1 ? 1 : p->rt == 2 ? 2 : 4;
+    // K parts: two workgroups for each compute unit, two steps of 32 or more
+    // for each wave; at most four parts, two for wide tiles (every expand
+    // workgroup reads them all: 4096 rows of rank 64, 70.1 us with two, 71.6
+    // with four)
+    p->shrink_ct = p->wide && p->rt > 1 ? 2 : 1;
     p->sub_tiles = tile_rows / (16 * p->shrink_ct);
-    const int steps = (K + 31) / 32, waves = shrink_waves(p->shrink_ct);
+    const int steps = (K + 31) / 32, waves = kShrinkWaves;
     const int groups = std::min(adapters, M);
     // about how many tiles there are: full ones, or one for each adapter
     const int tiles = std::max((M + tile_rows - 1) / tile_rows, groups);
@@ -734,13 +735,13 @@ void lora_plan(int M, int N, int K, int adapters, int max_rank, bool f32, LoraPl
     splits = std::max(std::min(splits, steps / (2 * waves)), 1);
     p->k_steps = (steps + waves * splits - 1) / (waves * splits);
     p->splits = (steps + waves * p->k_steps - 1) / (waves * p->k_steps);
-    // columns per expand workgroup: four stages, or runs as long as leave four
-    // workgroups for each compute unit
+    // columns per expand workgroup: four stages of the wide kernel, or runs
+    // as long as leave eight workgroups for each compute unit
     int n_chunk = 256;
     if (p->wide) {
         n_chunk = f32 ? 256 : 512;
     } else {
-        while (n_chunk < 4096 && (int64_t)((N + 2 * n_chunk - 1) / (2 * n_chunk)) * tiles >= 4 * kComputeUnits) n_chunk *= 2;
+        while (n_chunk < 4096 && (int64_t)((N + 2 * n_chunk - 1) / (2 * n_chunk)) * tiles >= 8 * kComputeUnits) n_chunk *= 2;
     }
     p->n_chunk = n_chunk;
     auto align = [](size_t v) { return (v + 255) & ~size_t(255); };
@@ -762,7 +763,7 @@ void lora_plan(int M, int N, int K, int adapters, int max_rank, bool f32, LoraPl
 
 template <int CT, int RT>
 static void launch_shrink(const LoraPlan &p, const LoraLaunch &a, hipStream_t s) {
-    constexpr int NW = shrink_waves(CT);
+    constexpr int NW = kShrinkWaves;
     const dim3 grid(p.splits, p.max_tiles * a.sub_tiles, p.rank_chunks), block(64 * NW);
     if (p.sorted) hipLaunchKernelGGL((shrink_kernel<CT, RT, NW, true>), grid, block, 0, s, a);
     else if constexpr (CT == 1) hipLaunchKernelGGL((shrink_kernel<CT, RT, NW, false>), grid, block, 0, s, a);
@@ -818,9 +819,9 @@ hipError_t launch_lora(const LoraPlan &p, bool f32, const LoraLaunch &a, hipStre
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (p.rt == 1) p.shrink_ct == 1 ? launch_shrink<1, 1>(p, a, s) : launch_shrink<1, 1>(p, a, s);
+    if (p.rt == 1) launch_shrink<1, 1>(p, a, s);
     else if (p.rt == 2) p.shrink_ct == 1 ? launch_shrink<1, 2>(p, a, s) : launch_shrink<2, 2>(p, a, s);
-    else p.shrink_ct == 1 ? launch_shrink<1, 4>(p, a, s) : launch_shrink<4, 4>(p, a, s);
+    else p.shrink_ct == 1 ? launch_shrink<1, 4>(p, a, s) : launch_shrink<2, 4>(p, a, s);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (f32) launch_expand_any<true>(p, a, s);

@@ -129,6 +129,21 @@ def test_many_rows(R, out):
     check(2100, 80, 96, 3, R, out=out, used="runs", rows=60)
 
 
+def test_more_rows_than_the_sort_holds():
+    """Rows past the 4096 that the sorting workgroup keeps in registers."""
+    for used in ("mixed", "runs"):
+        check(9001, 48, 64, 37, 8, used=used, rows=120)
+    check(5000, 32, 32, 4096, 16, rows=80, out=F32)
+
+
+@pytest.mark.parametrize("M", [1, 3, 16])
+@pytest.mark.parametrize("R", [8, 16, 24, 40, 64])
+def test_few_rows_of_small_adapters(M, R):
+    check(M, 528, 272, 3, R, out=F32, base="y", pad=8)
+    check(M, 48, 1040, 5, R, used="one")
+    check(M, 1040, 528, 4, R, base=None, use_scales=False)
+
+
 def test_defaults_and_many_adapters():
     check(40, 64, 64, 3, 16, use_ranks=False)
     check(40, 64, 64, 3, 16, use_scales=False)
