@@ -25,7 +25,9 @@ constexpr float kFltMax = 3.402823466e38f;
 // one DPP step of a maximum, a minimum or a sum (see max_dpp)
 template <int CTRL, int ROW_MASK = 0xF>
 __device__ __forceinline__ uint32_t moved_dpp(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, ROW_MASK, 0xF, false);
+    if constexpr (ROW_MASK == 0xF)   // every lane has a partner: nothing of the old value is needed
+        return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+    else return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, ROW_MASK, 0xF, false);
 }
 template <int CTRL>
 __device__ __forceinline__ float moved_dpp(float v) { return __uint_as_float(moved_dpp<CTRL, 0xF>(__float_as_uint(v))); }
@@ -328,6 +330,13 @@ __device__ __forceinline__ C row_max(C v) {
     return larger(v, moved_dpp<0x140>(v));
 }
 
+// What a score becomes once its expert is taken: the lowest float, or a double
+// below -2^1023 whose low word stays as it was.
+__device__ __forceinline__ float taken(bool now, float c) { return now ? -INFINITY : c; }
+__device__ __forceinline__ double taken(bool now, double c) {
+    return __hiloint2double(now ? (int)0xFFEFFFFF : __double2hiint(c), __double2loint(c));
+}
+
 // 1 / d for d >= 1: two Newton steps from the hardware's estimate (within
 // 2^-20 of itself or better, so within 2^-52 after them); 0 for infinity
 __device__ __forceinline__ double recip(double d) {
@@ -345,6 +354,7 @@ template <int EPL, bool WIDE>
 __device__ __forceinline__ void route_row(const RouteLaunch &a, int t, bool live, int lane, int &my_id, float &my_w) {
     using C = std::conditional_t<WIDE, double, float>;
     constexpr C kClosed = -INFINITY;
+    constexpr C kTaken = WIDE ? (C)-0x1p1023 : (C)-INFINITY;   // no score is this low
     float l[EPL];
     C c[EPL];
     load_logits<16>(a, t, live, lane, l);
@@ -429,9 +439,8 @@ __device__ __forceinline__ void route_row(const RouteLaunch &a, int t, bool live
         best = row_max(best);
         const uint32_t at = first_with<16>(c, best, lane);
 #pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            if (at == (uint32_t)(lane + 16 * j)) c[j] = kClosed;
-        if (lane == i && best > kClosed) my_id = (int)at;
+        for (int j = 0; j < EPL; ++j) c[j] = taken(at == (uint32_t)(lane + 16 * j), c[j]);
+        if (lane == i && best > kTaken) my_id = (int)at;
     }
     float my_l = -INFINITY;
     if (my_id >= 0) {
