@@ -122,9 +122,12 @@ template <int CT, int RT, int NW, bool SORTED>
 __global__ __launch_bounds__(64 * NW) void shrink_kernel(LoraLaunch a) {
     __shared__ int member[16 * CT];
     __shared__ v4f part[NW][RT][64];
-    const int split = blockIdx.x, rank0 = blockIdx.z * 16 * RT;
-    const Tile t = find_tile<CT, SORTED>(a, blockIdx.y / a.sub_tiles, blockIdx.y % a.sub_tiles, member);
-    if (t.count == 0 || rank0 >= rank_of(a, t.adapter)) return;
+    // grid x: K part, then row tile's part (2^20 rows are more than grid y holds)
+    const int split = blockIdx.x % a.splits, part_of = blockIdx.x / a.splits, rank0 = blockIdx.y * 16 * RT;
+    const Tile t = find_tile<CT, SORTED>(a, part_of / a.sub_tiles, part_of % a.sub_tiles, member);
+    // (the first ranks are computed whether the adapter has them or not: their
+    // loads do not wait for its rank)
+    if (t.count == 0 || t.adapter >= a.adapters || (rank0 > 0 && rank0 >= rank_of(a, t.adapter))) return;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int c16 = lane & 15, kg = lane >> 4;
     // this lane's part of the loads: row lane / 4, chunk lane % 4
@@ -261,11 +264,14 @@ __global__ __launch_bounds__(256, 4) void expand_kernel(LoraLaunch a) {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
         bp[j] = a.B + ((int64_t)t.adapter * a.N + col(j, lrow >> 2) + (lrow & 3)) * a.max_rank + lrank;
+    // single tokens load what max_rank covers, without waiting for the rank;
+    // sorted rows, where B's bytes are what takes the time, only the adapter's
+    const int loaded = SORTED ? ranks : t.adapter < a.adapters ? a.max_rank : 0;
     auto load_b = [&](int n, int q, uint4 (&b)[2]) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             b[j] = make_uint4(0, 0, 0, 0);
-            if (q * 32 + lrank < ranks && n + col(j, lrow >> 2) + (lrow & 3) < a.N)
+            if (q * 32 + lrank < loaded && n + col(j, lrow >> 2) + (lrow & 3) < a.N)
                 b[j] = *reinterpret_cast<const uint4 *>(bp[j] + (int64_t)n * a.max_rank + q * 32);
         }
     };
@@ -559,8 +565,10 @@ __global__ __launch_bounds__(512) void few_rows_kernel(LoraLaunch a) {
     const int n = blockIdx.x * PER + tid / P, rank0 = tid % P * 8;
     const int64_t at = (int64_t)m * a.ldy + n;
     const bool first = tid % P == 0 && n < a.N;
+    // A and B are loaded as far as max_rank, without waiting for the rank
+    const int loaded = adapter < a.adapters ? a.max_rank : 0;
     uint4 b = make_uint4(0, 0, 0, 0);
-    if (n < a.N && rank0 < ranks)
+    if (n < a.N && rank0 < loaded)
         b = *reinterpret_cast<const uint4 *>(a.B + ((int64_t)adapter * a.N + n) * a.max_rank + rank0);
     float base = 0.0f;
     if (first && a.base) {
@@ -572,7 +580,7 @@ __global__ __launch_bounds__(512) void few_rows_kernel(LoraLaunch a) {
     const uint16_t *x = a.x + (int64_t)m * a.ldx;
     for (int r = w; r < 8 * P; r += 8) {
         float sum = 0.0f;
-        if (r < ranks) {
+        if (r < loaded) {
             const uint16_t *row = a.A + ((int64_t)adapter * a.max_rank + r) * a.K;
 #pragma unroll 4
             for (int k = lane * 8; k < a.K; k += 512) {
@@ -719,9 +727,11 @@ void lora_plan(int M, int N, int K, int adapters, int max_rank, bool f32, LoraPl
     p->rank_chunks = (max_rank + 16 * p->rt - 1) / (16 * p->rt);
     p->v_stride = (max_rank + 15) / 16 * 16;
     // K parts: two workgroups for each compute unit, two steps of 32 or more
-    // for each wave; at most four parts, two for wide tiles (every expand
-    // workgroup reads them all: 4096 rows of rank 64, 70.1 us with two, 71.6
-    // with four)
+    // for each wave.  At most four parts, two for wide tiles: every expand
+    // workgroup reads them all (4096 rows of rank 64: 70.1 us with two, 71.6
+    // with four).  Up to 32 rows eight, as many as let a wave's loads leave at
+    // once (16 rows of rank 64, K 12288: 15.5 us against 18.0; 64 rows of rank
+    // 64, K 12288: 36.1 against 33.3).
     p->shrink_ct = p->wide && p->rt > 1 ? 2 : 1;
     p->sub_tiles = tile_rows / (16 * p->shrink_ct);
     const int steps = (K + 31) / 32, waves = kShrinkWaves;
@@ -730,7 +740,7 @@ void lora_plan(int M, int N, int K, int adapters, int max_rank, bool f32, LoraPl
     const int tiles = std::max((M + tile_rows - 1) / tile_rows, groups);
     const int shrink_tiles = std::max((M + 16 * p->shrink_ct - 1) / (16 * p->shrink_ct), groups);
     int splits = 2 * kComputeUnits / (shrink_tiles * p->rank_chunks);
-    const int cap = p->wide ? 2 : 4;
+    const int cap = p->wide ? 2 : M > 32 ? 4 : std::min(std::max(steps / (4 * waves), 4), 8);
     splits = std::min(std::max(splits, 1), cap);
     splits = std::max(std::min(splits, steps / (2 * waves)), 1);
     p->k_steps = (steps + waves * splits - 1) / (waves * splits);
@@ -764,7 +774,7 @@ void lora_plan(int M, int N, int K, int adapters, int max_rank, bool f32, LoraPl
 template <int CT, int RT>
 static void launch_shrink(const LoraPlan &p, const LoraLaunch &a, hipStream_t s) {
     constexpr int NW = kShrinkWaves;
-    const dim3 grid(p.splits, p.max_tiles * a.sub_tiles, p.rank_chunks), block(64 * NW);
+    const dim3 grid(p.splits * p.max_tiles * p.sub_tiles, p.rank_chunks), block(64 * NW);
     if (p.sorted) hipLaunchKernelGGL((shrink_kernel<CT, RT, NW, true>), grid, block, 0, s, a);
     else if constexpr (CT == 1) hipLaunchKernelGGL((shrink_kernel<CT, RT, NW, false>), grid, block, 0, s, a);
 }

@@ -129,6 +129,30 @@ def test_many_rows(R, out):
     check(2100, 80, 96, 3, R, out=out, used="runs", rows=60)
 
 
+@pytest.mark.parametrize("R", [16, 24, 40, 72, 136, 256])
+@pytest.mark.parametrize("out", [BF16, F32], ids=["bf16", "f32"])
+def test_wide_tiles_at_odd_ranks(R, out):
+    """64-row tiles whose ranks do not fill a stage, or fill several; a last stage and a tile that are not whole."""
+    check(1024 + 37, 528, 144, 3, R, out=out, rows=40, pad=8, base="y")
+    check(1100, 1296, 80, 2, R, out=out, used="one", rows=30, base=None)
+
+
+def test_the_largest_row_count():
+    """2^20 rows: more row tiles than a grid's y holds."""
+    M, N, K, n, R = 1 << 20, 16, 16, 2, 8
+    x = torch.ones(M, K, dtype=torch.bfloat16, device=DEV)
+    A = torch.ones(n, R, K, dtype=torch.bfloat16, device=DEV)
+    B = torch.ones(n, N, R, dtype=torch.bfloat16, device=DEV)
+    B[1] = 2.0
+    ids = torch.arange(M, dtype=torch.int32, device=DEV) % 3        # adapter 2: none
+    y = torch.full((M, N), -1.0, device=DEV)
+    work = torch.empty(q.qlin_lora_workspace_bytes(M, N, K, n, R), dtype=torch.uint8, device=DEV)
+    q.qlin_lora(M, N, K, n, R, x, K, ids, A, B, None, None, None, 0, y, N, F32, work)
+    torch.cuda.synchronize()
+    want = torch.tensor([128.0, 256.0, 0.0], device=DEV)[ids.long()]
+    assert (y == want[:, None]).all()
+
+
 def test_more_rows_than_the_sort_holds():
     """Rows past the 4096 that the sorting workgroup keeps in registers."""
     for used in ("mixed", "runs"):

@@ -315,6 +315,17 @@ def test_combine_keeps_infinities_and_nan_in_their_rows():
     assert (y == 2.0).all()
 
 
+def test_combine_more_tokens_than_a_grid_row():
+    T, N = 70001, 32
+    h = torch.arange(T, device=DEV, dtype=torch.float32)[:, None].expand(T, N).contiguous()
+    slots = torch.arange(T - 1, -1, -1, dtype=torch.int32, device=DEV)
+    w = torch.full((T, 1), 2.0, device=DEV)
+    y = torch.empty(T, N, device=DEV)
+    q.qlin_combine(T, 1, N, h, N, F32, slots, w, T, h, N, y, N, F32)
+    torch.cuda.synchronize()
+    assert torch.equal(y, h.flip(0) * 2 + h)
+
+
 def test_combine_rows_far_apart():
     """Row offsets past 2^32 bytes, in the rows read and the rows written."""
     N, ld = 32, (1 << 30) + 64
