@@ -158,9 +158,7 @@ def lib():
 
 
 def _ptr(t) -> int | None:
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 
@@ -173,15 +171,22 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
+_raw_stream = None
+
+
 def _current_stream() -> int:
     """torch's current stream on the current device, as a raw handle.  The raw
     getters take 0.2 us, building a Stream object of it 2.9 us: as long as a
     launch."""
-    import torch
-    try:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    except AttributeError:
-        return torch.cuda.current_stream().cuda_stream
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        try:
+            of, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            _raw_stream = lambda: of(device())  # noqa: E731
+        except AttributeError:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _raw_stream()
 
 
 def _nbytes(t) -> int:
