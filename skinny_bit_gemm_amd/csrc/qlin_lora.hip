@@ -185,6 +185,13 @@ __global__ __launch_bounds__(64 * NW) void shrink_kernel(LoraLaunch a) {
     }
 }
 
+// What bf16 number `hi` leaves of f; nothing where it is infinite (inf - inf
+// would turn an infinite product into NaN).
+__device__ __forceinline__ float left_of(float f, float hi) {
+    const float r = f - hi;
+    return __builtin_fabsf(r) < INFINITY ? r : 0.0f;
+}
+
 // Four numbers as TERMS bf16 numbers each that add up to them: each takes 8
 // more bits of the mantissa.
 template <int TERMS>
@@ -192,10 +199,10 @@ __device__ __forceinline__ void split4(v4f f, uint2 (&out)[TERMS]) {
 #pragma unroll
     for (int e = 0; e < TERMS; ++e) {
         out[e] = make_uint2(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]));
-        f[0] -= bf16_lo(out[e].x);
-        f[1] -= bf16_hi(out[e].x);
-        f[2] -= bf16_lo(out[e].y);
-        f[3] -= bf16_hi(out[e].y);
+        f[0] = left_of(f[0], bf16_lo(out[e].x));
+        f[1] = left_of(f[1], bf16_hi(out[e].x));
+        f[2] = left_of(f[2], bf16_lo(out[e].y));
+        f[3] = left_of(f[3], bf16_hi(out[e].y));
     }
 }
 

@@ -213,6 +213,26 @@ def test_a_bad_row_stays_alone():
         assert np.isnan(outs[1][7]).all()
 
 
+@pytest.mark.parametrize("M", [2, 40, 90, 1100])
+@pytest.mark.parametrize("out", [BF16, F32], ids=["bf16", "f32"])
+def test_an_infinite_row(M, out):
+    """An infinity in x of a row with an adapter of rank 1 leaves nothing to cancel: y is infinite, signed by B's columns."""
+    N, K, R = 64, 96, 16
+    x, A, B, ids, ranks, scales = make(M, N, K, 3, R, 6, "one")
+    ranks[0] = 1
+    x[1, 5] = 0x7F80
+    assert (A[0, 0, 5] & 0x7FFF) and (B[0, :, 0] & 0x7FFF).all()
+    y = torch.zeros(M, N, dtype=torch.float32 if out == F32 else torch.int16, device=DEV)
+    work = torch.empty(q.qlin_lora_workspace_bytes(M, N, K, 3, R), dtype=torch.uint8, device=DEV)
+    q.qlin_lora(M, N, K, 3, R, to_dev_bf16(x), K, to_dev(ids), to_dev_bf16(A), to_dev_bf16(B), to_dev(ranks),
+                to_dev(scales), None, 0, y, N, out, work)
+    torch.cuda.synchronize()
+    got = y.cpu().numpy() if out == F32 else f32_of(y.cpu().numpy().view(np.uint16))
+    sign = np.sign(f32_of(A[0, 0, 5:6])[0] * f32_of(B[0, :, 0]))
+    assert np.array_equal(got[1], sign * np.inf)
+    assert np.isfinite(np.delete(got, 1, 0)).all()
+
+
 @pytest.mark.parametrize("M", [33, 500])
 def test_same_bits_again_and_for_any_neighbours(M):
     """A second call gives the same bits, and so do the same rows when the
