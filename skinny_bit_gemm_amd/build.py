@@ -22,7 +22,8 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-munsafe-fp-a
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
           "-Wall", "-Wno-unused-function", "-Wno-unused-command-line-argument"]
 SOURCES = ["qlin_gemm_fp8.hip", "qlin_gemm_i8.hip", "qlin_gemm_block.hip", "qlin_kernels.hip",
-           "qlin_route.hip", "qlin_lora.hip", "qlin_api.cpp", "qlin_table.cpp"]
+           "qlin_route.hip", "qlin_expert_rows.hip", "qlin_lora.hip", "qlin_api.cpp", "qlin_table.cpp"]
+FLAGS = {"qlin_route.hip": ["-fno-honor-nans"]}   # why: see the file
 PROBE_SOURCES = ["qlin_probe.hip"]
 
 
@@ -39,7 +40,7 @@ def _compile(hipcc, srcs, verbose):
     for src in srcs:
         obj = os.path.join(OUT_DIR, os.path.splitext(src)[0] + ".o")
         lang = ["-x", "hip"] if src.endswith(".hip") else []
-        cmd = [hipcc, *COMMON, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
+        cmd = [hipcc, *COMMON, *FLAGS.get(src, []), *lang, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
