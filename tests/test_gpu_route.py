@@ -179,6 +179,17 @@ def test_route_prompts(E, groups, kept, score, steered):
                     renormalize=1 - top2)
 
 
+@pytest.mark.parametrize("E,groups,kept", [(48, 3, 2), (60, 1, 1), (128, 8, 4), (128, 1, 1), (256, 8, 4), (250, 1, 1)])
+@pytest.mark.parametrize("steered", [False, True], ids=["plain", "bias"])
+def test_route_around_the_block_sizes(E, groups, kept, steered):
+    """Around the token counts where the blocks of tokens change."""
+    bias = np.random.default_rng(E).normal(0, 0.05, E).astype(np.float32) if steered else None
+    for T in (31, 32, 33, 47, 48, 49, 63, 66, 4095, 4096, 4097, 6001):
+        l = logits_for(T, E, 41, False, 0.1)
+        l[T - 1], l[T // 2, ::3] = -INF, NAN
+        check_route(l, bias=bias, topk=5, score=SIG, groups=groups, topk_groups=kept, group_score=int(steered))
+
+
 def test_route_no_tokens():
     off = guarded((65,), torch.int32, -7)
     other = guarded((16,), torch.int32, -7)
