@@ -618,7 +618,7 @@ __global__ __launch_bounds__(512) void few_rows_kernel(LoraLaunch a) {
 // adapter's rows into tiles.  One workgroup.  The order of an adapter's rows
 // depends on which wave counts first; every row's result is the same in any
 // place of any tile.
-constexpr int kHeldRows = 4;
+constexpr int kHeldRows = 4, kRounds = 4;
 
 __global__ __launch_bounds__(1024) void group_kernel(LoraLaunch a, int tile_rows) {
     __shared__ uint32_t cnt[QLIN_MAX_ADAPTERS + 1];
@@ -627,14 +627,15 @@ __global__ __launch_bounds__(1024) void group_kernel(LoraLaunch a, int tile_rows
     const int n = a.adapters + 1;
     for (int i = tid; i < n; i += 1024) cnt[i] = 0;
     __syncthreads();
-    // each row's place among its adapter's rows: within the wave by ballots
-    // (one round for each adapter that the wave sees), across waves by one
-    // atomic of the round's first lane; a thread's first rows stay in registers
+    // each row's place among its adapter's rows: within the wave by ballots, a
+    // round for each of the first adapters that the wave sees (long runs have
+    // few), with one atomic of the round's first lane; the other rows by an
+    // atomic each.  A thread's first rows stay in registers.
     int ids[kHeldRows], places[kHeldRows];
     auto count = [&](int id, bool live) {
         uint64_t todo = __ballot(live);
-        int place = 0, lead = 0, rows = 0;
-        while (todo) {
+        int place = 0, lead = lane, rows = 1;
+        for (int round = 0; round < kRounds && todo; ++round) {
             const int l = __ffsll((unsigned long long)todo) - 1;
             const uint64_t same = __ballot(id == __builtin_amdgcn_readlane(id, l));
             if (same >> lane & 1) {
