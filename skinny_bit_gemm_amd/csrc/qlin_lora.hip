@@ -308,6 +308,12 @@ __global__ __launch_bounds__(256, 4) void expand_kernel(LoraLaunch a) {
             }
         }
     };
+    // many rows' y leaves with the non-temporal policy (see expand_wide_kernel;
+    // 2048 rows, 4096 columns of fp32, K 12288: 38 us against 44)
+    auto put = [](void *to, v4u v) {
+        if constexpr (SORTED) __builtin_nontemporal_store(v, static_cast<v4u *>(to));
+        else *static_cast<v4u *>(to) = v;
+    };
     constexpr int HELD = RK > 0 ? RK : 1;
     uint4 b_next[HELD][2], base_next[PARTS];
     if constexpr (RK > 0)
@@ -361,15 +367,15 @@ __global__ __launch_bounds__(256, 4) void expand_kernel(LoraLaunch a) {
             for (int h = 0; h < 2; ++h) {
                 const int at = n + col(h, kg);
                 if (at < n_end)
-                    *reinterpret_cast<v4f *>(static_cast<float *>(a.y) + yrow + at) =
-                        acc[h] + __builtin_bit_cast(v4f, base_now[h]);
+                    put(static_cast<float *>(a.y) + yrow + at,
+                        __builtin_bit_cast(v4u, acc[h] + __builtin_bit_cast(v4f, base_now[h])));
             }
         } else {
             const int at = n + col(0, kg);
             if (at < n_end)
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.y) + yrow + at) =
-                    add_pairs(base_now[0], acc[0][0], acc[0][1], acc[0][2], acc[0][3], acc[1][0], acc[1][1], acc[1][2],
-                              acc[1][3]);
+                put(static_cast<uint16_t *>(a.y) + yrow + at,
+                    __builtin_bit_cast(v4u, add_pairs(base_now[0], acc[0][0], acc[0][1], acc[0][2], acc[0][3], acc[1][0],
+                                                      acc[1][1], acc[1][2], acc[1][3])));
         }
     }
 }
@@ -709,7 +715,12 @@ __global__ __launch_bounds__(1024) void group_kernel(LoraLaunch a, int tile_rows
 
 // ---------------------------------------------------------------- planning
 
-constexpr int kWideFrom = 1024;   // rows from which tiles are wide
+// Rows from which tiles are wide (64 rows, each B row read once for them); a
+// call with fewer has too few such tiles for the compute units, and a smaller
+// rank has less of B to read again.  Narrow / wide, N 10240, K 5120: rank 8,
+// 1500 rows 0.98, 2500 0.90, 3000 1.13; rank 64, 1500 rows 1.00, 2048 1.09,
+// 3000 1.28; N = K = 4096: rank 16, 1024 rows 17.5 us against 23.6.
+static int wide_from(int max_rank) { return max_rank <= 16 ? 2400 : 1536; }
 
 // One launch for both products: where a row's A is small, so that reading it
 // in every workgroup costs less than a second launch.  In elements of A: a
@@ -728,7 +739,7 @@ static bool few_rows(int M, int N, int K, int max_rank) {
 void lora_plan(int M, int N, int K, int adapters, int max_rank, bool f32, LoraPlan *p) {
     p->few = few_rows(M, N, K, max_rank);
     p->sorted = M > kDirectRows;
-    p->wide = M >= kWideFrom;
+    p->wide = M >= wide_from(max_rank);
     const int tile_rows = p->wide ? kWideRows : 16;
     p->max_tiles = p->sorted ? (M + tile_rows - 1) / tile_rows + std::min(adapters + 1, M) : M;
     p->rt = max_rank <= 16 ? 1 : max_rank <= 32 ? 2 : 4;

@@ -137,6 +137,40 @@ def test_wide_tiles_at_odd_ranks(R, out):
     check(1100, 1296, 80, 2, R, out=out, used="one", rows=30, base=None)
 
 
+@pytest.mark.parametrize("R", [8, 16, 24, 32, 40, 64, 72, 136, 256])
+@pytest.mark.parametrize("out", [BF16, F32], ids=["bf16", "f32"])
+def test_prompts(R, out):
+    """Enough rows for 64-row tiles at every rank: odd counts, runs, single rows, tiles that are not whole."""
+    check(2400, 528, 144, 3, R, out=out, rows=40, pad=8, base="y")
+    check(2400 + 37, 592, 272, 40, R, out=out, rows=60, pad=8)
+    check(3001, 1296, 80, 9, R, out=out, used="runs", rows=30, base=None)
+
+
+@pytest.mark.parametrize("R", [16, 24])
+@pytest.mark.parametrize("M", [1535, 1536, 2399])
+def test_rows_where_the_tiles_change(M, R):
+    check(M, 272, 208, 5, R, rows=50, base="y")
+    check(M, 272, 208, 700, R, out=F32, rows=50)
+
+
+@pytest.mark.parametrize("R", [8, 32, 64, 80])
+def test_prompts_with_many_adapters_and_bad_rows(R):
+    check(2500, 32, 32, 4096, R, rows=80)
+    M, N, K = 2500, 64, 96
+    x, A, B, ids, ranks, scales = make(M, N, K, 3, R, 8, "one")
+    ranks[0] = 1
+    x[77, 5], x[78, 6] = 0x7F80, 0x7FC0
+    y = torch.zeros(M, N, device=DEV)
+    work = torch.empty(q.qlin_lora_workspace_bytes(M, N, K, 3, R), dtype=torch.uint8, device=DEV)
+    q.qlin_lora(M, N, K, 3, R, to_dev_bf16(x), K, to_dev(ids), to_dev_bf16(A), to_dev_bf16(B), to_dev(ranks),
+                to_dev(scales), None, 0, y, N, F32, work)
+    torch.cuda.synchronize()
+    got = y.cpu().numpy()
+    sign = np.sign(f32_of(A[0, 0, 5:6])[0] * f32_of(B[0, :, 0]))
+    assert np.array_equal(got[77], sign * np.inf) and np.isnan(got[78]).all()
+    assert np.isfinite(np.delete(got, [77, 78], 0)).all()
+
+
 def test_the_largest_row_count():
     """2^20 rows: more row tiles than a grid's y holds."""
     M, N, K, n, R = 1 << 20, 16, 16, 2, 8
