@@ -648,12 +648,12 @@ __global__ __launch_bounds__(kPlaceThreads) void place_kernel(RouteLaunch a) {
 // --------------------------------------------------------------- launchers
 
 // How a call runs.
-//   rows   16 lanes per token (route_row) instead of a wave: from 17 tokens
-//          on, where four tokens share an instruction (128 experts, 64 tokens:
-//          7.6 us against 10.4 in two launches; 256 in 8 groups, 128 tokens: 21
-//          against 25), and for a wave that would have a single number in a
-//          lane or a group at a time (256 in 8 groups, 16 tokens: 11 us against
-//          19; 128 experts, 1 token: 4.7 against 3.9)
+//   rows   16 lanes per token (route_row) instead of a wave: past 8 tokens,
+//          where four tokens share an instruction (256 experts with a bias,
+//          16 tokens: 7.1 us against 9.3; 4 tokens: 7.0 against 6.3), and for
+//          a wave that would have a single number in a lane or a group at a
+//          time (256 in 8 groups, 1 token: 8.7 us against 10.6, 4096 tokens:
+//          16.9 against 24.8; 60 experts, 64 tokens: 4.7 against 8.9)
 //   once   one launch for all tokens by one workgroup: 64 of them with 16
 //          lanes each (32 with groups, whose choice is longer: 256 in 8, 64
 //          tokens: 21 us against 15.6), 16 with a wave each
@@ -665,7 +665,7 @@ RoutePlan route_plan(const qlin_router &r, int T) {
     RoutePlan p = {};
     const int group = r.experts / r.groups;
     const bool fits = r.experts <= 256 && r.topk <= 16 && (r.groups == 1 || (r.groups <= 16 && group % 16 == 0));
-    p.rows = fits && (T > 16 || r.experts <= 64 || r.groups > 1);
+    p.rows = fits && (T > 8 || r.experts <= 64 || r.groups > 1);
     p.once = T <= (!p.rows ? 16 : r.groups > 1 ? 32 : 64);
     const int tokens = p.rows && T > 16 * kComputeUnits ? 32 : 16;
     p.block_tokens = tokens * ((T + tokens * 512 - 1) / (tokens * 512));

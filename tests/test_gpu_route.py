@@ -190,6 +190,17 @@ def test_route_around_the_block_sizes(E, groups, kept, steered):
         check_route(l, bias=bias, topk=5, score=SIG, groups=groups, topk_groups=kept, group_score=int(steered))
 
 
+@pytest.mark.parametrize("E", [60, 65, 128, 160, 256, 300])
+@pytest.mark.parametrize("steered", [False, True], ids=["plain", "bias"])
+def test_route_few_tokens(E, steered):
+    bias = np.random.default_rng(E).normal(0, 0.05, E).astype(np.float32) if steered else None
+    for T in (1, 2, 7, 8, 9, 16, 17):
+        l = logits_for(T, E, 51, True, 0.2)
+        l[T // 2, 1::2] = -INF
+        check_route(l, True, bias, topk=9, score=SIG)
+        check_route(l, True, bias, topk=3, renormalize=0)
+
+
 def test_route_no_tokens():
     off = guarded((65,), torch.int32, -7)
     other = guarded((16,), torch.int32, -7)
