@@ -444,6 +444,8 @@ qlin_status qlin_combine(int T, int topk, int N, const void *h, int64_t ldh, qli
  * views: column offsets in whole 16-byte units, ldb and ldy the wide one's.
  * Sums are fp32; the product A_a x is kept to at least 16 bits (24 for
  * QLIN_OUT_F32_ACC) of mantissa between the two products; y is rounded once.
+ * NaN and infinities in x reach y in their own row only; A and B, as far as
+ * the ranks go, are finite.
  * N % 16 == 0, K % 16 == 0, max_rank % 8 == 0 up to QLIN_MAX_RANK; leading
  * dimensions are whole 16-byte units; ldb is not looked at without base.
  *   workspace  qlin_lora_workspace_bytes(...) bytes; needs no initial value.
