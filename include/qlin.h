@@ -377,7 +377,7 @@ typedef struct {
  * than topk experts are open, the remaining choices have id -1, weight 0,
  * slot -1 and no row.
  * The weights: scale x s, or scale x s / (the sum of the token's chosen s),
- * 0 where that sum is 0.
+ * 0 where that sum is 0 in 64 bits (sigmoids of logits below -709.78).
  * Rows are in expert order and, within an expert, in token order.
  *   workspace  qlin_route_workspace_bytes(router, T) bytes (may be 0); needs
  *              no initial value.  Calls that overlap in time must not share it.

@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kPlaceThreads = 1024;
 constexpr float kFltMax = 3.402823466e38f;
+constexpr float kSigmoidZero = -709.782715f;   // e^709.782715 is past the largest double
 
 // ---------------------------------------------- reductions over a token's lanes
 //
@@ -162,7 +163,12 @@ __device__ __forceinline__ float weight_of(const RouteLaunch &a, const float (&l
         sum = token_sum<LPT>(sum);
         s = sum > 0.0f ? s / sum : 0.0f;
     } else {
-        s = mine ? 1.0f / (1.0f + expf(-my_l)) : 0.0f;
+        // renormalized: times e^-m (m: the largest chosen logit, if negative),
+        // which cancels and keeps what 32 bits would lose below -88.  What is 0
+        // in 64 bits, where 1 + e^-l overflows, is 0 here.
+        const float m = a.renormalize ? fminf(token_max<LPT>(my_l), 0.0f) : 0.0f;
+        const float e = expf(-fabsf(my_l));
+        s = mine && my_l > kSigmoidZero ? (my_l < 0.0f ? expf(my_l - m) : 1.0f) / (1.0f + e) : 0.0f;
         if (a.renormalize) {
             const float sum = token_sum<LPT>(s);
             s = sum > 0.0f ? s / sum : 0.0f;

@@ -201,6 +201,26 @@ def test_route_few_tokens(E, steered):
         check_route(l, True, bias, topk=3, renormalize=0)
 
 
+@pytest.mark.parametrize("E", [24, 70, 128, 300])
+@pytest.mark.parametrize("T", [3, 40, 90])
+@pytest.mark.parametrize("steered", [False, True], ids=["plain", "bias"])
+def test_route_sigmoid_of_low_logits(E, T, steered):
+    """Sigmoids far below what 32 bits hold still have a ratio: the renormalized weights are that."""
+    rng = np.random.default_rng([E, T])
+    bias = np.round(rng.normal(0, 0.05, E), 2).astype(np.float32) if steered else None
+    low = np.array([-80.0, -86.0, -90.0, -103.0, -120.0, -300.0, -700.0, -2000.0, 3.0])
+    for first in range(0, len(low), 3):      # few tokens see every level too
+        l = (low[(np.arange(T) + first) % len(low), None] - rng.uniform(0.0, 4.0, (T, E))).astype(np.float32)
+        l[0] = -INF
+        l[0, [3, 9]] = -100.0, -101.0
+        l[1, ::2] -= 5.0
+        l[2] = rng.uniform(-720.0, -700.0, E)    # on both sides of what is 0 in 64 bits, too
+        l[2, 5:8] = -709.7826, -709.7828, -710.0
+        for renorm in (1, 0):
+            check_route(l, bias=bias, topk=min(E, 8), score=SIG, renormalize=renorm, scale=2.5)
+            check_route(wl.bf16_bits_to_f32(to_bits(l)), True, bias, topk=3, score=SIG, renormalize=renorm)
+
+
 def test_route_no_tokens():
     off = guarded((65,), torch.int32, -7)
     other = guarded((16,), torch.int32, -7)
