@@ -615,7 +615,7 @@ __global__ __launch_bounds__(512) void few_rows_kernel(LoraLaunch a) {
     if constexpr (P > 1) y = y + moved<0xB1>(y);
     if constexpr (P > 2) y = y + moved<0x4E>(y);
     if constexpr (P > 4) y = y + moved<0x141>(y);
-    if (!first) return;
+    if (!first || (ranks == 0 && a.base == a.y)) return;   // a row without ranks is already there, every bit of it
     if constexpr (F32) static_cast<float *>(a.y)[at] = base + y;
     else static_cast<uint16_t *>(a.y)[at] = (uint16_t)bf16_pair(base + y, 0.0f);
 }

@@ -288,6 +288,27 @@ def test_same_bits_again_and_for_any_neighbours(M):
     assert np.array_equal(outs[0][::2], outs[2][::2])
 
 
+@pytest.mark.parametrize("M", [1, 5, 16, 40, 90, 2500, 4100])
+@pytest.mark.parametrize("out", [BF16, F32], ids=["bf16", "f32"])
+def test_rows_without_an_adapter_stay_as_they_are(M, out):
+    """In place, rows without an adapter and of rank 0 keep every bit: negative zeros and NaN payloads too."""
+    N, K, R = 80, 96, 16
+    x, A, B, ids, ranks, scales = make(M, N, K, 3, R, 9, "one")
+    ranks[1] = 0
+    ids[:] = np.arange(M) % 4 - 1                  # none, full rank, rank 0, some rank
+    rng = np.random.default_rng(M)
+    word, special = (np.uint16, [0x8000, 0x7F81, 0xFFC1, 0x8001]) if out == BF16 else (
+        np.uint32, [0x80000000, 0x7F800001, 0xFFC00001, 0x80000001])
+    before = rng.choice(np.array(special, dtype=word), (M, N))
+    y = to_dev(before.view(np.int16 if out == BF16 else np.int32))
+    work = torch.empty(q.qlin_lora_workspace_bytes(M, N, K, 3, R), dtype=torch.uint8, device=DEV)
+    q.qlin_lora(M, N, K, 3, R, to_dev_bf16(x), K, to_dev(ids), to_dev_bf16(A), to_dev_bf16(B), to_dev(ranks),
+                to_dev(scales), y, N, y, N, out, work)
+    torch.cuda.synchronize()
+    stay = (ids == -1) | (ids == 1)
+    assert np.array_equal(y.cpu().numpy().view(word)[stay], before[stay])
+
+
 def test_slices_of_a_wider_projection():
     """q, k, v: adapters for column ranges of one output, in place."""
     M, K, n, R, widths = 21, 256, 4, 16, (128, 64, 64)
