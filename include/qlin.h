@@ -448,8 +448,9 @@ qlin_status qlin_combine(int T, int topk, int N, const void *h, int64_t ldh, qli
  * the ranks go, are finite.
  * N % 16 == 0, K % 16 == 0, max_rank % 8 == 0 up to QLIN_MAX_RANK; leading
  * dimensions are whole 16-byte units; ldb is not looked at without base.
- *   workspace  qlin_lora_workspace_bytes(...) bytes; needs no initial value.
- *              Calls that overlap in time must not share it.
+ *   workspace  qlin_lora_workspace_bytes(...) bytes, which never shrink as M
+ *              grows: one for the most rows serves fewer.  Needs no initial
+ *              value.  Calls that overlap in time must not share it.
  * M may be 0.  A row's result depends on the call's sizes and on the row's
  * own data, not on which adapters the other rows have.
  * Errors: QLIN_ERR_INVALID_ARG (a null pointer, an unknown type), QLIN_ERR_SHAPE

@@ -759,9 +759,9 @@ void lora_plan(int M, int N, int K, int adapters, int max_rank, bool f32, LoraPl
     const int tiles = std::max((M + tile_rows - 1) / tile_rows, groups);
     const int shrink_tiles = std::max((M + 16 * p->shrink_ct - 1) / (16 * p->shrink_ct), groups);
     int splits = 2 * kComputeUnits / (shrink_tiles * p->rank_chunks);
-    const int cap = p->wide ? 2 : M > 32 ? 4 : std::min(std::max(steps / (4 * waves), 4), 8);
-    splits = std::min(std::max(splits, 1), cap);
-    splits = std::max(std::min(splits, steps / (2 * waves)), 1);
+    const int few_cap = std::min(std::max(steps / (4 * waves), 4), 8), most = std::max(steps / (2 * waves), 1);
+    const int cap = p->wide ? 2 : M > 32 ? 4 : few_cap;
+    splits = std::min({std::max(splits, 1), cap, most});
     p->k_steps = (steps + waves * splits - 1) / (waves * splits);
     p->splits = (steps + waves * p->k_steps - 1) / (waves * p->k_steps);
     // columns per expand workgroup: four stages of the wide kernel, or runs
@@ -774,12 +774,19 @@ void lora_plan(int M, int N, int K, int adapters, int max_rank, bool f32, LoraPl
     }
     p->n_chunk = n_chunk;
     auto align = [](size_t v) { return (v + 255) & ~size_t(255); };
+    // The workspace holds what any call of at most M rows takes, so that one
+    // sized for the most rows serves fewer: rows of v in all slices, which are
+    // M in one, up to few_cap slices of 32 rows, or up to four slices of which
+    // two workgroups for each compute unit, of at most 32 rows, write; and
+    // tiles of 16 rows.
+    const int64_t v_rows = std::max({(int64_t)M, (int64_t)std::min(M, 32) * std::min(few_cap, most),
+                                     std::min((int64_t)M * std::min(4, most), (int64_t)2 * kComputeUnits * 32)});
     size_t at = 0;
     p->v_at = at;
-    at += align((size_t)p->splits * M * p->v_stride * 4);
+    at += align((size_t)v_rows * p->v_stride * 4);
     if (p->sorted) {
         p->tiles_at = at;
-        at += align((size_t)p->max_tiles * 16);
+        at += align((size_t)((M + 15) / 16 + std::min(adapters + 1, M)) * 16);
         p->count_at = at;
         at += 256;
         p->perm_at = at;

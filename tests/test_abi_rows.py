@@ -1,5 +1,7 @@
 """The per-row calls refuse what they cannot take, before any HIP call (no
 GPU: the addresses are never dereferenced)."""
+import random
+
 import pytest
 
 import skinny_bit_gemm_amd as q
@@ -105,3 +107,18 @@ def test_lora_refusals():
     for bad in ((-1, 256, 512, 8, 16), (4, 248, 512, 8, 16), (4, 256, 512, 0, 16), (4, 256, 512, 8, 12)):
         with pytest.raises(q.QlinError):
             q.qlin_lora_workspace_bytes(*bad)
+
+
+def counts_of_rows():
+    """Every count around those where plans change, and random ones."""
+    rng = random.Random(7)
+    return sorted({max(0, c + d) for c in [1 << i for i in range(18)] + [48, 1024, 1536, 2400, 2500, 3750, 5000, 7500, 12288,
+                                                                     15000, 16384 * 3] for d in range(-2, 3)} |
+                  {rng.randint(0, 1 << 17) for _ in range(300)})
+
+
+def test_an_adapter_workspace_for_the_most_rows_serves_fewer():
+    for N, K, n, R in ((4096, 12288, 8, 64), (4096, 4096, 64, 64), (256, 512, 8, 16), (10240, 5120, 4096, 256),
+                       (2048, 2048, 1, 8), (80, 96, 300, 24), (151936, 4096, 16, 32), (16, 1 << 20, 2, 40)):
+        sizes = [q.qlin_lora_workspace_bytes(M, N, K, n, R) for M in counts_of_rows()]
+        assert sizes == sorted(sizes), f"{N} x {K}, {n} of rank {R}"

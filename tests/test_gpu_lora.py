@@ -309,6 +309,25 @@ def test_rows_without_an_adapter_stay_as_they_are(M, out):
     assert np.array_equal(y.cpu().numpy().view(word)[stay], before[stay])
 
 
+@pytest.mark.parametrize("R", [8, 64])
+def test_one_workspace_for_all_sizes(R):
+    """A workspace of the largest call's size serves the smaller ones, whatever is left in it."""
+    N, K, n = 48, 1040, 5
+    sizes = (2600, 1530, 130, 65, 64, 40, 20, 1)
+    work = guarded((q.qlin_lora_workspace_bytes(max(sizes), N, K, n, R),), torch.uint8, 0xFF)
+    for M in sizes:
+        x, A, B, ids, ranks, scales = make(M, N, K, n, R, 3)
+        y = guarded((M, N), torch.float32, 7)
+        q.qlin_lora(M, N, K, n, R, to_dev_bf16(x), K, to_dev(ids), to_dev_bf16(A), to_dev_bf16(B), to_dev(ranks),
+                    to_dev(scales), None, 0, y, N, F32, work)
+        torch.cuda.synchronize()
+        check_guards(y, work, what=f"qlin_lora M={M}")
+        pick = np.unique(np.linspace(0, M - 1, 40).astype(int))
+        ref, _, of_terms = orows.lora(f32_of(x[pick]), ids[pick], f32_of(A), f32_of(B), ranks, scales)
+        err = np.abs(y.cpu().numpy()[pick] - ref)
+        assert (err <= 4 * (np.sqrt(K) + 8) * U * (of_terms + np.abs(ref)) + 1e-37).all()
+
+
 def test_slices_of_a_wider_projection():
     """q, k, v: adapters for column ranges of one output, in place."""
     M, K, n, R, widths = 21, 256, 4, 16, (128, 64, 64)
