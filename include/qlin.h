@@ -379,8 +379,10 @@ typedef struct {
  * The weights: scale x s, or scale x s / (the sum of the token's chosen s),
  * 0 where that sum is 0 in 64 bits (sigmoids of logits below -709.78).
  * Rows are in expert order and, within an expert, in token order.
- *   workspace  qlin_route_workspace_bytes(router, T) bytes (may be 0); needs
- *              no initial value.  Calls that overlap in time must not share it.
+ *   workspace  qlin_route_workspace_bytes(router, T) bytes (may be 0), which
+ *              never shrink as T grows: one for the most tokens serves fewer.
+ *              Needs no initial value.  Calls that overlap in time must not
+ *              share it.
  * T may be 0: offsets are zeroed and nothing else is written.
  * Errors: QLIN_ERR_INVALID_ARG (a null pointer, a router field out of range),
  * QLIN_ERR_ALIGNMENT (ld < experts, pointers not aligned to their element),

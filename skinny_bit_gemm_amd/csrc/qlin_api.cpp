@@ -582,7 +582,7 @@ static bool aligned2(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 1
 static bool ld_ok(int64_t ld, int n, int bytes) { return ld >= n && ld % (16 / bytes) == 0; }
 
 static size_t route_ws(const RoutePlan &p, const qlin_router *r) {
-    return p.once ? 0 : align256((size_t)p.blocks * route_hist_stride(r->experts) * 2);
+    return align256((size_t)p.ws_blocks * route_hist_stride(r->experts) * 2);
 }
 
 static qlin_status check_tokens(int T, int topk) {

@@ -92,6 +92,7 @@ qlin_status make_plan(qlin_format fmt, int M, int N, int K, const qlin_config &c
 struct RoutePlan {
     int rows, once;
     int blocks, block_tokens;
+    int ws_blocks;             // blocks that the workspace has room for
 };
 
 // A routing launch (qlin_route), resolved on the host.

@@ -667,6 +667,8 @@ __global__ __launch_bounds__(kPlaceThreads) void place_kernel(RouteLaunch a) {
 //          long as there is a compute unit for each block (256 in 8 groups,
 //          1024 tokens: 17.7 us against 21.0 with 32), then 32 (8192: 22.1
 //          against 23.8 with 16); at most 512 blocks to sum over
+constexpr int kMostBlocks = 512;
+
 RoutePlan route_plan(const qlin_router &r, int T) {
     RoutePlan p = {};
     const int group = r.experts / r.groups;
@@ -674,8 +676,11 @@ RoutePlan route_plan(const qlin_router &r, int T) {
     p.rows = fits && (T > 8 || r.experts <= 64 || r.groups > 1);
     p.once = T <= (!p.rows ? 16 : r.groups > 1 ? 32 : 64);
     const int tokens = p.rows && T > 16 * kComputeUnits ? 32 : 16;
-    p.block_tokens = tokens * ((T + tokens * 512 - 1) / (tokens * 512));
+    p.block_tokens = tokens * ((T + tokens * kMostBlocks - 1) / (tokens * kMostBlocks));
     p.blocks = p.once ? 1 : (T + p.block_tokens - 1) / p.block_tokens;
+    // no call of at most T tokens has more blocks than this: a workspace for
+    // the most tokens serves fewer
+    p.ws_blocks = p.once ? 0 : std::min((T + 15) / 16, kMostBlocks);
     return p;
 }
 

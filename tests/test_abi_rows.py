@@ -122,3 +122,10 @@ def test_an_adapter_workspace_for_the_most_rows_serves_fewer():
                        (2048, 2048, 1, 8), (80, 96, 300, 24), (151936, 4096, 16, 32), (16, 1 << 20, 2, 40)):
         sizes = [q.qlin_lora_workspace_bytes(M, N, K, n, R) for M in counts_of_rows()]
         assert sizes == sorted(sizes), f"{N} x {K}, {n} of rank {R}"
+
+
+def test_a_routing_workspace_for_the_most_tokens_serves_fewer():
+    for E, k, groups in ((64, 8, 1), (60, 4, 1), (128, 8, 1), (256, 8, 8), (384, 6, 1), (160, 6, 8), (1024, 8, 1)):
+        r = q.make_router(E, k, groups=groups, topk_groups=min(2, groups))
+        sizes = [q.qlin_route_workspace_bytes(r, T) for T in counts_of_rows() if T * k <= 1 << 20]
+        assert sizes == sorted(sizes), f"{E} experts in {groups} groups"

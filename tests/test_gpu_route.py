@@ -221,6 +221,24 @@ def test_route_sigmoid_of_low_logits(E, T, steered):
             check_route(wl.bf16_bits_to_f32(to_bits(l)), True, bias, topk=3, score=SIG, renormalize=renorm)
 
 
+@pytest.mark.parametrize("E,groups", [(256, 8), (300, 1), (64, 1)])
+def test_route_one_workspace_for_all_sizes(E, groups):
+    """A workspace of the largest call's size serves the smaller ones."""
+    r = q.make_router(E, 4, SIG, groups, min(4, groups))
+    sizes = (5000, 4096, 300, 33, 9, 1)
+    work = guarded((q.qlin_route_workspace_bytes(r, max(sizes)),), torch.uint8, 0xEE)
+    for T in sizes:
+        l = logits_for(T, E, 61, False)
+        bufs = [guarded(s, d, -7) for s, d in (((T, 4), torch.int32), ((T, 4), torch.float32), ((E + 1,), torch.int32),
+                                               ((T * 4,), torch.int32), ((T, 4), torch.int32))]
+        q.qlin_route(r, T, to_dev(l), E, F32, None, *bufs, work)
+        torch.cuda.synchronize()
+        check_guards(*bufs, work, what=f"qlin_route T={T}")
+        want = orows.route(l, 4, SIG, None, groups, min(4, groups))
+        for i, j in ((0, 0), (2, 2), (3, 3), (4, 4)):
+            assert np.array_equal(bufs[i].cpu().numpy(), want[j])
+
+
 def test_route_no_tokens():
     off = guarded((65,), torch.int32, -7)
     other = guarded((16,), torch.int32, -7)
