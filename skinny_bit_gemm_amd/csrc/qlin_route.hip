@@ -7,9 +7,9 @@
 //
 // Compiled with -fno-honor-nans: a maximum of doubles is then one instruction
 // instead of two or three (8192 tokens, 256 experts in 8 groups: 20.6 us
-// against 22.1).  No NaN takes part: those of the caller are known by their
-// bits and closed first (is_nan), and what an all-closed token leaves in sums
-// is not selected.
+// against 22.1).  No NaN takes part: the caller's logits and biases are loaded
+// as integers, and a NaN among them has become -inf before it is a float
+// (number_or_closed); what an all-closed token leaves in sums is not selected.
 #include <algorithm>
 #include <type_traits>
 
@@ -109,8 +109,13 @@ __device__ __forceinline__ double token_sum(double v) {
     return v;
 }
 
-// By the bits, which hold whatever the compiler is told about NaN.
-__device__ __forceinline__ bool is_nan(float f) { return (__float_as_uint(f) & 0x7FFFFFFFu) > 0x7F800000u; }
+// The float of these bits, -inf where they are NaN's.
+__device__ __forceinline__ float number_or_closed(uint32_t bits) {
+    return __uint_as_float((bits & 0x7FFFFFFFu) > 0x7F800000u ? 0xFF800000u : bits);
+}
+__device__ __forceinline__ float bias_of(const RouteLaunch &a, int e) {
+    return number_or_closed(reinterpret_cast<const uint32_t *>(a.bias)[e]);
+}
 
 // ------------------------------------------------------------- ordered keys
 
@@ -183,18 +188,19 @@ __device__ __forceinline__ float weight_of(const RouteLaunch &a, const float (&l
 template <int LPT, int EPL>
 __device__ __forceinline__ void load_logits(const RouteLaunch &a, int t, bool live, int lane, float (&l)[EPL]) {
     const int64_t row = (int64_t)(live ? t : a.T - 1) * a.ld;
+    uint32_t bits[EPL];
     if (a.logits_bf16) {
         const uint16_t *p = static_cast<const uint16_t *>(a.logits) + row;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) l[j] = __uint_as_float((uint32_t)p[min(lane + LPT * j, a.experts - 1)] << 16);
+        for (int j = 0; j < EPL; ++j) bits[j] = (uint32_t)p[min(lane + LPT * j, a.experts - 1)] << 16;
     } else {
-        const float *p = static_cast<const float *>(a.logits) + row;
+        const uint32_t *p = static_cast<const uint32_t *>(a.logits) + row;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) l[j] = p[min(lane + LPT * j, a.experts - 1)];
+        for (int j = 0; j < EPL; ++j) bits[j] = p[min(lane + LPT * j, a.experts - 1)];
     }
 #pragma unroll
     for (int j = 0; j < EPL; ++j)
-        l[j] = live && lane + LPT * j < a.experts && !is_nan(l[j]) ? fminf(l[j], kFltMax) : -INFINITY;
+        l[j] = live && lane + LPT * j < a.experts ? fminf(number_or_closed(bits[j]), kFltMax) : -INFINITY;
 }
 
 // One token by a wave: lane j < topk ends with the j-th chosen expert
@@ -231,8 +237,8 @@ __device__ __forceinline__ void route_token(const RouteLaunch &a, int t, int lan
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
             const int e = lane + 64 * j;
-            const float b = a.bias && e < a.experts ? a.bias[e] : 0.0f;
-            key[j] = l[j] > -INFINITY && b > -INFINITY && !is_nan(b) ? ordered(s[j] + (double)b) : 0;
+            const float b = a.bias && e < a.experts ? bias_of(a, e) : 0.0f;
+            key[j] = l[j] > -INFINITY && b > -INFINITY ? ordered(s[j] + (double)b) : 0;
         }
     } else {
 #pragma unroll
@@ -374,8 +380,8 @@ __device__ __forceinline__ void route_row(const RouteLaunch &a, int t, bool live
         if (a.bias) {
 #pragma unroll
             for (int j = 0; j < EPL; ++j) {
-                const float b = a.bias[min(lane + 16 * j, a.experts - 1)];
-                c[j] = b > -INFINITY && !is_nan(b) ? c[j] + (double)b : kClosed;
+                const float b = bias_of(a, min(lane + 16 * j, a.experts - 1));
+                c[j] = b > -INFINITY ? c[j] + (double)b : kClosed;
             }
         }
 #pragma unroll

@@ -145,6 +145,33 @@ def test_route_masks_and_extremes(score, steered):
             check_route(l, bf16, bias, score=score, renormalize=renorm, groups=7, topk_groups=3, group_score=int(steered))
 
 
+@pytest.mark.parametrize("E,groups", [(40, 1), (70, 1), (256, 8), (300, 1)])
+@pytest.mark.parametrize("T", [5, 50])
+@pytest.mark.parametrize("steered", [False, True], ids=["plain", "bias"])
+def test_route_every_kind_of_nan(E, groups, T, steered):
+    """NaN of both signs, quiet and signalling, smallest and largest payload, are closed: in logits of both types and biases."""
+    kinds = np.array([0x7FC00000, 0xFFC00000, 0x7F800001, 0xFF800001, 0x7FFFFFFF, 0xFFFFFFFF, 0x7FA00000], dtype=np.uint32)
+    kinds16 = np.array([0x7FC0, 0xFFC0, 0x7F81, 0xFF81, 0x7FFF, 0xFFFF, 0x7FA0], dtype=np.uint16)
+    rng = np.random.default_rng([E, T])
+    r = q.make_router(E, 6, SIG, groups, min(3, groups), q.QLIN_GROUP_TOP2)
+    l = logits_for(T, E, 71, True)
+    gone = rng.random((T, E)) < 0.3
+    gone[T // 2] = True
+    which = rng.integers(0, 7, (T, E))
+    bias, bias_ref = None, None
+    if steered:
+        bias = rng.normal(0, 0.05, E).astype(np.float32)
+        bias_ref = bias.copy()
+        bias.view(np.uint32)[3:10], bias_ref[3:10] = kinds, NAN
+    want = orows.route(np.where(gone, NAN, l), 6, SIG, bias_ref, groups, min(3, groups), 1)
+    wide = np.where(gone, kinds[which], l.view(np.uint32)).astype(np.uint32)
+    half = np.where(gone, kinds16[which], to_bits(l)).astype(np.uint16)
+    for logits, lt in ((to_dev(wide.view(np.int32)), F32), (to_dev_bf16(half), BF16)):
+        got = run_route(r, logits, T, E, lt, bias)
+        assert np.array_equal(got[0], want[0]) and np.array_equal(got[3], want[3]) and np.array_equal(got[4], want[4])
+        assert np.isfinite(got[1]).all()
+
+
 def test_route_strided_logits_and_sub_byte_alignment():
     check_route(logits_for(50, 60, 5, False), ld=61)
     check_route(logits_for(50, 60, 5, True), True, ld=61)
