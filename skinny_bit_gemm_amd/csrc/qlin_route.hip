@@ -576,7 +576,7 @@ constexpr int kPlaceBlocks = 8;
 
 __global__ __launch_bounds__(kPlaceThreads) void place_kernel(RouteLaunch a) {
     __shared__ uint32_t pre[QLIN_MAX_EXPERTS], tot[QLIN_MAX_EXPERTS], off[QLIN_MAX_EXPERTS + 1];
-    __shared__ uint16_t own[kPlaceBlocks][QLIN_MAX_EXPERTS];   // counts, then places, of this workgroup's blocks
+    __shared__ __align__(16) uint16_t own[kPlaceBlocks][QLIN_MAX_EXPERTS];   // counts, then places, of this workgroup's blocks
     __shared__ uint32_t wave_tot[16];
     const int tid = threadIdx.x;
     const int b0 = blockIdx.x * kPlaceBlocks, b1 = min(a.blocks, b0 + kPlaceBlocks);
