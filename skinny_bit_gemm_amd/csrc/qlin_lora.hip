@@ -715,12 +715,24 @@ __global__ __launch_bounds__(1024) void group_kernel(LoraLaunch a, int tile_rows
 
 // ---------------------------------------------------------------- planning
 
-// Rows from which tiles are wide (64 rows, each B row read once for them); a
-// call with fewer has too few such tiles for the compute units, and a smaller
-// rank has less of B to read again.  Narrow / wide, N 10240, K 5120: rank 8,
-// 1500 rows 0.98, 2500 0.90, 3000 1.13; rank 64, 1500 rows 1.00, 2048 1.09,
-// 3000 1.28; N = K = 4096: rank 16, 1024 rows 17.5 us against 23.6.
-static int wide_from(int max_rank) { return max_rank <= 16 ? 2400 : 1536; }
+// Whether tiles are wide (64 rows, each B row read once for them instead of
+// every 16 rows, and base and y in longer pieces).  Wide tiles pay where B is
+// read often (rows x rank) or where base and y come from HBM; before that the
+// narrow ones, of which there are four times as many, fill the compute units
+// better.  Narrow / wide (time), with new x and base each call, six adapters
+// in runs of 251 rows and 64 with single rows:
+//   rank 8   10240 x 5120: 2000 rows (82 MB of base and y) 0.92, 0.97; 3000 1.30, 1.07
+//            4096 x 4096: 3000 rows (49 MB) 0.92, 0.86; 4000 1.07, 1.07; 2048 x 2048: 6000 0.95, 0.87
+//   rank 32  4096 x 4096: 3000 rows 0.95, 0.96; 4000 1.15, 1.22
+//   rank 64  2048 x 6144: 2000 rows 0.82, 0.98; 3000 1.12, 1.23; 10240 x 5120: 1536 rows 0.99, 1.17; 2000 1.19, 1.27
+//   rank 256 4096 x 4096: 2000 rows 1.08, 0.89; 3000 0.89, 1.29
+//   fp32     10240 x 5120: rank 8, 1100 rows (90 MB) 1.01, 0.87; 1536 1.16, 1.01; rank 32, 1100 rows 0.90, 1.05
+// With x and base still in the caches narrow tiles stay ahead for longer, for
+// ranks up to 16 by 5 to 15 %.
+static bool wide_tiles(int M, int N, int max_rank, bool f32) {
+    if (M < 1280) return false;
+    return (int64_t)M * N * (f32 ? 8 : 4) >= 80000000 || (int64_t)M * std::min(max_rank, 48) >= 120000;
+}
 
 // One launch for both products: where a row's A is small, so that reading it
 // in every workgroup costs less than a second launch.  In elements of A: a
@@ -739,7 +751,7 @@ static bool few_rows(int M, int N, int K, int max_rank) {
 void lora_plan(int M, int N, int K, int adapters, int max_rank, bool f32, LoraPlan *p) {
     p->few = few_rows(M, N, K, max_rank);
     p->sorted = M > kDirectRows;
-    p->wide = M >= wide_from(max_rank);
+    p->wide = wide_tiles(M, N, max_rank, f32);
     const int tile_rows = p->wide ? kWideRows : 16;
     p->max_tiles = p->sorted ? (M + tile_rows - 1) / tile_rows + std::min(adapters + 1, M) : M;
     p->rt = max_rank <= 16 ? 1 : max_rank <= 32 ? 2 : 4;

@@ -171,6 +171,29 @@ def test_prompts_with_many_adapters_and_bad_rows(R):
     assert np.isfinite(np.delete(got, [77, 78], 0)).all()
 
 
+WIDE = [(15001, 8), (7501, 16), (5003, 24), (3751, 32), (3001, 40), (2500, 64), (2501, 72), (2600, 136), (2750, 256)]
+
+
+@pytest.mark.parametrize("M,R", WIDE)
+@pytest.mark.parametrize("out", [BF16, F32], ids=["bf16", "f32"])
+def test_wide_tiles(M, R, out):
+    """Enough rows for 64-row tiles at each rank: ranks that do not fill a stage or fill several, tiles and stages
+    that are not whole, every order of the rows and every base."""
+    check(M, 144, 96, 3, R, out=out, rows=30, pad=8, base="y")
+    check(M, 80, 48, 40, R, out=out, rows=30)
+    check(M, 144, 80, 7, R, out=out, used="runs", rows=30, base=None)
+    check(M, 48, 32, 2, R, out=out, used="one", rows=30, base="y")
+    for base in (None, "new", "y"):
+        check(M, 48, 32, 2, R, out=out, used="none", rows=30, base=base, pad=8)
+
+
+@pytest.mark.parametrize("M,N,R,out", [(1279, 15648, 8, BF16), (1280, 15632, 8, BF16), (1290, 15520, 16, BF16),
+                                       (1290, 7760, 24, F32), (2499, 208, 48, BF16), (2500, 208, 48, F32)])
+def test_rows_where_tiles_become_wide(M, N, R, out):
+    check(M, N, 64, 5, R, out=out, rows=20, base="y")
+    check(M, N, 64, 700, R, out=out, rows=20)
+
+
 def test_the_largest_row_count():
     """2^20 rows: more row tiles than a grid's y holds."""
     M, N, K, n, R = 1 << 20, 16, 16, 2, 8
