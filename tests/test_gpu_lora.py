@@ -194,6 +194,52 @@ def test_rows_where_tiles_become_wide(M, N, R, out):
     check(M, N, 64, 700, R, out=out, rows=20)
 
 
+@pytest.mark.parametrize("M,R", [(2500, 64), (15001, 8)])
+@pytest.mark.parametrize("out", [BF16, F32], ids=["bf16", "f32"])
+def test_bad_rows_in_wide_tiles(M, R, out):
+    """A NaN and an infinity in x stay in their rows of a wide tile; with rank 1 the infinity reaches y as one."""
+    N, K = 64, 96
+    x, A, B, ids, ranks, scales = make(M, N, K, 3, R, 6, "one")
+    ranks[0] = 1
+    outs = []
+    for bad in (False, True):
+        if bad:
+            x[1, 5], x[M - 2, 6] = 0x7F80, 0x7FC0
+        y = torch.zeros(M, N, dtype=torch.float32 if out == F32 else torch.int16, device=DEV)
+        work = torch.empty(q.qlin_lora_workspace_bytes(M, N, K, 3, R), dtype=torch.uint8, device=DEV)
+        q.qlin_lora(M, N, K, 3, R, to_dev_bf16(x), K, to_dev(ids), to_dev_bf16(A), to_dev_bf16(B), to_dev(ranks),
+                    to_dev(scales), None, 0, y, N, out, work)
+        torch.cuda.synchronize()
+        outs.append(y.cpu().numpy() if out == F32 else f32_of(y.cpu().numpy().view(np.uint16)))
+    sign = np.sign(f32_of(A[0, 0, 5:6])[0] * f32_of(B[0, :, 0]))
+    assert np.array_equal(outs[1][1], sign * np.inf) and np.isnan(outs[1][M - 2]).all()
+    assert np.array_equal(np.delete(outs[0], [1, M - 2], 0), np.delete(outs[1], [1, M - 2], 0))
+
+
+@pytest.mark.parametrize("M,R", [(2, 16), (16, 64), (64, 16), (2500, 64), (9000, 16), (15001, 8), (6000, 8)])
+@pytest.mark.parametrize("out", [BF16, F32], ids=["bf16", "f32"])
+def test_same_bits_on_every_path(M, R, out):
+    """One launch, direct tiles, sorted tiles of both heights, and more rows than a sorting thread holds: a second call
+    gives the same bits, and so do the same rows when the others have other adapters."""
+    N, K, n = 144, 272, 5
+    x, A, B, ids, ranks, scales = make(M, N, K, n, R, 8, "runs")
+    dev = [to_dev_bf16(x), to_dev_bf16(A), to_dev_bf16(B), to_dev(ranks), to_dev(scales)]
+    work = torch.empty(q.qlin_lora_workspace_bytes(M, N, K, n, R), dtype=torch.uint8, device=DEV)
+    outs = []
+    for turn in range(4):
+        i = ids.copy()
+        if turn == 2:
+            i[1::2] = np.random.default_rng(1).integers(-1, n, len(i[1::2]))
+        if turn == 3:
+            i[1::2] = -1
+        y = torch.zeros(M, N, dtype=torch.float32 if out == F32 else torch.int16, device=DEV)
+        q.qlin_lora(M, N, K, n, R, dev[0], K, to_dev(i), dev[1], dev[2], dev[3], dev[4], None, 0, y, N, out, work)
+        torch.cuda.synchronize()
+        outs.append(y.cpu().numpy())
+    assert np.array_equal(outs[0], outs[1])
+    assert np.array_equal(outs[0][::2], outs[2][::2]) and np.array_equal(outs[0][::2], outs[3][::2])
+
+
 def test_the_largest_row_count():
     """2^20 rows: more row tiles than a grid's y holds."""
     M, N, K, n, R = 1 << 20, 16, 16, 2, 8
