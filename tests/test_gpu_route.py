@@ -145,6 +145,18 @@ def test_route_masks_and_extremes(score, steered):
             check_route(l, bf16, bias, score=score, renormalize=renorm, groups=7, topk_groups=3, group_score=int(steered))
 
 
+@pytest.mark.parametrize("E,topk,groups,kept", [(384, 6, 1, 1), (512, 10, 8, 3), (160, 6, 8, 3), (128, 20, 1, 1)])
+@pytest.mark.parametrize("T", [1025, 8192, 8209, 17001])
+def test_route_prompts_of_a_wave_per_token(E, topk, groups, kept, T):
+    """Prompts with more than 256 experts, groups that are not whole 16s, more than 16 choices: blocks of one and of
+    several rounds of 16 tokens."""
+    top2 = int(T % 2 == 1 and groups > 1)
+    bias = np.round(np.random.default_rng(E).normal(0, 0.05, E), 3).astype(np.float32) if T == 8209 else None
+    l = logits_for(T, E, 81, False, 0.2)
+    l[T // 3], l[T - 1] = -INF, -INF
+    check_route(l, bias=bias, topk=topk, score=SIG, groups=groups, topk_groups=kept, group_score=top2)
+
+
 @pytest.mark.parametrize("E,groups", [(40, 1), (70, 1), (256, 8), (300, 1)])
 @pytest.mark.parametrize("T", [5, 50])
 @pytest.mark.parametrize("steered", [False, True], ids=["plain", "bias"])
