@@ -372,10 +372,11 @@ typedef struct {
  * is NaN or -inf is never chosen).  With groups, the topk_groups groups worth
  * most stay open (the worth is over c).  Then the topk largest c are chosen.
  * Ties, of groups too, go to the lowest index.  The order is that of the
- * logits where neither a bias nor QLIN_GROUP_TOP2 comes in, and of scores in
- * 64 bits otherwise: it does not depend on the order of any sum.  Where fewer
- * than topk experts are open, the remaining choices have id -1, weight 0,
- * slot -1 and no row.
+ * logits where neither a bias nor QLIN_GROUP_TOP2 comes in, and of scores
+ * rounded to 64 bits otherwise, where sums are always added up in one order: a
+ * token's choice does not depend on the call's other tokens or their number.
+ * Where fewer than topk experts are open, the remaining choices have id -1,
+ * weight 0, slot -1 and no row.
  * The weights: scale x s, or scale x s / (the sum of the token's chosen s),
  * 0 where that sum is 0 in 64 bits (sigmoids of logits below -709.78).
  * Rows are in expert order and, within an expert, in token order.

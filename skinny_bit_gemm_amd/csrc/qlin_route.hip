@@ -109,6 +109,22 @@ __device__ __forceinline__ double token_sum(double v) {
     return v;
 }
 
+// 1 / d for d >= 1: two Newton steps from the hardware's estimate (within
+// 2^-20 of itself or better, so within 2^-52 after them); 0 for infinity
+__device__ __forceinline__ double recip(double d) {
+    double y = __builtin_amdgcn_rcp(d);
+    y = __builtin_fma(y, __builtin_fma(-d, y, 1.0), y);
+    y = __builtin_fma(y, __builtin_fma(-d, y, 1.0), y);
+    return d < INFINITY ? y : 0.0;
+}
+
+// p + q of what are products or exponentials, never fused into them: the two
+// ways of routing a token have to get the same bits.
+__device__ __forceinline__ double plus(double p, double q) {
+#pragma clang fp contract(off)
+    return p + q;
+}
+
 // The float of these bits, -inf where they are NaN's.
 __device__ __forceinline__ float number_or_closed(uint32_t bits) {
     return __uint_as_float((bits & 0x7FFFFFFFu) > 0x7F800000u ? 0xFF800000u : bits);
@@ -225,20 +241,20 @@ __device__ __forceinline__ void route_token(const RouteLaunch &a, int t, int lan
 #pragma unroll
             for (int j = 0; j < EPL; ++j) {
                 s[j] = l[j] > -INFINITY ? exp((double)l[j] - (double)top) : 0.0;
-                sum += s[j];
+                sum = plus(sum, s[j]);
             }
-            sum = token_sum<64>(sum);
+            const double y = 1.0 / token_sum<64>(sum);
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) s[j] /= sum;
+            for (int j = 0; j < EPL; ++j) s[j] *= y;
         } else {
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) s[j] = 1.0 / (1.0 + exp(-(double)l[j]));
+            for (int j = 0; j < EPL; ++j) s[j] = recip(plus(1.0, exp(-(double)l[j])));
         }
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
             const int e = lane + 64 * j;
             const float b = a.bias && e < a.experts ? bias_of(a, e) : 0.0f;
-            key[j] = l[j] > -INFINITY && b > -INFINITY ? ordered(s[j] + (double)b) : 0;
+            key[j] = l[j] > -INFINITY && b > -INFINITY ? ordered(plus(s[j], b)) : 0;
         }
     } else {
 #pragma unroll
@@ -335,19 +351,12 @@ __device__ __forceinline__ double taken(bool now, double c) {
     return __hiloint2double(now ? (int)0xFFEFFFFF : __double2hiint(c), __double2loint(c));
 }
 
-// 1 / d for d >= 1: two Newton steps from the hardware's estimate (within
-// 2^-20 of itself or better, so within 2^-52 after them); 0 for infinity
-__device__ __forceinline__ double recip(double d) {
-    double y = __builtin_amdgcn_rcp(d);
-    y = __builtin_fma(y, __builtin_fma(-d, y, 1.0), y);
-    y = __builtin_fma(y, __builtin_fma(-d, y, 1.0), y);
-    return d < INFINITY ? y : 0.0;
-}
-
 // One token by a row of 16 lanes, where four tokens share each instruction of
 // the reductions (groups of a multiple of 16 experts, at most 16 of them).  The
 // scores are compared as numbers, in 64 bits (WIDE) where their sums need it:
-// a double's maximum is one instruction.
+// a double's maximum is one instruction.  They have the bits that route_token
+// gives them, a softmax's sum in the same order (sum[q]: the experts that a
+// wave has in its row q), so a token chooses the same in a call of any size.
 template <int EPL, bool WIDE>
 __device__ __forceinline__ void route_row(const RouteLaunch &a, int t, bool live, int lane, int &my_id, float &my_w) {
     using C = std::conditional_t<WIDE, double, float>;
@@ -364,24 +373,24 @@ __device__ __forceinline__ void route_row(const RouteLaunch &a, int t, bool live
     }
     if constexpr (WIDE) {
         if (a.score == QLIN_SCORE_SOFTMAX) {
-            double sum = 0.0;
+            double sum[4] = {};
 #pragma unroll
             for (int j = 0; j < EPL; ++j) {
                 c[j] = l[j] > -INFINITY ? exp((double)l[j] - (double)top) : 0.0;
-                sum += c[j];
+                sum[j & 3] = plus(sum[j & 3], c[j]);
             }
-            const double y = 1.0 / row16_sum(sum);
+            const double y = 1.0 / ((row16_sum(sum[3]) + row16_sum(sum[2])) + (row16_sum(sum[1]) + row16_sum(sum[0])));
 #pragma unroll
             for (int j = 0; j < EPL; ++j) c[j] *= y;
         } else {
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) c[j] = recip(1.0 + exp(-(double)l[j]));
+            for (int j = 0; j < EPL; ++j) c[j] = recip(plus(1.0, exp(-(double)l[j])));
         }
         if (a.bias) {
 #pragma unroll
             for (int j = 0; j < EPL; ++j) {
                 const float b = bias_of(a, min(lane + 16 * j, a.experts - 1));
-                c[j] = b > -INFINITY ? c[j] + (double)b : kClosed;
+                c[j] = b > -INFINITY ? plus(c[j], b) : kClosed;
             }
         }
 #pragma unroll

@@ -278,6 +278,31 @@ def test_route_one_workspace_for_all_sizes(E, groups):
             assert np.array_equal(bufs[i].cpu().numpy(), want[j])
 
 
+@pytest.mark.parametrize("E", [65, 100, 128, 200, 256])
+@pytest.mark.parametrize("score", [SOFT, SIG], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("spread", [1e-16, 4e-16, 3e-15, 1e-8, 1.0])
+def test_route_same_choice_in_calls_of_any_size(E, score, spread):
+    """Scores a few units in the last of 64 bits apart, or ordinary ones: a token chooses the same experts in a call of
+    8 tokens (a wave each), of 40 and of 2000 (16 lanes each)."""
+    T = 2000
+    rng = np.random.default_rng([E, score])
+    l = (rng.normal(size=(T, E)) * spread).astype(np.float32)
+    l[rng.random((T, E)) < 0.1] = -INF
+    for bias in (np.zeros(E), rng.choice([0.0, 0.25], E), rng.normal(0, 0.1, E)):
+        router, ids = q.make_router(E, 7, score), {}
+        ld, bd = to_dev(l), to_dev(bias.astype(np.float32))
+        work = torch.empty(max(16, q.qlin_route_workspace_bytes(router, T)), dtype=torch.uint8, device=DEV)
+        for n in (8, 40, T):
+            got = torch.empty(T, 7, dtype=torch.int32, device=DEV)
+            w, slots = torch.empty(n, 7, device=DEV), torch.empty(n, 7, dtype=torch.int32, device=DEV)
+            off, rows = torch.empty(E + 1, dtype=torch.int32, device=DEV), torch.empty(n * 7, dtype=torch.int32, device=DEV)
+            for t in range(0, T, n):
+                q.qlin_route(router, n, ld[t:], E, F32, bd, got[t:], w, off, rows, slots, work)
+            torch.cuda.synchronize()
+            ids[n] = got.cpu().numpy()
+        assert np.array_equal(ids[8], ids[40]) and np.array_equal(ids[8], ids[T])
+
+
 def test_route_no_tokens():
     off = guarded((65,), torch.int32, -7)
     other = guarded((16,), torch.int32, -7)
