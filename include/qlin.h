@@ -445,8 +445,8 @@ qlin_status qlin_combine(int T, int topk, int N, const void *h, int64_t ldh, qli
  *   y        [M, ldy] of out_type (QLIN_OUT_BF16 or QLIN_OUT_F32_ACC)
  * A projection that is a slice of a wider one (q, k, v) takes base and y as
  * views: column offsets in whole 16-byte units, ldb and ldy the wide one's.
- * Sums are fp32; the product A_a x is kept to at least 16 bits (24 for
- * QLIN_OUT_F32_ACC) of mantissa between the two products; y is rounded once.
+ * Sums are fp32; the product A_a x keeps its 24 bits of mantissa between the
+ * two products; y is rounded once.
  * NaN and infinities in x reach y in their own row only; A and B, as far as
  * the ranks go, are finite.
  * N % 16 == 0, K % 16 == 0, max_rank % 8 == 0 up to QLIN_MAX_RANK; leading

@@ -192,12 +192,16 @@ __device__ __forceinline__ float left_of(float f, float hi) {
     return __builtin_fabsf(r) < INFINITY ? r : 0.0f;
 }
 
-// Four numbers as TERMS bf16 numbers each that add up to them: each takes 8
-// more bits of the mantissa.
-template <int TERMS>
-__device__ __forceinline__ void split4(v4f f, uint2 (&out)[TERMS]) {
+// A number between the products is this many bf16 numbers that add up to it:
+// each takes 8 more bits of the mantissa, so three keep the 24 bits of fp32.
+// Two would be 1 to 2 % faster for ranks up to 64 (3 to 6 % for 256; 4096 rows
+// of rank 64: 70.4 us against 71.0) but lose what B's products leave where
+// they cancel across the ranks.
+constexpr int kTerms = 3;
+
+__device__ __forceinline__ void split4(v4f f, uint2 (&out)[kTerms]) {
 #pragma unroll
-    for (int e = 0; e < TERMS; ++e) {
+    for (int e = 0; e < kTerms; ++e) {
         out[e] = make_uint2(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]));
         f[0] = left_of(f[0], bf16_lo(out[e].x));
         f[1] = left_of(f[1], bf16_hi(out[e].x));
@@ -213,12 +217,10 @@ __device__ __forceinline__ uint4 add_pairs(uint4 b, float f0, float f1, float f2
                       bf16_pair(bf16_lo(b.z) + f4, bf16_hi(b.z) + f5), bf16_pair(bf16_lo(b.w) + f6, bf16_hi(b.w) + f7));
 }
 
-// A tile's v into the LDS (vs[TERMS][ROWS][32 steps + 8]) by 256 threads: the
+// A tile's v into the LDS (vs[kTerms][ROWS][32 steps + 8]) by 256 threads: the
 // slices are added up, the adapter's scale is applied and the sum is kept as
-// TERMS bf16 numbers that add up to it, so that the second product loses
-// nothing that its fp32 sums would keep (3, for fp32 y) or less than the bf16
-// rounding of y shows (2).  Ranks past the adapter's are zero.
-template <int ROWS, int TERMS>
+// kTerms bf16 numbers.  Ranks past the adapter's are zero.
+template <int ROWS>
 __device__ __forceinline__ void fill_v(const LoraLaunch &a, const Tile &t, const int *member, int ranks, int steps,
                                        uint16_t *vs) {
     const int tid = threadIdx.x, stride = steps * 32 + 8;
@@ -232,10 +234,10 @@ __device__ __forceinline__ void fill_v(const LoraLaunch &a, const Tile &t, const
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) f[j] = rank + j < ranks ? f[j] * scale : 0.0f;
-            uint2 o[TERMS];
-            split4<TERMS>(f, o);
+            uint2 o[kTerms];
+            split4(f, o);
 #pragma unroll
-            for (int e = 0; e < TERMS; ++e) *reinterpret_cast<uint2 *>(vs + (e * ROWS + row) * stride + rank) = o[e];
+            for (int e = 0; e < kTerms; ++e) *reinterpret_cast<uint2 *>(vs + (e * ROWS + row) * stride + rank) = o[e];
         }
 }
 
@@ -248,8 +250,7 @@ __device__ __forceinline__ void fill_v(const LoraLaunch &a, const Tile &t, const
 // consecutive bytes of its row.
 template <int RK, bool F32, bool SORTED>
 __global__ __launch_bounds__(256, 4) void expand_kernel(LoraLaunch a) {
-    constexpr int TERMS = F32 ? 3 : 2;
-    extern __shared__ __align__(16) uint16_t vs[];   // [TERMS][16][stride]
+    extern __shared__ __align__(16) uint16_t vs[];   // [kTerms][16][stride]
     __shared__ int member[16];
     const Tile t = find_tile<1, SORTED>(a, blockIdx.y, 0, member);
     if (t.count == 0) return;
@@ -321,7 +322,7 @@ __global__ __launch_bounds__(256, 4) void expand_kernel(LoraLaunch a) {
         for (int q = 0; q < RK; ++q) load_b(n_begin, q, b_next[q]);
     load_base(n_begin, base_next);
 
-    fill_v<16, TERMS>(a, t, member, ranks, steps, vs);
+    fill_v<16>(a, t, member, ranks, steps, vs);
     __syncthreads();
 
     for (int n = n_begin; n < n_end; n += 32) {
@@ -353,7 +354,7 @@ __global__ __launch_bounds__(256, 4) void expand_kernel(LoraLaunch a) {
             for (int j = 0; j < 2; ++j) b[j] = to_fragment(b[j], from);
             clear_past(q, b);
 #pragma unroll
-            for (int e = TERMS - 1; e >= 0; --e) {
+            for (int e = kTerms - 1; e >= 0; --e) {
                 const uint4 v = *reinterpret_cast<const uint4 *>(vs + (e * 16 + c16) * stride + q * 32 + kg * 8);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) acc[j] = mfma_bf16(b[j], v, acc[j]);
@@ -397,10 +398,10 @@ __global__ __launch_bounds__(256, 4) void expand_kernel(LoraLaunch a) {
 //   ONE   a stage holds all ranks (max_rank <= 8 PASS): v stays in registers
 template <int PASS, bool ONE, bool F32>
 __global__ __launch_bounds__(256) void expand_wide_kernel(LoraLaunch a) {
-    constexpr int TERMS = F32 ? 3 : 2, ROWS = kWideRows, NJ = F32 ? 4 : 8, COLS = 16 * NJ;
+    constexpr int ROWS = kWideRows, NJ = F32 ? 4 : 8, COLS = 16 * NJ;
     constexpr int LOADS = COLS * PASS / 256;              // 16-byte loads of a thread for a stage
     __shared__ uint4 bs[COLS * (PASS + 1)];               // [tile j, lane's column][chunk], rows one chunk apart
-    extern __shared__ __align__(16) uint16_t vs[];        // [TERMS][ROWS][stride]
+    extern __shared__ __align__(16) uint16_t vs[];        // [kTerms][ROWS][stride]
     __shared__ int member[ROWS];
     const Tile t = find_tile<ROWS / 16, true>(a, blockIdx.y, 0, member);
     if (t.count == 0) return;
@@ -448,7 +449,7 @@ __global__ __launch_bounds__(256) void expand_wide_kernel(LoraLaunch a) {
     };
     load_b(n_begin, 0);
 
-    fill_v<ROWS, TERMS>(a, t, member, ranks, steps, vs);
+    fill_v<ROWS>(a, t, member, ranks, steps, vs);
     put_b();
     __syncthreads();
 
@@ -467,12 +468,12 @@ __global__ __launch_bounds__(256) void expand_wide_kernel(LoraLaunch a) {
         base_at[i] = (m * a.ldb + n_begin) / PER + c16;
         y_at[i] = (m * a.ldy + n_begin) / PER + c16;
     }
-    uint4 vf[PASS / 4][TERMS];
+    uint4 vf[PASS / 4][kTerms];
     auto load_v = [&](int pass) {
 #pragma unroll
         for (int q = 0; q < PASS / 4; ++q)
 #pragma unroll
-            for (int e = 0; e < TERMS; ++e)
+            for (int e = 0; e < kTerms; ++e)
                 vf[q][e] = pass * PASS * 8 + q * 32 < ranks
                                ? *reinterpret_cast<const uint4 *>(vs + (e * ROWS + row0 + c16) * stride + pass * PASS * 8 +
                                                                   q * 32 + kg * 8)
@@ -512,7 +513,7 @@ __global__ __launch_bounds__(256) void expand_wide_kernel(LoraLaunch a) {
                         bq[j] = make_uint4(bq[j].x & keep[0], bq[j].y & keep[1], bq[j].z & keep[2], bq[j].w & keep[3]);
                 }
 #pragma unroll
-                for (int e = TERMS - 1; e >= 0; --e)
+                for (int e = kTerms - 1; e >= 0; --e)
 #pragma unroll
                     for (int j = 0; j < NJ; ++j) acc[j] = mfma_bf16(vf[q][e], bq[j], acc[j]);
             }
@@ -821,7 +822,7 @@ template <int RK, bool F32>
 static void launch_expand(const LoraPlan &p, const LoraLaunch &a, hipStream_t s) {
     const dim3 grid((a.N + p.n_chunk - 1) / p.n_chunk, p.max_tiles), block(256);
     const int steps = RK > 0 ? RK : (a.max_rank + 31) / 32;
-    const size_t lds = (size_t)(F32 ? 3 : 2) * 16 * (steps * 32 + 8) * 2;
+    const size_t lds = (size_t)kTerms * 16 * (steps * 32 + 8) * 2;
     if (p.sorted) hipLaunchKernelGGL((expand_kernel<RK, F32, true>), grid, block, lds, s, a);
     else hipLaunchKernelGGL((expand_kernel<RK, F32, false>), grid, block, lds, s, a);
 }
@@ -829,7 +830,7 @@ static void launch_expand(const LoraPlan &p, const LoraLaunch &a, hipStream_t s)
 template <int PASS, bool ONE, bool F32>
 static void launch_expand_wide(const LoraPlan &p, const LoraLaunch &a, hipStream_t s) {
     const dim3 grid((a.N + p.n_chunk - 1) / p.n_chunk, p.max_tiles), block(256);
-    const size_t lds = (size_t)(F32 ? 3 : 2) * kWideRows * ((a.max_rank + 31) / 32 * 32 + 8) * 2;
+    const size_t lds = (size_t)kTerms * kWideRows * ((a.max_rank + 31) / 32 * 32 + 8) * 2;
     hipLaunchKernelGGL((expand_wide_kernel<PASS, ONE, F32>), grid, block, lds, s, a);
 }
 

@@ -397,6 +397,29 @@ def test_one_workspace_for_all_sizes(R):
         assert (err <= 4 * (np.sqrt(K) + 8) * U * (of_terms + np.abs(ref)) + 1e-37).all()
 
 
+@pytest.mark.parametrize("M,R", [(2, 16), (40, 16), (40, 128), (90, 64), (2500, 64), (2500, 136), (15001, 8)])
+@pytest.mark.parametrize("out", [BF16, F32], ids=["bf16", "f32"])
+def test_products_that_cancel(M, R, out):
+    """A x has 24 bits and B takes the difference of two ranks that agree in their first 16: what is left is exact,
+    on every path."""
+    N, K = 48, 64
+    rng = np.random.default_rng([M, R])
+    a = 1.0 + (2 * rng.integers(0, 64, 3) + 1) / 128.0               # eight bits each
+    A, B = np.zeros((1, R, K)), np.zeros((1, N, R))
+    A[0, 0, :3], A[0, 1, :2] = a, a[:2]
+    B[0, :, 0], B[0, :, 1] = 1.0, -1.0
+    x = np.zeros((M, K))
+    x[:, :3] = 1.0, 2.0 ** -8, 2.0 ** -16
+    bits = [to_dev_bf16(wl._to_bf16_bits(v.astype(np.float32))) for v in (x, A, B)]
+    y = torch.zeros(M, N, dtype=torch.float32 if out == F32 else torch.int16, device=DEV)
+    work = torch.empty(q.qlin_lora_workspace_bytes(M, N, K, 1, R), dtype=torch.uint8, device=DEV)
+    q.qlin_lora(M, N, K, 1, R, bits[0], K, torch.zeros(M, dtype=torch.int32, device=DEV), bits[1], bits[2], None, None,
+                None, 0, y, N, out, work)
+    torch.cuda.synchronize()
+    got = y.cpu().numpy() if out == F32 else f32_of(y.cpu().numpy().view(np.uint16))
+    assert (got == np.float32(a[2] * 2.0 ** -16)).all()
+
+
 def test_slices_of_a_wider_projection():
     """q, k, v: adapters for column ranges of one output, in place."""
     M, K, n, R, widths = 21, 256, 4, 16, (128, 64, 64)
