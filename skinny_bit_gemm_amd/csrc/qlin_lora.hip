@@ -392,8 +392,9 @@ __global__ __launch_bounds__(256, 4) void expand_kernel(LoraLaunch a) {
 // j has the columns NJ c + j), so that 16 lanes load and store 256 consecutive
 // bytes of a row of y, with the non-temporal policy (the next call's shrink
 // then does not wait for y's lines to leave the caches: 27 -> 21 us).  4096
-// rows, 10240 columns, rank 64: 44 us against 62 with B read by each wave and
-// half lines of y at a time, 55 with 128 bytes of a row.
+// rows, 10240 columns, rank 64: 45 us (with two terms of v 44, against 62 with
+// B read by each wave and half lines of y at a time, 55 with 128 bytes of a
+// row).
 //   PASS  8-rank chunks of B in a stage: 4 (max_rank <= 32) or 8
 //   ONE   a stage holds all ranks (max_rank <= 8 PASS): v stays in registers
 template <int PASS, bool ONE, bool F32>
@@ -738,10 +739,12 @@ static bool wide_tiles(int M, int N, int max_rank, bool f32) {
 // One launch for both products: where a row's A is small, so that reading it
 // in every workgroup costs less than a second launch.  In elements of A: a
 // row's, all rows', and what all workgroups read together.  Inside these
-// bounds 4.1 us against 7.3 (rank 16, 4096 x 2048, 1 row), 6.0 against 8.7
-// (rank 16, 10240 x 5120, 4 rows), 8.5 against 9.7 (rank 64, 4096 x 2048, 2);
-// outside 10.4 against 8.7 (rank 16, 10240 x 5120, 8 rows), 9.7 against 8.4
-// (rank 32, 4096 x 2048, 16).
+// bounds (times: in a replayed graph, an adapter for each row) 3.9 us against
+// 7.0 (rank 16, 4096 x 2048, 1 row), 6.1 against 8.4 (rank 16, 10240 x 5120, 4
+// rows), 8.5 against 8.6 (rank 64, 2048 x 2048, 2); outside 9.3 against 8.5
+// (rank 32, 10240 x 5120, 1 row), 12.5 against 8.7 (the same, 4 rows), 9.2
+// against 8.8 (rank 64, 2048 x 2048, 8).  Small ranks would gain from a few
+// rows more: 5.6 against 8.0 (rank 16, 4096 x 4096, 16).
 static bool few_rows(int M, int N, int K, int max_rank) {
     if (M > 16 || max_rank > 64) return false;
     const int lanes = max_rank <= 8 ? 1 : max_rank <= 16 ? 2 : max_rank <= 32 ? 4 : 8;   // of a column
@@ -760,10 +763,10 @@ void lora_plan(int M, int N, int K, int adapters, int max_rank, bool f32, LoraPl
     p->v_stride = (max_rank + 15) / 16 * 16;
     // K parts: two workgroups for each compute unit, two steps of 32 or more
     // for each wave.  At most four parts, two for wide tiles: every expand
-    // workgroup reads them all (4096 rows of rank 64: 70.1 us with two, 71.6
-    // with four).  Up to 32 rows eight, as many as let a wave's loads leave at
-    // once (16 rows of rank 64, K 12288: 15.5 us against 18.0; 64 rows of rank
-    // 64, K 12288: 36.1 against 33.3).
+    // workgroup reads them all (4096 rows of rank 64: four take 2 % longer than
+    // two).  Up to 32 rows eight, as many as let a wave's loads leave at once
+    // (rank 64, K 12288: 16 rows 14.3 us against 17.3 with four; 64 rows 33.8
+    // against 30.3).
     p->shrink_ct = p->wide && p->rt > 1 ? 2 : 1;
     p->sub_tiles = tile_rows / (16 * p->shrink_ct);
     const int steps = (K + 31) / 32, waves = kShrinkWaves;

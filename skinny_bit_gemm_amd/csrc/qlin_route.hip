@@ -6,7 +6,7 @@
 // model-coverage paragraph).
 //
 // Compiled with -fno-honor-nans: a maximum of doubles is then one instruction
-// instead of two or three (8192 tokens, 256 experts in 8 groups: 20.6 us
+// instead of two or three (8192 tokens, 256 experts in 8 groups: 20.4 us
 // against 22.1).  No NaN takes part: the caller's logits and biases are loaded
 // as integers, and a NaN among them has become -inf before it is a float
 // (number_or_closed); what an all-closed token leaves in sums is not selected.
@@ -668,20 +668,23 @@ __global__ __launch_bounds__(kPlaceThreads) void place_kernel(RouteLaunch a) {
 
 // --------------------------------------------------------------- launchers
 
-// How a call runs.
+// How a call runs (times: inside a replayed graph).
 //   rows   16 lanes per token (route_row) instead of a wave: past 8 tokens,
 //          where four tokens share an instruction (256 experts with a bias,
-//          16 tokens: 7.1 us against 9.3; 4 tokens: 7.0 against 6.3), and for
+//          16 tokens: 7.1 us against 9.6; 4 tokens: 7.0 against 6.4), and for
 //          a wave that would have a single number in a lane or a group at a
-//          time (256 in 8 groups, 1 token: 8.7 us against 10.6, 4096 tokens:
-//          16.9 against 24.8; 60 experts, 64 tokens: 4.7 against 8.9)
+//          time (256 in 8 groups, 1 token: 8.8 us against 10.8, 4096 tokens:
+//          16.4 against 24.6; 60 experts, 64 tokens: 4.5 against 8.5)
 //   once   one launch for all tokens by one workgroup: 64 of them with 16
-//          lanes each (32 with groups, whose choice is longer: 256 in 8, 64
-//          tokens: 21 us against 15.6), 16 with a wave each
+//          lanes each (64 tokens, 60 experts with a bias: 6.2 us against 8.5
+//          in two launches, 128: 8.4 against 8.8; 256: 7.0 against 8.4 without
+//          a bias, but 12.9 against 10.8 with one), 32 with groups, whose
+//          choice is longer (256 in 8, 64 tokens: 19.3 against 13.7), 16 with
+//          a wave each
 //   else   blocks of block_tokens tokens and a second launch: 16 tokens as
 //          long as there is a compute unit for each block (256 in 8 groups,
-//          1024 tokens: 17.7 us against 21.0 with 32), then 32 (8192: 22.1
-//          against 23.8 with 16); at most 512 blocks to sum over
+//          1024 tokens: 15.8 us against 19.7 with 32), then 32 (8192: 20.5
+//          against 21.8 with 16); at most 512 blocks to sum over
 constexpr int kMostBlocks = 512;
 
 RoutePlan route_plan(const qlin_router &r, int T) {
