@@ -174,9 +174,21 @@ static void launch_dispatch_token(const DispatchLaunch &a, hipStream_t s) {
 
 hipError_t launch_dispatch(int fmt, const DispatchLaunch &a, hipStream_t s) {
     if (fmt == FMT_BLOCK) {
-        const int64_t groups = (int64_t)a.T * (a.K / kGroup);
-        hipLaunchKernelGGL(dispatch_group_kernel, dim3((unsigned)((groups + 15) / 16)), dim3(256), 0, s, a);
-    } else if (fmt == FMT_I8) {
+        // a launch has fewer than 2^32 threads, 16 for each group
+        const int G = a.K / kGroup, most = (1 << 27) / G;
+        for (int t0 = 0; t0 < a.T; t0 += most) {
+            DispatchLaunch c = a;
+            c.T = a.T - t0 < most ? a.T - t0 : most;
+            c.x += (int64_t)t0 * a.ldx;
+            c.slots += (int64_t)t0 * a.topk;
+            const int64_t groups = (int64_t)c.T * G;
+            hipLaunchKernelGGL(dispatch_group_kernel, dim3((unsigned)((groups + 15) / 16)), dim3(256), 0, s, c);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
+    }
+    if (fmt == FMT_I8) {
         launch_dispatch_token<FMT_I8>(a, s);
     } else {
         launch_dispatch_token<FMT_FP8>(a, s);

@@ -379,6 +379,33 @@ def test_dispatch(fmt, T, topk, K, pad):
     assert np.array_equal(xs.cpu().numpy().view(np.uint32), want_s.view(np.uint32)), "scales differ"
 
 
+def test_dispatch_more_groups_than_a_launch_has_threads_for():
+    """2^20 tokens of 257 groups (64 GiB of x): 16 threads for each group are more than 2^32."""
+    T, K, fmt = 1 << 20, 32896, wl.BLOCK_FP8
+    if torch.cuda.mem_get_info()[0] < (80 << 30):
+        torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < (80 << 30):
+        pytest.skip("no 80 GiB of free memory")
+    part = (1 << 27) // (K // 128)                       # tokens of a launch
+    tokens = np.array([0, 1, part - 1, part, part + 1, 2 * part - 1, 2 * part, T - 1])
+    x = torch.empty(T * K, dtype=torch.int16, device=DEV)
+    rows = wl.activations(fmt, 4096, K, len(tokens))
+    slots = np.full(T, -1, dtype=np.int32)
+    for i, t in enumerate(tokens):
+        x[int(t) * K:(int(t) + 1) * K] = to_dev_bf16(rows[i])
+        slots[t] = len(tokens) - 1 - i
+    xq = guarded((len(tokens), K), torch.uint8, 0x55)
+    xs = guarded((len(tokens), K // 128), torch.float32, -1.0)
+    print(f"[dispatch] T={T} K={K}, {part} tokens a launch", flush=True)
+    q.qlin_dispatch_quantize(fmt, T, 1, K, x, K, to_dev(slots), len(tokens), xq, xs)
+    torch.cuda.synchronize()
+    check_guards(xq, xs, what="qlin_dispatch_quantize")
+    qa, sa = oracle.quant_act(fmt, rows)
+    assert np.array_equal(as_u8(xq)[::-1], qa.view(np.uint8)) and np.array_equal(xs.cpu().numpy()[::-1], sa)
+    del x
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------------- combine
 
 def bits_of(v):
