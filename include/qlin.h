@@ -465,6 +465,184 @@ qlin_status qlin_lora(int M, int N, int K, int adapters, int max_rank, const voi
                       qlin_out_type out_type, void *workspace, size_t ws_bytes, void *stream);
 qlin_status qlin_lora_workspace_bytes(int M, int N, int K, int adapters, int max_rank, size_t *bytes);
 
+/* ------------------------------------------------ attention over an 8-bit cache
+ *
+ * What stands between a layer's qkv and o projections: the norms and the
+ * rotation of the heads, a paged cache of keys and values in the 8-bit codes
+ * of the linear layers ("Building a High-Performance and Portable vLLM Linear
+ * Backend with Helion", section "Scope": amax / qmax scales, here one for each
+ * page and head), and the attention that reads it.
+ */
+
+/* The heads of a layer and their rotation.
+ *   q_heads, kv_heads  0..QLIN_MAX_HEADS each, at least one in all
+ *   head_dim           D, a multiple of 8 up to 256
+ *   rotary_dim         R, the first R channels of a head are rotated: a
+ *                      multiple of 8 (or 0: none) up to D
+ *   interleaved        0: channel i is turned with channel R / 2 + i;
+ *                      1: channel 2 i with 2 i + 1   (i = 0 .. R / 2 - 1)
+ *   positions          rows of the table of angles
+ *   eps                of the norms (finite, >= 0)                          */
+typedef struct {
+    int32_t q_heads;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t rotary_dim;
+    int32_t interleaved;
+    int32_t positions;
+    float eps;
+} qlin_rope;
+
+#define QLIN_MAX_HEADS 1024
+
+/* Norm of each query and key head, and its rotation, in one pass:
+ *   x' = x / sqrt(mean(x^2) + eps) * weight           (over a head's D channels)
+ *   (a, b) -> (a cos - b sin, b cos + a sin)          (x's pairs, see above)
+ *   q, k         [T, ldq], [T, ldk] of in_type (QLIN_OUT_BF16 or
+ *                QLIN_OUT_F32_ACC): head h at columns h D .., as qlin_linear
+ *                writes them; views into a wider qkv row are meant.  k and
+ *                k_out are not looked at where kv_heads is 0, nor q's pair
+ *                where q_heads is 0
+ *   q_norm, k_norm  fp32 [D], or NULL: no norm (weights 1 still norm)
+ *   cos_sin      fp32 [positions][R]: R / 2 cosines, then R / 2 sines of a
+ *                position's angles (not looked at where R is 0)
+ *   position     int32 [T] on the device.  A token whose position is outside
+ *                [0, positions) is padding: its outputs are left as they were
+ *                (not looked at where R is 0)
+ *   q_out, k_out [T, ldqo], [T, ldko] of out_type; q_out may be q and k_out k
+ *                (in place) where types and leading dimensions agree, and
+ *                overlap nothing else
+ * Sums and products are fp32, rounded once at the end.  T may be 0.
+ * Errors: QLIN_ERR_INVALID_ARG (a null pointer, a field or type out of range, in
+ * place with different types or leading dimensions), QLIN_ERR_SHAPE (T outside
+ * [0, 2^20]), QLIN_ERR_ALIGNMENT (a pointer or leading dimension that is not
+ * whole 16-byte units, or a leading dimension shorter than its heads). */
+qlin_status qlin_norm_rope(const qlin_rope *rope, int T, const void *q, int64_t ldq, const void *k, int64_t ldk,
+                           qlin_out_type in_type, const float *q_norm, const float *k_norm, const float *cos_sin,
+                           const int32_t *position, void *q_out, int64_t ldqo, void *k_out, int64_t ldko,
+                           qlin_out_type out_type, void *stream);
+
+/* One layer's cache: a pool of pages of page_tokens tokens, keys and values
+ * apart, each page and head with one scale.
+ *   format       QLIN_FP8_DYNAMIC (e4m3 codes) or QLIN_W8A8_INT8
+ *   kv_heads     1..QLIN_MAX_HEADS
+ *   head_dim     D: 64, 128, 192 or 256
+ *   page_tokens  16, 32, 64 or 128
+ *   pages        pages of the pool, 1..2^24
+ *   k, v         codes, qlin_cache_bytes' code_bytes each
+ *   k_scales, v_scales  fp32 [pages][kv_heads]
+ * The codes of a page and head are tiles of 16 tokens, of which every 64
+ * channels are 1 KiB in the order of the matrix cores: of a head's
+ * page_tokens x D bytes (pages and heads follow each other as [pages][heads]),
+ *   key    (token t, channel d) is byte 16 D (t / 16) + 1024 (d / 64) +
+ *          256 (d % 64 / 16) + 16 (t % 16) + d % 16,
+ *   value  (t, d) is byte 16 D (t / 16) + 1024 (d / 64) + 256 (t % 16 / 4) +
+ *          16 (d % 16) + 4 (d % 64 / 16) + t % 4.
+ * Nothing needs an initial value.                                            */
+typedef struct {
+    int32_t format;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t page_tokens;
+    int32_t pages;
+    void *k;
+    void *v;
+    float *k_scales;
+    float *v_scales;
+} qlin_cache;
+
+/* The sequences of a call.  Sequence s holds lengths[s] tokens, of which the
+ * last n = offsets[s + 1] - offsets[s] are the call's own: rows offsets[s] ..
+ * of q, k, v or y, at positions lengths[s] - n .. lengths[s] - 1.
+ *   sequences    0..2^20
+ *   tokens       T, rows of the call's tensors, 0..2^20; rows past
+ *                offsets[sequences] belong to no sequence and are left alone
+ *   max_pages    columns of the page table, 1..2^24
+ *   max_context  the longest sequence to be expected, 1..2^30: attention
+ *                spreads its work by it.  Longer ones are computed whole
+ *   offsets      int32 [sequences + 1], from 0, non-decreasing
+ *   lengths      int32 [sequences], with the call's own tokens
+ *   pages        int32 [sequences][max_pages]: token p is in page
+ *                pages[s][p / page_tokens]
+ * The arrays are on the device and read by the kernels, so a captured graph
+ * follows them.  Whatever they hold, nothing outside the tensors is read or
+ * written: offsets are taken as clamped into [0, T], and a token whose page is
+ * outside [0, cache.pages) or past max_pages, or whose position is outside
+ * [0, 2^30), is absent: it is not stored, not read back, and seen by no query.  Pages that a
+ * sequence has left behind its attention window may so be taken out (-1).      */
+typedef struct {
+    int32_t sequences;
+    int32_t tokens;
+    int32_t max_pages;
+    int32_t max_context;
+    const int32_t *offsets;
+    const int32_t *lengths;
+    const int32_t *pages;
+} qlin_sequences;
+
+/* Bytes of a cache's codes (of k and of v, each) and scales (likewise).  k, v
+ * and the scales of *cache are not looked at. */
+qlin_status qlin_cache_bytes(const qlin_cache *cache, size_t *code_bytes, size_t *scale_bytes);
+
+/* Stores the call's own tokens behind those that their sequences hold.
+ *   k, v   [T, ldk], [T, ldv] of type (QLIN_OUT_BF16 or QLIN_OUT_F32_ACC), head
+ *          h at columns h D ..
+ * For every page and head that gets tokens, s = max(s of the tokens before them
+ * in the page, amax of the new ones / qmax) becomes the scale; where it grew, the
+ * older codes are quantized again from the values they stood for, fp32(code x old
+ * s).  A page whose first token is stored starts anew, whatever it held.  Tokens
+ * behind a sequence's last (a draft that was not taken) can be stored over: give
+ * the shorter length; the scale does not shrink until the page starts anew.
+ * A page may be in several sequences' tables (a shared prefix) as long as no
+ * call stores into it; into one page, only one sequence of a call may store.
+ * Keys and values are finite.
+ * Errors: QLIN_ERR_INVALID_ARG (a null pointer, a field or type out of range),
+ * QLIN_ERR_SHAPE (a count out of range), QLIN_ERR_ALIGNMENT. */
+qlin_status qlin_cache_append(const qlin_cache *cache, const qlin_sequences *sequences, const void *k, int64_t ldk,
+                              const void *v, int64_t ldv, qlin_out_type type, void *stream);
+
+/* Reads the call's own tokens back: k and v as qlin_cache_append takes them,
+ * fp32(code x s), rounded once to type.  Rows of absent tokens are left as they
+ * were.  k or v may be NULL: not read.  Errors as qlin_cache_append. */
+qlin_status qlin_cache_read(const qlin_cache *cache, const qlin_sequences *sequences, void *k, int64_t ldk, void *v,
+                            int64_t ldv, qlin_out_type type, void *stream);
+
+/* Attention.
+ *   q_heads  a multiple of the cache's kv_heads, up to QLIN_MAX_HEADS: query
+ *            head h reads key head h / (q_heads / kv_heads)
+ *   causal   1: a token sees those up to its own position; 0: all of its
+ *            sequence's
+ *   window   0, or the number of latest positions that a token sees: those
+ *            after its own position - window
+ *   scale    of q . k (finite)                                              */
+typedef struct {
+    int32_t q_heads;
+    int32_t causal;
+    int32_t window;
+    float scale;
+} qlin_attention;
+
+/* y = softmax(scale q . k) v over the tokens that each of the call's own tokens
+ * sees, which the cache holds (its own too: qlin_cache_append comes first).
+ *   q   bf16 [T, ldq], head h at columns h D ..
+ *   y   [T, ldy] of out_type (QLIN_OUT_BF16 or QLIN_OUT_F32_ACC); not q.  A
+ *       token that sees nothing gets zeros
+ * Products with the codes are exact, sums and the softmax are fp32; the
+ * probabilities enter the second product with 16 bits of mantissa (24 where y is
+ * fp32); y is rounded once.  What lies in absent or unseen tokens' places, NaN
+ * codes among it, does not matter.
+ *   workspace  qlin_cache_attention_workspace_bytes(...) bytes (may be 0), of
+ *              counts and max_context only: as any of sequences, tokens and
+ *              max_context grows it never shrinks.  Needs no initial value.
+ *              Calls that overlap in time must not share it.
+ * Errors: QLIN_ERR_INVALID_ARG, QLIN_ERR_SHAPE (counts out of range, or more
+ * work than 2^31 - 1 workgroups), QLIN_ERR_ALIGNMENT, QLIN_ERR_WORKSPACE. */
+qlin_status qlin_cache_attention(const qlin_attention *attention, const qlin_cache *cache,
+                                 const qlin_sequences *sequences, const void *q, int64_t ldq, void *y, int64_t ldy,
+                                 qlin_out_type out_type, void *workspace, size_t ws_bytes, void *stream);
+qlin_status qlin_cache_attention_workspace_bytes(const qlin_attention *attention, const qlin_cache *cache,
+                                                 const qlin_sequences *sequences, size_t *bytes);
+
 /* Selection table.  qlin_load_table parses a text table (replacing any loaded
  * one; path NULL = the table installed next to the library); the table is
  * immutable afterwards, so lookups are thread-safe.  qlin_set_strict(1)

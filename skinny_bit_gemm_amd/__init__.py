@@ -34,7 +34,8 @@ EXPORTS = (
     "qlin_grouped_gemm", "qlin_grouped_select_variant", "qlin_grouped_workspace_bytes",
     "qlin_linear_scratch", "qlin_packed_weight_bytes", "qlin_pack_weight", "qlin_quantize_act_cfg",
     "qlin_route", "qlin_route_workspace_bytes", "qlin_dispatch_quantize", "qlin_combine", "qlin_lora",
-    "qlin_lora_workspace_bytes",
+    "qlin_lora_workspace_bytes", "qlin_norm_rope", "qlin_cache_bytes", "qlin_cache_append", "qlin_cache_read",
+    "qlin_cache_attention", "qlin_cache_attention_workspace_bytes",
 )
 # format flag: the weight codes are in the packed layout of qlin_pack_weight
 QLIN_PACKED_WEIGHTS = 0x100
@@ -99,6 +100,53 @@ _I = ctypes.c_int
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 
+QLIN_MAX_HEADS = 1024
+
+
+class qlin_rope(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("positions", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+def make_rope(q_heads, kv_heads, head_dim, rotary_dim, positions, interleaved=0, eps=1e-6) -> qlin_rope:
+    return qlin_rope(q_heads, kv_heads, head_dim, rotary_dim, interleaved, positions, eps)
+
+
+class qlin_cache(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("pages", ctypes.c_int32), ("k", _P), ("v", _P), ("k_scales", _P),
+                ("v_scales", _P)]
+
+
+def make_cache(fmt, kv_heads, head_dim, page_tokens, pages, k=None, v=None, k_scales=None, v_scales=None) -> qlin_cache:
+    """One layer's cache.  Of tensors the structure has the addresses and keeps
+    the tensors themselves alive; without them it serves qlin_cache_bytes."""
+    c = qlin_cache(fmt, kv_heads, head_dim, page_tokens, pages, _ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales))
+    c.tensors = (k, v, k_scales, v_scales)
+    return c
+
+
+class qlin_sequences(ctypes.Structure):
+    _fields_ = [("sequences", ctypes.c_int32), ("tokens", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("max_context", ctypes.c_int32), ("offsets", _P), ("lengths", _P), ("pages", _P)]
+
+
+def make_sequences(sequences, tokens, offsets, lengths, pages, max_pages, max_context) -> qlin_sequences:
+    """A call's sequences; keeps the tensors alive like make_cache."""
+    s = qlin_sequences(sequences, tokens, max_pages, max_context, _ptr(offsets), _ptr(lengths), _ptr(pages))
+    s.tensors = (offsets, lengths, pages)
+    return s
+
+
+class qlin_attention(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("causal", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+def make_attention(q_heads, scale, causal=1, window=0) -> qlin_attention:
+    return qlin_attention(q_heads, causal, window, scale)
+
 
 def lib():
     """Load libqlin.so (raises if it was not built)."""
@@ -139,6 +187,12 @@ def lib():
         L.qlin_combine.argtypes = [_I, _I, _I, _P, _I64, _I, _P, _P, _I, _P, _I64, _P, _I64, _I, _P]
         L.qlin_lora.argtypes = [_I, _I, _I, _I, _I, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _P, _I64, _I, _P, _SZ, _P]
         L.qlin_lora_workspace_bytes.argtypes = [_I, _I, _I, _I, _I, ctypes.POINTER(_SZ)]
+        L.qlin_norm_rope.argtypes = [_P, _I, _P, _I64, _P, _I64, _I, _P, _P, _P, _P, _P, _I64, _P, _I64, _I, _P]
+        L.qlin_cache_bytes.argtypes = [_P, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)]
+        L.qlin_cache_append.argtypes = [_P, _P, _P, _I64, _P, _I64, _I, _P]
+        L.qlin_cache_read.argtypes = [_P, _P, _P, _I64, _P, _I64, _I, _P]
+        L.qlin_cache_attention.argtypes = [_P, _P, _P, _P, _I64, _P, _I64, _I, _P, _SZ, _P]
+        L.qlin_cache_attention_workspace_bytes.argtypes = [_P, _P, _P, ctypes.POINTER(_SZ)]
         L.qlin_load_table.argtypes = [ctypes.c_char_p]
         L.qlin_set_strict.argtypes = [_I]
         L.qlin_table_entries.argtypes = []
@@ -344,6 +398,52 @@ def qlin_lora_workspace_bytes(M, N, K, adapters, max_rank) -> int:
     out = _SZ(0)
     st = lib().qlin_lora_workspace_bytes(M, N, K, adapters, max_rank, ctypes.byref(out))
     _check(st, "qlin_lora_workspace_bytes", True)
+    return int(out.value)
+
+
+def _ref(struct):
+    return ctypes.byref(struct) if struct is not None else None
+
+
+def qlin_norm_rope(rope, T, q, ldq, k, ldk, in_type, q_norm, k_norm, cos_sin, position, q_out, ldqo, k_out, ldko,
+                   out_type=QLIN_OUT_BF16, stream=None, raise_on_error=True):
+    st = lib().qlin_norm_rope(_ref(rope), T, _ptr(q), ldq, _ptr(k), ldk, in_type, _ptr(q_norm), _ptr(k_norm),
+                              _ptr(cos_sin), _ptr(position), _ptr(q_out), ldqo, _ptr(k_out), ldko, out_type,
+                              _stream(stream))
+    return _check(st, "qlin_norm_rope", raise_on_error)
+
+
+def qlin_cache_bytes(cache) -> tuple:
+    """(bytes of the codes, of the scales), of keys and of values each."""
+    codes, scales = _SZ(0), _SZ(0)
+    st = lib().qlin_cache_bytes(_ref(cache), ctypes.byref(codes), ctypes.byref(scales))
+    _check(st, "qlin_cache_bytes", True)
+    return int(codes.value), int(scales.value)
+
+
+def qlin_cache_append(cache, sequences, k, ldk, v, ldv, type=QLIN_OUT_BF16, stream=None, raise_on_error=True):
+    st = lib().qlin_cache_append(_ref(cache), _ref(sequences), _ptr(k), ldk, _ptr(v), ldv, type, _stream(stream))
+    return _check(st, "qlin_cache_append", raise_on_error)
+
+
+def qlin_cache_read(cache, sequences, k, ldk, v, ldv, type=QLIN_OUT_BF16, stream=None, raise_on_error=True):
+    st = lib().qlin_cache_read(_ref(cache), _ref(sequences), _ptr(k), ldk, _ptr(v), ldv, type, _stream(stream))
+    return _check(st, "qlin_cache_read", raise_on_error)
+
+
+def qlin_cache_attention(attention, cache, sequences, q, ldq, y, ldy, out_type=QLIN_OUT_BF16, workspace=None,
+                         ws_bytes=None, stream=None, raise_on_error=True):
+    if ws_bytes is None:
+        ws_bytes = _nbytes(workspace)
+    st = lib().qlin_cache_attention(_ref(attention), _ref(cache), _ref(sequences), _ptr(q), ldq, _ptr(y), ldy, out_type,
+                                    _ptr(workspace), ws_bytes, _stream(stream))
+    return _check(st, "qlin_cache_attention", raise_on_error)
+
+
+def qlin_cache_attention_workspace_bytes(attention, cache, sequences) -> int:
+    out = _SZ(0)
+    st = lib().qlin_cache_attention_workspace_bytes(_ref(attention), _ref(cache), _ref(sequences), ctypes.byref(out))
+    _check(st, "qlin_cache_attention_workspace_bytes", True)
     return int(out.value)
 
 

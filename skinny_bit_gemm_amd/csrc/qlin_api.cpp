@@ -771,6 +771,224 @@ qlin_status qlin_lora(int M, int N, int K, int adapters, int max_rank, const voi
     return hip_status(launch_lora(p, out_type == QLIN_OUT_F32_ACC, a, static_cast<hipStream_t>(stream)));
 }
 
+// ------------------------------------------------ attention over an 8-bit cache
+
+static bool finite(float v) { return v - v == 0.0f; }
+static bool flag_ok(int v) { return v == 0 || v == 1; }
+
+qlin_status qlin_norm_rope(const qlin_rope *rope, int T, const void *q, int64_t ldq, const void *k, int64_t ldk,
+                           qlin_out_type in_type, const float *q_norm, const float *k_norm, const float *cos_sin,
+                           const int32_t *position, void *q_out, int64_t ldqo, void *k_out, int64_t ldko,
+                           qlin_out_type out_type, void *stream) {
+    if (!rope || !row_type_ok(in_type) || !row_type_ok(out_type)) return QLIN_ERR_INVALID_ARG;
+    const int D = rope->head_dim, R = rope->rotary_dim;
+    if (rope->q_heads < 0 || rope->q_heads > QLIN_MAX_HEADS || rope->kv_heads < 0 || rope->kv_heads > QLIN_MAX_HEADS ||
+        rope->q_heads + rope->kv_heads == 0)
+        return QLIN_ERR_INVALID_ARG;
+    if (D < 8 || D > 256 || D % 8 != 0 || R < 0 || R > D || R % 8 != 0 || !flag_ok(rope->interleaved))
+        return QLIN_ERR_INVALID_ARG;
+    if ((R > 0 && rope->positions < 1) || !finite(rope->eps) || rope->eps < 0.0f) return QLIN_ERR_INVALID_ARG;
+    if (T < 0 || T > kMaxDim) return QLIN_ERR_SHAPE;
+    if (R > 0 && (!cos_sin || !position)) return QLIN_ERR_INVALID_ARG;
+    const int in = row_type_bytes(in_type), out = row_type_bytes(out_type);
+    if (rope->q_heads > 0) {
+        if (!q || !q_out || (q == q_out && (in_type != out_type || ldq != ldqo))) return QLIN_ERR_INVALID_ARG;
+        if (!ld_ok(ldq, rope->q_heads * D, in) || !ld_ok(ldqo, rope->q_heads * D, out) || !aligned16(q) || !aligned16(q_out))
+            return QLIN_ERR_ALIGNMENT;
+    }
+    if (rope->kv_heads > 0) {
+        if (!k || !k_out || (k == k_out && (in_type != out_type || ldk != ldko))) return QLIN_ERR_INVALID_ARG;
+        if (!ld_ok(ldk, rope->kv_heads * D, in) || !ld_ok(ldko, rope->kv_heads * D, out) || !aligned16(k) ||
+            !aligned16(k_out))
+            return QLIN_ERR_ALIGNMENT;
+    }
+    if (!aligned16(q_norm) || !aligned16(k_norm) || (R > 0 && (!aligned16(cos_sin) || !aligned4(position))))
+        return QLIN_ERR_ALIGNMENT;
+    if (T == 0) return QLIN_OK;
+    RopeLaunch a = {};
+    a.q = q;
+    a.k = k;
+    a.ldq = ldq;
+    a.ldk = ldk;
+    a.q_norm = q_norm;
+    a.k_norm = k_norm;
+    a.cos_sin = cos_sin;
+    a.position = position;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.ldqo = ldqo;
+    a.ldko = ldko;
+    a.T = T;
+    a.q_heads = rope->q_heads;
+    a.kv_heads = rope->kv_heads;
+    a.head_dim = D;
+    a.rotary_dim = R;
+    a.interleaved = rope->interleaved;
+    a.positions = rope->positions;
+    a.eps = rope->eps;
+    return hip_status(
+        launch_rope(in_type == QLIN_OUT_F32_ACC, out_type == QLIN_OUT_F32_ACC, a, static_cast<hipStream_t>(stream)));
+}
+
+static qlin_status check_cache(const qlin_cache *c) {
+    if (!c) return QLIN_ERR_INVALID_ARG;
+    if (c->format != QLIN_FP8_DYNAMIC && c->format != QLIN_W8A8_INT8) return QLIN_ERR_INVALID_ARG;
+    if (c->kv_heads < 1 || c->kv_heads > QLIN_MAX_HEADS) return QLIN_ERR_INVALID_ARG;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 192 && c->head_dim != 256) return QLIN_ERR_INVALID_ARG;
+    if (c->page_tokens != 16 && c->page_tokens != 32 && c->page_tokens != 64 && c->page_tokens != 128)
+        return QLIN_ERR_INVALID_ARG;
+    if (c->pages < 1 || c->pages > 1 << 24) return QLIN_ERR_SHAPE;
+    return QLIN_OK;
+}
+
+static qlin_status check_counts(const qlin_sequences *s) {
+    if (!s) return QLIN_ERR_INVALID_ARG;
+    if (s->sequences < 0 || s->sequences > kMaxDim || s->tokens < 0 || s->tokens > kMaxDim) return QLIN_ERR_SHAPE;
+    if (s->max_pages < 1 || s->max_pages > 1 << 24 || s->max_context < 1 || s->max_context > 1 << 30) return QLIN_ERR_SHAPE;
+    return QLIN_OK;
+}
+
+// The arrays of a cache and of a call's sequences.
+static qlin_status check_arrays(const qlin_cache *c, const qlin_sequences *s) {
+    if (!c->k || !c->v || !c->k_scales || !c->v_scales || !s->offsets || !s->lengths || !s->pages)
+        return QLIN_ERR_INVALID_ARG;
+    if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(c->k_scales) || !aligned4(c->v_scales) || !aligned4(s->offsets) ||
+        !aligned4(s->lengths) || !aligned4(s->pages))
+        return QLIN_ERR_ALIGNMENT;
+    return QLIN_OK;
+}
+
+static CacheArgs cache_args(const qlin_cache *c, const qlin_sequences *s) {
+    CacheArgs a = {};
+    a.k = static_cast<uint8_t *>(c->k);
+    a.v = static_cast<uint8_t *>(c->v);
+    a.k_scales = c->k_scales;
+    a.v_scales = c->v_scales;
+    a.heads = c->kv_heads;
+    a.pages = c->pages;
+    a.page_shift = c->page_tokens == 16 ? 4 : c->page_tokens == 32 ? 5 : c->page_tokens == 64 ? 6 : 7;
+    a.B = s->sequences;
+    a.T = s->tokens;
+    a.max_pages = s->max_pages;
+    a.offsets = s->offsets;
+    a.lengths = s->lengths;
+    a.table = s->pages;
+    return a;
+}
+
+qlin_status qlin_cache_bytes(const qlin_cache *cache, size_t *code_bytes, size_t *scale_bytes) {
+    if (!code_bytes || !scale_bytes) return QLIN_ERR_INVALID_ARG;
+    const qlin_status st = check_cache(cache);
+    if (st != QLIN_OK) return st;
+    *scale_bytes = (size_t)cache->pages * cache->kv_heads * sizeof(float);
+    *code_bytes = (size_t)cache->pages * cache->kv_heads * cache->page_tokens * cache->head_dim;
+    return QLIN_OK;
+}
+
+qlin_status qlin_cache_append(const qlin_cache *cache, const qlin_sequences *sequences, const void *k, int64_t ldk,
+                              const void *v, int64_t ldv, qlin_out_type type, void *stream) {
+    qlin_status st = check_cache(cache);
+    if (st == QLIN_OK) st = check_counts(sequences);
+    if (st != QLIN_OK) return st;
+    if (!row_type_ok(type) || !k || !v) return QLIN_ERR_INVALID_ARG;
+    st = check_arrays(cache, sequences);
+    if (st != QLIN_OK) return st;
+    const int width = cache->kv_heads * cache->head_dim, bytes = row_type_bytes(type);
+    if (!ld_ok(ldk, width, bytes) || !ld_ok(ldv, width, bytes) || !aligned16(k) || !aligned16(v)) return QLIN_ERR_ALIGNMENT;
+    RowsLaunch a = {};
+    a.c = cache_args(cache, sequences);
+    a.k = const_cast<void *>(k);
+    a.v = const_cast<void *>(v);
+    a.ldk = ldk;
+    a.ldv = ldv;
+    a.units = (int)cache_units(a.c);
+    if (a.units == 0) return QLIN_OK;
+    return hip_status(launch_append(cache->format, type == QLIN_OUT_F32_ACC, cache->head_dim, a,
+                                    static_cast<hipStream_t>(stream)));
+}
+
+qlin_status qlin_cache_read(const qlin_cache *cache, const qlin_sequences *sequences, void *k, int64_t ldk, void *v,
+                            int64_t ldv, qlin_out_type type, void *stream) {
+    qlin_status st = check_cache(cache);
+    if (st == QLIN_OK) st = check_counts(sequences);
+    if (st != QLIN_OK) return st;
+    if (!row_type_ok(type) || (!k && !v)) return QLIN_ERR_INVALID_ARG;
+    st = check_arrays(cache, sequences);
+    if (st != QLIN_OK) return st;
+    const int width = cache->kv_heads * cache->head_dim, bytes = row_type_bytes(type);
+    if ((k && !ld_ok(ldk, width, bytes)) || (v && !ld_ok(ldv, width, bytes)) || !aligned16(k) || !aligned16(v))
+        return QLIN_ERR_ALIGNMENT;
+    RowsLaunch a = {};
+    a.c = cache_args(cache, sequences);
+    a.k = k;
+    a.v = v;
+    a.ldk = ldk;
+    a.ldv = ldv;
+    a.units = (int)cache_units(a.c);
+    if (a.units == 0) return QLIN_OK;
+    return hip_status(launch_read(cache->format, type == QLIN_OUT_F32_ACC, cache->head_dim, a,
+                                  static_cast<hipStream_t>(stream)));
+}
+
+// Checks an attention call's sizes and plans it.
+static qlin_status plan_attention(const qlin_attention *t, const qlin_cache *cache, const qlin_sequences *s,
+                                  AttentionPlan *p) {
+    if (!t) return QLIN_ERR_INVALID_ARG;
+    qlin_status st = check_cache(cache);
+    if (st == QLIN_OK) st = check_counts(s);
+    if (st != QLIN_OK) return st;
+    if (t->q_heads < 1 || t->q_heads > QLIN_MAX_HEADS || t->q_heads % cache->kv_heads != 0) return QLIN_ERR_INVALID_ARG;
+    if (!flag_ok(t->causal) || t->window < 0 || !finite(t->scale)) return QLIN_ERR_INVALID_ARG;
+    *p = attention_plan(s->sequences, s->tokens, s->max_context, cache->kv_heads, t->q_heads / cache->kv_heads,
+                        cache->head_dim);
+    // a grid's first dimension has fewer than 2^24 workgroups of 256 threads
+    return p->units >= 1 << 24 ? QLIN_ERR_SHAPE : QLIN_OK;
+}
+
+qlin_status qlin_cache_attention_workspace_bytes(const qlin_attention *attention, const qlin_cache *cache,
+                                                 const qlin_sequences *sequences, size_t *bytes) {
+    if (!bytes) return QLIN_ERR_INVALID_ARG;
+    AttentionPlan p = {};
+    const qlin_status st = plan_attention(attention, cache, sequences, &p);
+    if (st != QLIN_OK) return st;
+    *bytes = p.ws_bytes;
+    return QLIN_OK;
+}
+
+qlin_status qlin_cache_attention(const qlin_attention *attention, const qlin_cache *cache,
+                                 const qlin_sequences *sequences, const void *q, int64_t ldq, void *y, int64_t ldy,
+                                 qlin_out_type out_type, void *workspace, size_t ws_bytes, void *stream) {
+    AttentionPlan p = {};
+    qlin_status st = plan_attention(attention, cache, sequences, &p);
+    if (st != QLIN_OK) return st;
+    if (!row_type_ok(out_type) || !q || !y || q == y) return QLIN_ERR_INVALID_ARG;
+    st = check_arrays(cache, sequences);
+    if (st != QLIN_OK) return st;
+    const int width = attention->q_heads * cache->head_dim;
+    if (!ld_ok(ldq, width, 2) || !ld_ok(ldy, width, row_type_bytes(out_type)) || !aligned16(q) || !aligned16(y))
+        return QLIN_ERR_ALIGNMENT;
+    if (p.ws_bytes && (!workspace || ws_bytes < p.ws_bytes)) return QLIN_ERR_WORKSPACE;
+    if (p.ws_bytes && !aligned16(workspace)) return QLIN_ERR_ALIGNMENT;
+    if (p.units == 0) return QLIN_OK;
+    AttentionLaunch a = {};
+    a.c = cache_args(cache, sequences);
+    a.q = static_cast<const uint16_t *>(q);
+    a.ldq = ldq;
+    a.y = y;
+    a.ldy = ldy;
+    a.group = attention->q_heads / cache->kv_heads;
+    a.causal = attention->causal;
+    a.window = attention->window;
+    a.scale = (float)(attention->scale * 1.4426950408889634);
+    a.units = (int)p.units;
+    a.parts = p.parts;
+    a.chunk = p.chunk;
+    a.part_o = static_cast<float *>(workspace);
+    a.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + p.ml_at);
+    return hip_status(launch_attention(cache->format, out_type == QLIN_OUT_F32_ACC, cache->head_dim, p, a,
+                                       static_cast<hipStream_t>(stream)));
+}
+
 struct qlin_graph_s {
     hipGraphExec_t exec;
 };

@@ -168,6 +168,57 @@ struct LoraLaunch {
     int *tile_count, *perm, *place;
 };
 
+// ---- attention over an 8-bit cache
+struct RopeLaunch {
+    const void *q, *k;
+    int64_t ldq, ldk;
+    const float *q_norm, *k_norm, *cos_sin;
+    const int *position;
+    void *q_out, *k_out;
+    int64_t ldqo, ldko;
+    int T, q_heads, kv_heads, head_dim, rotary_dim, interleaved, positions;
+    float eps;
+    int steps;                 // head groups that a workgroup takes one after another
+};
+
+// A cache and a call's sequences as the kernels take them.
+struct CacheArgs {
+    uint8_t *k, *v;
+    float *k_scales, *v_scales;
+    int heads, pages, page_shift;
+    int B, T, max_pages;
+    const int *offsets, *lengths, *table;
+};
+
+struct RowsLaunch {            // append and read
+    CacheArgs c;
+    void *k, *v;
+    int64_t ldk, ldv;
+    int units;                 // (sequence, touched page) pairs, at most
+};
+
+// How qlin_cache_attention runs (qlin_attention.hip).
+struct AttentionPlan {
+    int rows;                  // (token, head of the group) rows of a workgroup
+    int64_t units;             // row tiles, at most
+    int parts, chunk;          // parts of a sequence's tokens, tokens of each
+    size_t ml_at, ws_bytes;
+};
+
+struct AttentionLaunch {
+    CacheArgs c;
+    const uint16_t *q;
+    int64_t ldq;
+    void *y;
+    int64_t ldy;
+    int group;                 // query heads of a key head
+    int causal, window;
+    float scale;               // times log2(e)
+    int units, parts, chunk;
+    float *part_o;             // [part][unit][head][rows][D]
+    float2 *part_ml;           // [part][unit][head][rows]: maximum (log2), sum
+};
+
 // Host-side selection table (qlin_table.cpp).
 qlin_status table_lookup(qlin_format fmt, int M, int N, int K, qlin_config *out, bool *found);
 qlin_status table_nearest(qlin_format fmt, int M, int N, int K, qlin_config *out, bool *found);
@@ -197,6 +248,13 @@ hipError_t launch_dispatch(int fmt, const DispatchLaunch &a, hipStream_t s);
 hipError_t launch_combine(bool h32, bool y32, const CombineLaunch &a, hipStream_t s);
 void lora_plan(int M, int N, int K, int adapters, int max_rank, bool f32, LoraPlan *p);
 hipError_t launch_lora(const LoraPlan &p, bool f32, const LoraLaunch &a, hipStream_t s);
+hipError_t launch_rope(bool in32, bool out32, const RopeLaunch &a, hipStream_t s);
+int64_t cache_units(const CacheArgs &c);
+hipError_t launch_append(int fmt, bool f32, int head_dim, const RowsLaunch &a, hipStream_t s);
+hipError_t launch_read(int fmt, bool f32, int head_dim, const RowsLaunch &a, hipStream_t s);
+AttentionPlan attention_plan(int sequences, int tokens, int max_context, int kv_heads, int group, int head_dim);
+hipError_t launch_attention(int fmt, bool f32, int head_dim, const AttentionPlan &p, const AttentionLaunch &a,
+                            hipStream_t s);
 bool gemm_variant_exists(int fmt, bool swap, int tile_m, int nr, int xc);
 // this device's static scratch array (kScratchBytes, zero between calls);
 // see qlin_linear_scratch
