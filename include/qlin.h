@@ -635,8 +635,8 @@ typedef struct {
  *              counts and max_context only: as any of sequences, tokens and
  *              max_context grows it never shrinks.  Needs no initial value.
  *              Calls that overlap in time must not share it.
- * Errors: QLIN_ERR_INVALID_ARG, QLIN_ERR_SHAPE (counts out of range, or more
- * work than 2^31 - 1 workgroups), QLIN_ERR_ALIGNMENT, QLIN_ERR_WORKSPACE. */
+ * Errors: QLIN_ERR_INVALID_ARG (a null pointer, a field or type out of range),
+ * QLIN_ERR_SHAPE (a count out of range), QLIN_ERR_ALIGNMENT, QLIN_ERR_WORKSPACE. */
 qlin_status qlin_cache_attention(const qlin_attention *attention, const qlin_cache *cache,
                                  const qlin_sequences *sequences, const void *q, int64_t ldq, void *y, int64_t ldy,
                                  qlin_out_type out_type, void *workspace, size_t ws_bytes, void *stream);

@@ -941,8 +941,7 @@ static qlin_status plan_attention(const qlin_attention *t, const qlin_cache *cac
     if (!flag_ok(t->causal) || t->window < 0 || !finite(t->scale)) return QLIN_ERR_INVALID_ARG;
     *p = attention_plan(s->sequences, s->tokens, s->max_context, cache->kv_heads, t->q_heads / cache->kv_heads,
                         cache->head_dim);
-    // a grid's first dimension has fewer than 2^24 workgroups of 256 threads
-    return p->units >= 1 << 24 ? QLIN_ERR_SHAPE : QLIN_OK;
+    return QLIN_OK;
 }
 
 qlin_status qlin_cache_attention_workspace_bytes(const qlin_attention *attention, const qlin_cache *cache,
@@ -969,7 +968,7 @@ qlin_status qlin_cache_attention(const qlin_attention *attention, const qlin_cac
         return QLIN_ERR_ALIGNMENT;
     if (p.ws_bytes && (!workspace || ws_bytes < p.ws_bytes)) return QLIN_ERR_WORKSPACE;
     if (p.ws_bytes && !aligned16(workspace)) return QLIN_ERR_ALIGNMENT;
-    if (p.units == 0) return QLIN_OK;
+    if (p.workers == 0) return QLIN_OK;
     AttentionLaunch a = {};
     a.c = cache_args(cache, sequences);
     a.q = static_cast<const uint16_t *>(q);
@@ -980,11 +979,11 @@ qlin_status qlin_cache_attention(const qlin_attention *attention, const qlin_cac
     a.causal = attention->causal;
     a.window = attention->window;
     a.scale = (float)(attention->scale * 1.4426950408889634);
-    a.units = (int)p.units;
-    a.parts = p.parts;
-    a.chunk = p.chunk;
+    a.workers = p.workers;
+    a.whole = p.whole;
     a.part_o = static_cast<float *>(workspace);
     a.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + p.ml_at);
+    a.cuts = reinterpret_cast<AttentionCut *>(static_cast<char *>(workspace) + p.cuts_at);
     return hip_status(launch_attention(cache->format, out_type == QLIN_OUT_F32_ACC, cache->head_dim, p, a,
                                        static_cast<hipStream_t>(stream)));
 }

@@ -28,12 +28,13 @@ typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 constexpr int kTile = 16;
 constexpr int kWaves = 4;
-constexpr int kMaxParts = 256;
+constexpr int kMostWorkers = 768;
 
 // four codes of a word as bf16 (exact)
 template <int FMT>
 __device__ __forceinline__ uint2 bf16_codes(uint32_t w) {
     if constexpr (FMT == FMT_I8) {
+        asm("" : "+v"(w));      // one register until here: its bytes are not taken apart when it is loaded
         const uint32_t f0 = __float_as_uint((float)(int8_t)w), f1 = __float_as_uint((float)(int8_t)(w >> 8));
         const uint32_t f2 = __float_as_uint((float)(int8_t)(w >> 16)), f3 = __float_as_uint((float)(int8_t)(w >> 24));
         return make_uint2(__builtin_amdgcn_perm(f1, f0, 0x07060302u), __builtin_amdgcn_perm(f3, f2, 0x07060302u));
@@ -47,6 +48,27 @@ template <int FMT>
 __device__ __forceinline__ v8bf operand(uint32_t lo, uint32_t hi) {
     const uint2 a = bf16_codes<FMT>(lo), b = bf16_codes<FMT>(hi);
     return __builtin_bit_cast(v8bf, v4u{a.x, a.y, b.x, b.y});
+}
+
+typedef float v2f __attribute__((ext_vector_type(2)));
+
+// eight probabilities as TERMS operands, whose sum has 8 bits of mantissa from each
+template <int TERMS>
+__device__ __forceinline__ void terms(v4f a, v4f b, v8bf (&p)[TERMS]) {
+    v2f rest[4] = {{a[0], a[1]}, {a[2], a[3]}, {b[0], b[1]}, {b[2], b[3]}};
+#pragma unroll
+    for (int n = 0; n < TERMS; ++n) {
+        v4u w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest[i], v2bf));     // nearest even
+            if (n + 1 < TERMS) {
+                rest[i][0] -= bf16_lo(w[i]);
+                rest[i][1] -= bf16_hi(w[i]);
+            }
+        }
+        p[n] = __builtin_bit_cast(v8bf, w);
+    }
 }
 
 // over the four lanes l, l ^ 16, l ^ 32, l ^ 48 of a query row
@@ -63,13 +85,13 @@ __device__ __forceinline__ float row_sum(float v) {
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// The rows of a workgroup (unit) and the tokens that they see.
+// A unit of work: a tile of a sequence's query rows (token x group + head of the
+// group), and the tokens that they see.
 struct Unit {
-    int seq, row0, rows;       // first row (token x group + head of the group), rows that are there
+    int seq, row0, rows;       // first row, rows that are there
     Sequence q;
     int lo, up;                // tokens that any row sees
     int all_lo, all_up;        // tokens that every row sees
-    int tile0, tiles;          // tiles of 16 tokens of [lo, up)
 };
 
 struct Seen {
@@ -83,31 +105,18 @@ __device__ __forceinline__ Seen seen_by(const AttentionLaunch &a, const Sequence
     return s;
 }
 
-template <int ROWS>
-__device__ __forceinline__ bool unit_of(const AttentionLaunch &a, Unit *u) {
-    int within;
-    u->seq = unit_sequence(
-        a.c, blockIdx.x,
-        [&](const Sequence &q) { return (int)min(((int64_t)q.n * a.group + ROWS - 1) / ROWS, (int64_t)1 << 24); },
-        &within);
-    if (u->seq < 0) return false;
-    u->q = sequence_at(a.c, u->seq);
-    u->row0 = within * ROWS;
-    u->rows = min(ROWS, u->q.n * a.group - u->row0);
-    const Seen first = seen_by(a, u->q, u->row0 / a.group), last = seen_by(a, u->q, (u->row0 + u->rows - 1) / a.group);
-    u->lo = first.lo;
-    u->up = last.up;
-    u->all_lo = last.lo;
-    u->all_up = first.up;
-    u->tile0 = u->lo / kTile;
-    u->tiles = u->up > u->lo ? (u->up + kTile - 1) / kTile - u->tile0 : 0;
-    return true;
-}
-
-// parts that a unit's tokens are in (one at least)
-__device__ __forceinline__ int parts_of(const AttentionLaunch &a, const Unit &u) {
-    const int per = a.chunk / kTile;
-    return max(1, min(a.parts, (u.tiles + per - 1) / per));
+__device__ __forceinline__ Unit unit_at(const AttentionLaunch &a, int seq, const Sequence &q, int tile, int tile_rows) {
+    Unit u;
+    u.seq = seq;
+    u.q = q;
+    u.row0 = tile * tile_rows;
+    u.rows = min(tile_rows, q.n * a.group - u.row0);
+    const Seen first = seen_by(a, q, u.row0 / a.group), last = seen_by(a, q, (u.row0 + u.rows - 1) / a.group);
+    u.lo = first.lo;
+    u.up = last.up;
+    u.all_lo = last.lo;
+    u.all_up = first.up;
+    return u;
 }
 
 template <bool F32>
@@ -126,24 +135,142 @@ __device__ __forceinline__ int64_t row_at(const AttentionLaunch &a, const Unit &
     return (int64_t)(u.q.first + token) * ld + (int64_t)(head * a.group + r - token * a.group) * D;
 }
 
+// a value that all lanes have, in scalar registers
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+    return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)v) |
+                     (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32);
+}
+
+// ------------------------------------------------------------ few rows a sequence
+//
+// The cached tokens of every unit, for every key head, are one long line of steps
+// of STEP tokens, and each workgroup takes an equal share of it: the codes are
+// what bounds the call, so all compute units read the same number of them,
+// however the lengths differ.  A unit that lies in one share is written at once;
+// of one that is cut, each workgroup leaves its sums, and join_kernel adds them.
+// Where a context is expected to be no longer than a step, a unit is one step of
+// any length: none is cut, and the second launch is left out.
+
+// a / b, both not negative; 64-bit divisions take some 100 instructions
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return (a | b) >> 32 == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+struct SequenceWork {
+    int tiles, tile0, steps;       // row tiles; first tile of 16 tokens, and steps of each
+    __device__ __forceinline__ int64_t all() const { return (int64_t)tiles * steps; }
+};
+template <int ROWS, int STEP>
+__device__ __forceinline__ SequenceWork sequence_work(const AttentionLaunch &a, const Sequence &q) {
+    SequenceWork w = {0, 0, 0};
+    if (q.n == 0) return w;
+    const Seen first = seen_by(a, q, 0), last = seen_by(a, q, q.n - 1);
+    w.tiles = (q.n * a.group + ROWS - 1) / ROWS;
+    w.tile0 = first.lo / kTile;
+    w.steps = last.up > first.lo && !a.whole ? (last.up - w.tile0 * kTile + STEP - 1) / STEP : 1;
+    return w;
+}
+
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ int64_t add_dpp(int64_t v) {
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROW_MASK, 0xF, ROW_MASK == 0xF);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(v >> 32), CTRL, ROW_MASK, 0xF, ROW_MASK == 0xF);
+    return v + (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+// What the workgroups find their shares with.
+struct Shares {
+    int64_t sums[256];             // steps (for one head) of the sequences up to and with each thread's
+    int64_t waves[4];
+    Sequence first[256];           // each thread's first sequence
+};
+
+// Threads have B / 256 sequences each, in order.
+template <int ROWS, int STEP>
+__device__ __forceinline__ void sum_steps(const AttentionLaunch &a, Shares &sh) {
+    const int tid = threadIdx.x, per = (a.c.B + 255) / 256;
+    int64_t v = 0;
+    for (int s = tid * per; s < min(a.c.B, (tid + 1) * per); ++s) {
+        const Sequence q = sequence_at(a.c, s);
+        v += sequence_work<ROWS, STEP>(a, q).all();
+        if (s == tid * per) sh.first[tid] = q;
+    }
+    v = add_dpp<0x111, 0xF>(v);    // as wave_scan
+    v = add_dpp<0x112, 0xF>(v);
+    v = add_dpp<0x114, 0xF>(v);
+    v = add_dpp<0x118, 0xF>(v);
+    v = add_dpp<0x142, 0xA>(v);
+    v = add_dpp<0x143, 0xC>(v);
+    if ((tid & 63) == 63) sh.waves[tid >> 6] = v;
+    __syncthreads();
+    for (int w = 0; w < tid >> 6; ++w) v += sh.waves[w];
+    sh.sums[tid] = v;
+    __syncthreads();
+}
+
+__device__ __forceinline__ Sequence uniform(const Sequence &q) {
+    Sequence r;
+    r.first = __builtin_amdgcn_readfirstlane(q.first);
+    r.n = __builtin_amdgcn_readfirstlane(q.n);
+    r.start = __builtin_amdgcn_readfirstlane(q.start);
+    r.length = __builtin_amdgcn_readfirstlane(q.length);
+    return r;
+}
+
 // RT: tiles of 16 query rows; all waves have the same rows and take groups of NT
 // tiles of tokens in turn, so a code is read and converted once for all rows.
 template <int D, int FMT, int TERMS, int RT>
-__global__ __launch_bounds__(64 * kWaves) void attention_kernel(AttentionLaunch a) {
+__global__ __launch_bounds__(64 * kWaves, RT == 1 ? 2 : 1) void attention_kernel(AttentionLaunch a) {
     constexpr int ROWS = 16 * RT, J = D / 64, DT = D / 16, NT = D <= 128 ? 4 : 2;
+    constexpr int STEP = kWaves * NT * kTile;
     constexpr int AHEAD = 64 / NT;              // groups whose pages a wave looks up at once
     constexpr bool F32 = TERMS == 3;
     __shared__ float merge[kWaves][16][D + 4];
     __shared__ float2 merge_ml[kWaves][16];
     const CacheArgs &c = a.c;
-    const int head = blockIdx.y, part = blockIdx.z;
-    Unit u;
-    if (!unit_of<ROWS>(a, &u)) return;
-    const int parts = parts_of(a, u);
-    if (part >= parts) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, col = lane & 15;
-    const int tile_begin = u.tile0 + part * (a.chunk / kTile);
-    const int tile_end = part == a.parts - 1 ? u.tile0 + u.tiles : min(u.tile0 + u.tiles, tile_begin + a.chunk / kTile);
+    const int worker = blockIdx.x;
+    const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+    // this worker's share
+    Shares &sh = *reinterpret_cast<Shares *>(merge);
+    static_assert(sizeof(Shares) <= sizeof(merge), "they share the LDS");
+    sum_steps<ROWS, STEP>(a, sh);
+    const int64_t per_head = uniform(sh.sums[255]), steps = per_head * c.heads;
+    const int64_t share = quotient(steps + a.workers - 1, a.workers);
+    int64_t at = worker * share;
+    const int64_t end = min(steps, at + share);
+    if (threadIdx.x == 0 && !a.whole) a.cuts[worker].last = -1;
+    if (at >= end) return;
+    int head = (int)quotient(at, per_head), seq;
+    int64_t begin = (int64_t)head * per_head;   // of the sequence, and then of the unit
+    Sequence sq;
+    {
+        int block = 0;                          // the thread whose sequences have it
+#pragma unroll
+        for (int i = 0; i < 4; ++i) block += __popcll(__ballot(sh.sums[64 * i + lane] <= at - begin));
+        seq = block * ((c.B + 255) / 256);
+        begin += block ? uniform(sh.sums[block - 1]) : 0;
+        sq = uniform(sh.first[block]);
+    }
+    __syncthreads();                            // their place is used again
+    SequenceWork sw = sequence_work<ROWS, STEP>(a, sq);
+    while (begin + sw.all() <= at) {
+        begin += sw.all();
+        sq = sequence_at(c, ++seq);
+        sw = sequence_work<ROWS, STEP>(a, sq);
+    }
+    int tile = sw.tiles > 1 ? (int)quotient(at - begin, sw.steps) : 0;
+    begin += (int64_t)tile * sw.steps;
+
+    while (true) {
+    const Unit u = unit_at(a, seq, sq, tile, ROWS);
+    const int64_t unit_end = begin + sw.steps, stop = min(unit_end, end);
+    const bool starts = at == begin, whole = starts && stop == unit_end;
+    // tiles of 16 tokens that this worker has of the unit, and that any row sees
+    const int tile_begin = max(sw.tile0 + (int)(at - begin) * (STEP / kTile), u.lo / kTile);
+    int tile_end = u.up > u.lo ? (u.up + kTile - 1) / kTile : 0;
+    if (!a.whole) tile_end = min(tile_end, sw.tile0 + (int)(stop - begin) * (STEP / kTile));
 
     v8bf q[RT][2 * J];
     Seen seen[RT];
@@ -168,54 +295,88 @@ __global__ __launch_bounds__(64 * kWaves) void attention_kernel(AttentionLaunch 
     }
 
     const int tile_shift = c.page_shift - 4;    // tiles of a page, log2
-    const int groups = (tile_end - tile_begin + NT - 1) / NT;
+    const int groups = tile_end > tile_begin ? (tile_end - tile_begin + NT - 1) / NT : 0;
     int page = -1;
     float ks = 0.0f, vs = 0.0f;
-    for (int gi = wave, k = 0; gi < groups; gi += kWaves, ++k) {
-        if (k % AHEAD == 0) {                   // pages and scales of the next groups, a tile a lane
+    int there[NT];                              // pages of the tiles whose codes are on their way
+    float kf[NT], vf[NT];
+    int64_t tile_at[NT];                        // where they are, in tiles
+    // a group's pages: every AHEAD groups a wave looks them up, a tile a lane
+    auto find = [&](int gi, int k) {
+        if (k % AHEAD == 0) {
             const int tile = tile_begin + (gi + kWaves * (lane / NT)) * NT + lane % NT;
             page = tile < tile_end ? pool_page(c, u.seq, tile >> tile_shift) : -1;
             const int64_t slot = (int64_t)max(page, 0) * c.heads + head;
             ks = c.k_scales[slot];
             vs = c.v_scales[slot];
         }
-        const int lane0 = (k % AHEAD) * NT, tile0 = tile_begin + gi * NT;
-        uint4 kc[NT][J], vc[NT][J];
-        float kf[NT], vf[NT];
-        bool edge = tile0 * kTile < u.all_lo || (tile0 + NT) * kTile > u.all_up;
-        int there[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            there[t] = __builtin_amdgcn_readlane(page, lane0 + t);
-            edge |= there[t] < 0;
-            kf[t] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), lane0 + t)) * a.scale;
-            vf[t] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs), lane0 + t));
-            const int64_t tile = (((int64_t)max(there[t], 0) * c.heads + head) << tile_shift) +
-                                 ((tile0 + t) & ((1 << tile_shift) - 1));
-            const uint4 *kp = reinterpret_cast<const uint4 *>(c.k + tile * (kTile * D)) + lane;
-            const uint4 *vp = reinterpret_cast<const uint4 *>(c.v + tile * (kTile * D)) + lane;
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                kc[t][j] = kp[64 * j];
-                vc[t][j] = vp[64 * j];
-            }
+            there[t] = __builtin_amdgcn_readlane(page, (k % AHEAD) * NT + t);
+            tile_at[t] = (((int64_t)max(there[t], 0) * c.heads + head) << tile_shift) +
+                         ((tile_begin + gi * NT + t) & ((1 << tile_shift) - 1));
         }
-        // scores: row token 4 g + r of tile t, column the lane's query row
+    };
+    auto find_scales = [&](int k) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            kf[t] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), (k % AHEAD) * NT + t)) * a.scale;
+            vf[t] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs), (k % AHEAD) * NT + t));
+        }
+    };
+    uint4 kc[NT][J], vc[NT][J];
+    auto load = [&](uint4 (&to)[NT][J], const uint8_t *codes) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const v4u *p = reinterpret_cast<const v4u *>(codes + tile_at[t] * (kTile * D)) + lane;
+#pragma unroll
+            for (int j = 0; j < J; ++j) to[t][j] = __builtin_bit_cast(uint4, __builtin_nontemporal_load(p + 64 * j));
+        }
+    };
+    if (wave < groups) {
+        find(wave, 0);
+        load(kc, c.k);
+        __builtin_amdgcn_sched_barrier(0);      // in this order the keys can be waited for alone
+        load(vc, c.v);
+    }
+    for (int gi = wave, k = 0; gi < groups; gi += kWaves, ++k) {
+        const int tile0 = tile_begin + gi * NT;
+        find_scales(k);
+        bool edge = tile0 * kTile < u.all_lo || (tile0 + NT) * kTile > u.all_up;
+        int mine[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            mine[t] = there[t];
+            edge |= mine[t] < 0;
+        }
+        const bool more = gi + kWaves < groups;
+        // scores: row token 4 g + r of tile t, column the lane's query row.  The
+        // barriers keep conversions beside the products that take them: hoisted over
+        // them, they double the registers.
         v4f x[RT][NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
+        for (int t = 0; t < NT; t += 2) {
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) x[rt][t] = v4f{0, 0, 0, 0};
+            for (int rt = 0; rt < RT; ++rt) x[rt][t] = x[rt][t + 1] = v4f{0, 0, 0, 0};
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const v8bf k0 = operand<FMT>(kc[t][j].x, kc[t][j].y), k1 = operand<FMT>(kc[t][j].z, kc[t][j].w);
+            for (int k = 0; k < 2 * J; ++k) {
+                const uint4 &c0 = kc[t][k >> 1], &c1 = kc[t + 1][k >> 1];
+                const v8bf k0 = k & 1 ? operand<FMT>(c0.z, c0.w) : operand<FMT>(c0.x, c0.y);
+                const v8bf k1 = k & 1 ? operand<FMT>(c1.z, c1.w) : operand<FMT>(c1.x, c1.y);
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
-                    x[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q[rt][2 * j], x[rt][t], 0, 0, 0);
-                    x[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, q[rt][2 * j + 1], x[rt][t], 0, 0, 0);
+                    x[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q[rt][k], x[rt][t], 0, 0, 0);
+                    x[rt][t + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, q[rt][k], x[rt][t + 1], 0, 0, 0);
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
+        // the next keys, while these scores become probabilities and meet the values
+        if (more) {
+            find(gi + kWaves, k + 1);
+            load(kc, c.k);
+        }
+        __builtin_amdgcn_sched_barrier(0);
         if (edge) {
             // tokens that no row sees may hold anything: NaN codes must not meet the probability 0
 #pragma unroll
@@ -224,7 +385,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_kernel(AttentionLaunch 
                 uint32_t keep = 0;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const bool any = there[t] >= 0 && token + r >= u.lo && token + r < u.up;
+                    const bool any = mine[t] >= 0 && token + r >= u.lo && token + r < u.up;
                     if (any) keep |= 0xFFu << (8 * r);
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt)
@@ -235,7 +396,7 @@ __global__ __launch_bounds__(64 * kWaves) void attention_kernel(AttentionLaunch 
                 for (int j = 0; j < J; ++j) {
                     vc[t][j].x &= keep; vc[t][j].y &= keep; vc[t][j].z &= keep; vc[t][j].w &= keep;
                 }
-                if (there[t] < 0) vf[t] = 0.0f;      // the scale is another page's
+                if (mine[t] < 0) vf[t] = 0.0f;       // the scale is another page's
             }
         } else {
 #pragma unroll
@@ -268,41 +429,36 @@ __global__ __launch_bounds__(64 * kWaves) void attention_kernel(AttentionLaunch 
                     x[rt][t][r] *= vf[t];
                 }
         }
-        // second product, 32 tokens at a time
+        __builtin_amdgcn_sched_barrier(0);
+        // second product, 32 tokens and 32 channels at a time
 #pragma unroll
         for (int t = 0; t < NT; t += 2) {
             v8bf p[RT][TERMS];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
+            for (int rt = 0; rt < RT; ++rt) terms<TERMS>(x[rt][t], x[rt][t + 1], p[rt]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float rest = x[rt][t + (i >> 2)][i & 3];
-#pragma unroll
-                    for (int n = 0; n < TERMS; ++n) {
-                        p[rt][n][i] = (__bf16)rest;
-                        rest -= (float)p[rt][n][i];
-                    }
-                }
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                const uint4 &v0 = vc[t][d >> 2], &v1 = vc[t + 1][d >> 2];
-                const uint32_t w0 = (d & 3) == 0 ? v0.x : (d & 3) == 1 ? v0.y : (d & 3) == 2 ? v0.z : v0.w;
-                const uint32_t w1 = (d & 3) == 0 ? v1.x : (d & 3) == 1 ? v1.y : (d & 3) == 2 ? v1.z : v1.w;
-                const v8bf v = operand<FMT>(w0, w1);
+            for (int d = 0; d < DT; d += 2) {
+                const uint4 &c0 = vc[t][d >> 2], &c1 = vc[t + 1][d >> 2];
+                const v8bf v0 = d & 2 ? operand<FMT>(c0.z, c1.z) : operand<FMT>(c0.x, c1.x);
+                const v8bf v1 = d & 2 ? operand<FMT>(c0.w, c1.w) : operand<FMT>(c0.y, c1.y);
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                    for (int n = 0; n < TERMS; ++n)
-                        y[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[rt][n], y[rt][d], 0, 0, 0);
+                    for (int n = 0; n < TERMS; ++n) {
+                        y[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, p[rt][n], y[rt][d], 0, 0, 0);
+                        y[rt][d + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, p[rt][n], y[rt][d + 1], 0, 0, 0);
+                    }
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
+        if (more) load(vc, c.v);
     }
 
     // the waves' sums together, 16 rows at a time
-    const int64_t slot = ((int64_t)part * a.units + blockIdx.x) * c.heads + head;
+    const int64_t slot = 2 * worker + (starts ? 1 : 0);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        if (rt) __syncthreads();
+        __syncthreads();                        // the last ones are read
         const float sum = row_sum(l[rt]);
         if (g == 0) merge_ml[wave][col] = make_float2(m[rt], sum);
 #pragma unroll
@@ -330,61 +486,96 @@ __global__ __launch_bounds__(64 * kWaves) void attention_kernel(AttentionLaunch 
             v4f v = {0, 0, 0, 0};
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) v += *reinterpret_cast<const v4f *>(&merge[w][r][d]) * ml[w].x;
-            if (parts == 1) store_y4<F32>(a.y, to + d, v * by);
+            if (whole) store_y4<F32>(a.y, to + d, v * by);
             else *reinterpret_cast<v4f *>(a.part_o + (slot * ROWS + row) * D + d) = v;
         }
-        if (parts > 1 && (threadIdx.x & 15) == 0) a.part_ml[slot * ROWS + row] = make_float2(top, total);
+        if (!whole && (threadIdx.x & 15) == 0) a.part_ml[slot * ROWS + row] = make_float2(top, total);
+    }
+    if (stop == end) {
+        if (threadIdx.x == 0 && starts && !whole) {      // the unit goes on in other shares
+            AttentionCut cut_here;
+            cut_here.last = (int)quotient(unit_end - 1, share);
+            cut_here.head = head;
+            cut_here.first = u.q.first;
+            cut_here.row0 = u.row0;
+            cut_here.rows = u.rows;
+            a.cuts[worker] = cut_here;
+        }
+        return;
+    }
+    // the next unit: the sequence's next row tile, the next sequence, the next head
+    at = begin = unit_end;
+    if (++tile == sw.tiles) {
+        tile = 0;
+        do {
+            if (++seq == c.B) {
+                seq = 0;
+                ++head;
+            }
+            sq = sequence_at(c, seq);
+            sw = sequence_work<ROWS, STEP>(a, sq);
+        } while (sw.tiles == 0);
+    }
     }
 }
 
-// The parts of a unit's row together: a workgroup each.
+// The sums of a unit that was cut: the first worker's that has some of it, and
+// those of the workers behind it.  A workgroup has a row.
 template <int D, bool F32, int ROWS>
 __global__ __launch_bounds__(256) void join_kernel(AttentionLaunch a) {
     constexpr int LANES = D / 4, SETS = 256 / LANES;
-    __shared__ float factor[kMaxParts];
+    __shared__ float factor[kMostWorkers];
     __shared__ v4f sums[SETS][LANES];
     __shared__ float red[2][4];
-    Unit u;
-    if (!unit_of<ROWS>(a, &u)) return;
-    const int head = blockIdx.y, row = blockIdx.z, tid = threadIdx.x;
-    const int parts = parts_of(a, u);
-    if (row >= u.rows || parts == 1) return;
-    const int64_t step = (int64_t)a.units * a.c.heads * ROWS;
-    const int64_t at = ((int64_t)blockIdx.x * a.c.heads + head) * ROWS + row;
-    float2 ml = make_float2(-INFINITY, 0.0f);
-    if (tid < parts) ml = a.part_ml[tid * step + at];
-    const float top_w = wave_max(ml.x);
-    if ((tid & 63) == 0) red[0][tid >> 6] = top_w;
+    const int first = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
+    const AttentionCut cut = a.cuts[first];
+    if (cut.last <= first || row >= cut.rows) return;
+    const int parts = cut.last - first + 1;
+    // a part's row among the workers' sums: the first worker's second place, the others' first
+    auto place = [&](int p) { return (int64_t)(2 * (first + p) + (p == 0 ? 1 : 0)) * ROWS + row; };
+    float top = -INFINITY;
+    for (int p = tid; p < parts; p += 256) top = fmaxf(top, a.part_ml[place(p)].x);
+    top = wave_max(top);
+    if ((tid & 63) == 0) red[0][tid >> 6] = top;
     __syncthreads();
-    const float top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-    const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
-    factor[tid] = f;
-    float sum = f * ml.y;
+    top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    float total = 0.0f;
+    for (int p = tid; p < parts; p += 256) {
+        const float2 ml = a.part_ml[place(p)];
+        const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
+        factor[p] = f;
+        total += f * ml.y;
+    }
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
-    if ((tid & 63) == 0) red[1][tid >> 6] = sum;
+    for (int d = 1; d < 64; d *= 2) total += __shfl_xor(total, d);
+    if ((tid & 63) == 0) red[1][tid >> 6] = total;
     __syncthreads();
-    const float total = red[1][0] + red[1][1] + red[1][2] + red[1][3];
-    const int set = tid / LANES, d = 4 * (tid % LANES);
+    total = red[1][0] + red[1][1] + red[1][2] + red[1][3];
+    const int set = tid / LANES, lane = tid % LANES;
     if (set < SETS) {
         v4f v = {0, 0, 0, 0};
+#pragma unroll 4
         for (int p = set; p < parts; p += SETS)
-            v += *reinterpret_cast<const v4f *>(a.part_o + (p * step + at) * D + d) * factor[p];
-        sums[set][tid % LANES] = v;
+            v += *reinterpret_cast<const v4f *>(a.part_o + place(p) * D + 4 * lane) * factor[p];
+        sums[set][lane] = v;
     }
     __syncthreads();
     if (tid < LANES) {
         v4f v = sums[0][tid];
+#pragma unroll
         for (int s = 1; s < SETS; ++s) v += sums[s][tid];
-        store_y4<F32>(a.y, row_at(a, u, row, a.ldy, head, D) + 4 * tid, v * (total > 0.0f ? 1.0f / total : 0.0f));
+        const int at = cut.row0 + row, token = at / a.group;
+        store_y4<F32>(a.y,
+                      (int64_t)(cut.first + token) * a.ldy + (int64_t)(cut.head * a.group + at - token * a.group) * D + 4 * tid,
+                      v * (total > 0.0f ? 1.0f / total : 0.0f));
     }
 }
 
 template <int D, int FMT, int TERMS, int RT>
 void launch_rows(const AttentionPlan &p, const AttentionLaunch &a, hipStream_t s) {
-    hipLaunchKernelGGL((attention_kernel<D, FMT, TERMS, RT>), dim3(a.units, a.c.heads, a.parts), dim3(64 * kWaves), 0, s, a);
-    if (a.parts > 1)
-        hipLaunchKernelGGL((join_kernel<D, TERMS == 3, 16 * RT>), dim3(a.units, a.c.heads, 16 * RT), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((attention_kernel<D, FMT, TERMS, RT>), dim3(a.workers), dim3(64 * kWaves), 0, s, a);
+    if (!a.whole && a.workers > 1)
+        hipLaunchKernelGGL((join_kernel<D, TERMS == 3, 16 * RT>), dim3(a.workers - 1, p.live_rows), dim3(256), 0, s, a);
 }
 
 template <int D, int FMT>
@@ -409,29 +600,30 @@ int64_t row_tiles(int64_t sequences, int64_t tokens, int group, int rows) {
     return std::min((tokens * group + some * (rows - 1)) / rows, tokens * ((group + rows - 1) / rows));
 }
 
-constexpr int kSlots = 2048;       // (unit, head, part) workgroups that a split call aims at, at most
-constexpr int kMinChunk = 512;     // tokens of a part, at least
-
-int64_t most_parts(int max_context) {
-    return std::min<int64_t>(kMaxParts, std::max<int64_t>(1, (max_context + kMinChunk - 1) / kMinChunk));
-}
-
 }  // namespace
 
 AttentionPlan attention_plan(int sequences, int tokens, int max_context, int kv_heads, int group, int head_dim) {
     AttentionPlan p = {};
     if (sequences == 0 || tokens == 0) return p;
     p.rows = (int64_t)tokens * group <= 16 * (int64_t)sequences ? 16 : 32;
-    p.units = row_tiles(sequences, tokens, group, p.rows);
-    const int64_t most = most_parts(max_context);
-    p.parts = (int)std::max<int64_t>(1, std::min(most, kSlots / (p.units * kv_heads)));
-    p.chunk = (int)(((int64_t)max_context + p.parts - 1) / p.parts + 255) / 256 * 256;   // whole groups of each wave
-    // the workspace of the calls with as many or fewer sequences, tokens, and context
-    const int64_t slots = std::min<int64_t>(kSlots, row_tiles(sequences, tokens, group, 16) * kv_heads * most);
-    if (most > 1) {
-        p.ml_at = (size_t)slots * 32 * head_dim * sizeof(float);
-        p.ws_bytes = p.ml_at + (size_t)slots * 32 * sizeof(float2);
+    p.live_rows = (int)std::min<int64_t>(p.rows, (int64_t)tokens * group);
+    const int step = head_dim <= 128 ? 256 : 128;
+    p.whole = max_context <= step;
+    // as many workers as are resident at once
+    const int resident = p.rows == 32 ? 1 : head_dim == 64 ? 3 : 2;
+    const int64_t units = row_tiles(sequences, tokens, group, p.rows) * kv_heads;
+    if (p.whole) {
+        p.workers = (int)std::min<int64_t>(units, kMostWorkers);
+        return p;
     }
+    p.workers = (int)std::min<int64_t>(256 * resident, units * (((int64_t)max_context + step - 1) / step + 1));
+    // the workspace of any plan of as many or fewer sequences, tokens and context
+    const int64_t most = std::min<int64_t>(
+        kMostWorkers, row_tiles(sequences, tokens, group, 16) * kv_heads * (((int64_t)max_context + step - 1) / step + 1));
+    const size_t slots = 2 * (size_t)most * ((int64_t)tokens * group <= 16 ? 16 : 32);
+    p.ml_at = slots * head_dim * sizeof(float);
+    p.cuts_at = p.ml_at + slots * sizeof(float2);
+    p.ws_bytes = p.cuts_at + (size_t)most * sizeof(AttentionCut);
     return p;
 }
 

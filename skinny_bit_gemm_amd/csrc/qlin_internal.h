@@ -199,10 +199,16 @@ struct RowsLaunch {            // append and read
 
 // How qlin_cache_attention runs (qlin_attention.hip).
 struct AttentionPlan {
-    int rows;                  // (token, head of the group) rows of a workgroup
-    int64_t units;             // row tiles, at most
-    int parts, chunk;          // parts of a sequence's tokens, tokens of each
-    size_t ml_at, ws_bytes;
+    int rows;                  // (token, head of the group) rows of a unit
+    int live_rows;             // of them, at most, there
+    int workers, whole;        // workgroups; no unit is cut between them
+    size_t ml_at, cuts_at, ws_bytes;
+};
+
+// A unit whose tokens are in the shares of several workers; in the entry of the first.
+struct AttentionCut {
+    int last;                  // worker that has its end; -1: the worker's last unit goes no further
+    int head, first, row0, rows;
 };
 
 struct AttentionLaunch {
@@ -214,9 +220,10 @@ struct AttentionLaunch {
     int group;                 // query heads of a key head
     int causal, window;
     float scale;               // times log2(e)
-    int units, parts, chunk;
-    float *part_o;             // [part][unit][head][rows][D]
-    float2 *part_ml;           // [part][unit][head][rows]: maximum (log2), sum
+    int workers, whole;
+    float *part_o;             // [worker][2][rows][D]: of the unit in the worker's share
+    float2 *part_ml;           // that began before it, and of the one that goes on: maximum (log2), sum
+    AttentionCut *cuts;        // [worker]
 };
 
 // Host-side selection table (qlin_table.cpp).
