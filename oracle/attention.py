@@ -135,13 +135,14 @@ class Cache:
 
 
 def attention(cache, offsets, lengths, table, q, scale, causal=True, window=0):
-    """q [T, q_heads, D] -> (y, W, E).  W = sum p |v| / sum p.  E: by how much y
+    """q [T, q_heads, D] -> (y, W, E, F).  W = sum p |v| / sum p.  E: by how much y
     is off when log2 p_j is off by u ((D + 8) A_j + 2 |x_j - max x|), for u = 1,
-    A_j being the absolute terms of x_j = log2(e) scale q . k_j."""
+    A_j being the absolute terms of x_j = log2(e) scale q . k_j.  F = sum |v| /
+    sum p, with p = 1 for the largest."""
     q = np.asarray(q, dtype=np.float64)
     T, Hq, D = q.shape
     G = Hq // cache.heads
-    y, W, E = np.full((T, Hq, D), np.nan), np.zeros((T, Hq, D)), np.zeros((T, Hq, D))
+    y, W, E, F = np.full((T, Hq, D), np.nan), *np.zeros((3, T, Hq, D))
     to_log2 = scale / np.log(2.0)
     for s in range(len(lengths)):
         first, n = int(offsets[s]), int(offsets[s + 1]) - int(offsets[s])
@@ -168,8 +169,9 @@ def attention(cache, offsets, lengths, table, q, scale, causal=True, window=0):
                 A = np.abs(ks) @ np.abs(one) * abs(to_log2)
                 p = np.exp2(x - x.max())
                 off = p * np.log(2.0) * ((D + 8) * A + 2 * np.abs(x - x.max()))
+                F[first + i, h] = np.abs(vs).sum(0) / p.sum()
                 p, off = p / p.sum(), off / p.sum()
                 y[first + i, h] = p @ vs
                 W[first + i, h] = p @ np.abs(vs)
                 E[first + i, h] = off @ np.abs(vs) + off.sum() * np.abs(y[first + i, h])
-    return y, W, E
+    return y, W, E, F

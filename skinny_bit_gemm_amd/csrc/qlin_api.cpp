@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstdio>
+#include <cstdlib>
 #include <new>
 
 #include <hip/hip_runtime_api.h>
@@ -968,7 +969,7 @@ qlin_status qlin_cache_attention(const qlin_attention *attention, const qlin_cac
         return QLIN_ERR_ALIGNMENT;
     if (p.ws_bytes && (!workspace || ws_bytes < p.ws_bytes)) return QLIN_ERR_WORKSPACE;
     if (p.ws_bytes && !aligned16(workspace)) return QLIN_ERR_ALIGNMENT;
-    if (p.workers == 0) return QLIN_OK;
+    if (sequences->sequences == 0 || sequences->tokens == 0) return QLIN_OK;
     AttentionLaunch a = {};
     a.c = cache_args(cache, sequences);
     a.q = static_cast<const uint16_t *>(q);
@@ -978,12 +979,19 @@ qlin_status qlin_cache_attention(const qlin_attention *attention, const qlin_cac
     a.group = attention->q_heads / cache->kv_heads;
     a.causal = attention->causal;
     a.window = attention->window;
-    a.scale = (float)(attention->scale * 1.4426950408889634);
+    a.scale = (float)(std::abs((double)attention->scale) * 1.4426950408889634);
+    a.flip = attention->scale < 0.0f ? 0x80008000u : 0u;
+    a.few_rows = p.few_rows;
     a.workers = p.workers;
     a.whole = p.whole;
-    a.part_o = static_cast<float *>(workspace);
-    a.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + p.ml_at);
-    a.cuts = reinterpret_cast<AttentionCut *>(static_cast<char *>(workspace) + p.cuts_at);
+    a.wide_units = p.wide_units;
+    a.wide_parts = p.wide_parts;
+    a.wide_place = (int)p.wide_place;
+    char *ws = static_cast<char *>(workspace);
+    a.part_o = reinterpret_cast<float *>(ws);
+    a.part_ml = reinterpret_cast<float2 *>(ws + p.ml_at);
+    a.cuts = reinterpret_cast<AttentionCut *>(ws + p.cuts_at);
+    a.wide_cuts = reinterpret_cast<AttentionCut *>(ws + p.wide_cuts_at);
     return hip_status(launch_attention(cache->format, out_type == QLIN_OUT_F32_ACC, cache->head_dim, p, a,
                                        static_cast<hipStream_t>(stream)));
 }

@@ -1,145 +1,18 @@
-// qlin_attention.hip -- attention over the paged 8-bit cache.
+// qlin_attention.hip -- attention over the paged 8-bit cache: sequences with few
+// query rows, the join of what was cut, and the plan of a call.
 //
-//   y = sum_j p_j v_j / sum_j p_j,  p_j = 2^(x_j - max x),  x_j = log2(e) scale q . k_j
-//
-// One pass over a sequence's tokens with a running maximum and sum.  Both
-// products run transposed on the bf16 matrix cores, with the codes as their left
-// operands: S^T = K Q^T, then Y^T = V^T P^T.  A lane then has one query row in
-// the scores, in the running maximum and sum, and in Y^T alike, and the scores
-// of two tiles of 16 tokens are the second product's operand as they stand: no
-// value changes lanes but the maximum.  The cache's tiles are stored in the order
-// of these operands, so every load of a wave is 1 KiB of consecutive codes.
-// e4m3 and int8 codes are bf16 numbers, so products with them are exact; the
-// scales of a page multiply the scores and the probabilities.  Probabilities
-// enter the second product as two bf16 terms (16 bits of mantissa; three, 24
-// bits, where y is fp32): one term alone costs as much again as the rounding of y.
+// Probabilities enter the second product as two bf16 terms (16 bits of mantissa;
+// three, 24 bits, where y is fp32): one term alone costs as much again as the
+// rounding of y, and the codes' stream, which bounds these calls, hides the rest.
 #include <algorithm>
 
-#include "qlin_sequences.h"
+#include "qlin_attention.h"
 
 namespace qlin {
 
 namespace {
 
-typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-
-constexpr int kTile = 16;
-constexpr int kWaves = 4;
 constexpr int kMostWorkers = 768;
-
-// four codes of a word as bf16 (exact)
-template <int FMT>
-__device__ __forceinline__ uint2 bf16_codes(uint32_t w) {
-    if constexpr (FMT == FMT_I8) {
-        asm("" : "+v"(w));      // one register until here: its bytes are not taken apart when it is loaded
-        const uint32_t f0 = __float_as_uint((float)(int8_t)w), f1 = __float_as_uint((float)(int8_t)(w >> 8));
-        const uint32_t f2 = __float_as_uint((float)(int8_t)(w >> 16)), f3 = __float_as_uint((float)(int8_t)(w >> 24));
-        return make_uint2(__builtin_amdgcn_perm(f1, f0, 0x07060302u), __builtin_amdgcn_perm(f3, f2, 0x07060302u));
-    }
-    return make_uint2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false)),
-                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true)));
-}
-
-// eight codes as a matrix operand
-template <int FMT>
-__device__ __forceinline__ v8bf operand(uint32_t lo, uint32_t hi) {
-    const uint2 a = bf16_codes<FMT>(lo), b = bf16_codes<FMT>(hi);
-    return __builtin_bit_cast(v8bf, v4u{a.x, a.y, b.x, b.y});
-}
-
-typedef float v2f __attribute__((ext_vector_type(2)));
-
-// eight probabilities as TERMS operands, whose sum has 8 bits of mantissa from each
-template <int TERMS>
-__device__ __forceinline__ void terms(v4f a, v4f b, v8bf (&p)[TERMS]) {
-    v2f rest[4] = {{a[0], a[1]}, {a[2], a[3]}, {b[0], b[1]}, {b[2], b[3]}};
-#pragma unroll
-    for (int n = 0; n < TERMS; ++n) {
-        v4u w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest[i], v2bf));     // nearest even
-            if (n + 1 < TERMS) {
-                rest[i][0] -= bf16_lo(w[i]);
-                rest[i][1] -= bf16_hi(w[i]);
-            }
-        }
-        p[n] = __builtin_bit_cast(v8bf, w);
-    }
-}
-
-// over the four lanes l, l ^ 16, l ^ 32, l ^ 48 of a query row
-__device__ __forceinline__ float row_max(float v) {
-    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
-    const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
-}
-__device__ __forceinline__ float row_sum(float v) {
-    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-    const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
-}
-
-// A unit of work: a tile of a sequence's query rows (token x group + head of the
-// group), and the tokens that they see.
-struct Unit {
-    int seq, row0, rows;       // first row, rows that are there
-    Sequence q;
-    int lo, up;                // tokens that any row sees
-    int all_lo, all_up;        // tokens that every row sees
-};
-
-struct Seen {
-    int lo, up;
-};
-__device__ __forceinline__ Seen seen_by(const AttentionLaunch &a, const Sequence &q, int token) {
-    const int p = q.start + token;
-    Seen s;
-    s.up = a.causal ? min(q.length, p + 1) : q.length;
-    s.lo = a.window > 0 ? (int)max((int64_t)0, (int64_t)p + 1 - a.window) : 0;
-    return s;
-}
-
-__device__ __forceinline__ Unit unit_at(const AttentionLaunch &a, int seq, const Sequence &q, int tile, int tile_rows) {
-    Unit u;
-    u.seq = seq;
-    u.q = q;
-    u.row0 = tile * tile_rows;
-    u.rows = min(tile_rows, q.n * a.group - u.row0);
-    const Seen first = seen_by(a, q, u.row0 / a.group), last = seen_by(a, q, (u.row0 + u.rows - 1) / a.group);
-    u.lo = first.lo;
-    u.up = last.up;
-    u.all_lo = last.lo;
-    u.all_up = first.up;
-    return u;
-}
-
-template <bool F32>
-__device__ __forceinline__ void store_y4(void *y, int64_t at, v4f v) {
-    if constexpr (F32) {
-        *reinterpret_cast<v4f *>(static_cast<float *>(y) + at) = v;
-    } else {
-        const v4bf b = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-        *reinterpret_cast<v4bf *>(static_cast<uint16_t *>(y) + at) = b;
-    }
-}
-
-// element of y (or of q) where a unit's row and this head's channels begin
-__device__ __forceinline__ int64_t row_at(const AttentionLaunch &a, const Unit &u, int row, int64_t ld, int head, int D) {
-    const int r = u.row0 + row, token = r / a.group;
-    return (int64_t)(u.q.first + token) * ld + (int64_t)(head * a.group + r - token * a.group) * D;
-}
-
-// a value that all lanes have, in scalar registers
-__device__ __forceinline__ int64_t uniform(int64_t v) {
-    return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)v) |
-                     (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32);
-}
 
 // ------------------------------------------------------------ few rows a sequence
 //
@@ -163,7 +36,7 @@ struct SequenceWork {
 template <int ROWS, int STEP>
 __device__ __forceinline__ SequenceWork sequence_work(const AttentionLaunch &a, const Sequence &q) {
     SequenceWork w = {0, 0, 0};
-    if (q.n == 0) return w;
+    if (q.n == 0 || (int64_t)q.n * a.group > a.few_rows) return w;
     const Seen first = seen_by(a, q, 0), last = seen_by(a, q, q.n - 1);
     w.tiles = (q.n * a.group + ROWS - 1) / ROWS;
     w.tile0 = first.lo / kTile;
@@ -208,15 +81,6 @@ __device__ __forceinline__ void sum_steps(const AttentionLaunch &a, Shares &sh) 
     __syncthreads();
 }
 
-__device__ __forceinline__ Sequence uniform(const Sequence &q) {
-    Sequence r;
-    r.first = __builtin_amdgcn_readfirstlane(q.first);
-    r.n = __builtin_amdgcn_readfirstlane(q.n);
-    r.start = __builtin_amdgcn_readfirstlane(q.start);
-    r.length = __builtin_amdgcn_readfirstlane(q.length);
-    return r;
-}
-
 // RT: tiles of 16 query rows; all waves have the same rows and take groups of NT
 // tiles of tokens in turn, so a code is read and converted once for all rows.
 template <int D, int FMT, int TERMS, int RT>
@@ -240,7 +104,7 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 2 : 1) void attention_kernel
     const int64_t share = quotient(steps + a.workers - 1, a.workers);
     int64_t at = worker * share;
     const int64_t end = min(steps, at + share);
-    if (threadIdx.x == 0 && !a.whole) a.cuts[worker].last = -1;
+    if (threadIdx.x == 0 && !a.whole) a.cuts[worker].parts = 0;
     if (at >= end) return;
     int head = (int)quotient(at, per_head), seq;
     int64_t begin = (int64_t)head * per_head;   // of the sequence, and then of the unit
@@ -280,7 +144,7 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 2 : 1) void attention_kernel
         const uint16_t *from = a.q + row_at(a, u, row, a.ldq, head, D);
 #pragma unroll
         for (int k = 0; k < 2 * J; ++k)
-            q[rt][k] = *reinterpret_cast<const v8bf *>(from + 64 * (k >> 1) + 16 * g + 8 * (k & 1));
+            q[rt][k] = query(a, from, k, g);
         seen[rt] = seen_by(a, u.q, (u.row0 + row) / a.group);
     }
 
@@ -493,13 +357,16 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 2 : 1) void attention_kernel
     }
     if (stop == end) {
         if (threadIdx.x == 0 && starts && !whole) {      // the unit goes on in other shares
-            AttentionCut cut_here;
-            cut_here.last = (int)quotient(unit_end - 1, share);
-            cut_here.head = head;
-            cut_here.first = u.q.first;
-            cut_here.row0 = u.row0;
-            cut_here.rows = u.rows;
-            a.cuts[worker] = cut_here;
+            AttentionCut cut;
+            cut.parts = (int)quotient(unit_end - 1, share) - worker + 1;
+            cut.place0 = (2 * worker + 1) * ROWS;
+            cut.place = 2 * worker * ROWS;
+            cut.step = 2 * ROWS;
+            cut.head = head;
+            cut.first = u.q.first;
+            cut.row0 = u.row0;
+            cut.rows = u.rows;
+            a.cuts[worker] = cut;
         }
         return;
     }
@@ -519,20 +386,18 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 2 : 1) void attention_kernel
     }
 }
 
-// The sums of a unit that was cut: the first worker's that has some of it, and
-// those of the workers behind it.  A workgroup has a row.
-template <int D, bool F32, int ROWS>
-__global__ __launch_bounds__(256) void join_kernel(AttentionLaunch a) {
+// The sums of a unit that was cut.  A workgroup has a row.
+template <int D, bool F32>
+__global__ __launch_bounds__(256) void join_kernel(AttentionLaunch a, const AttentionCut *cuts) {
     constexpr int LANES = D / 4, SETS = 256 / LANES;
     __shared__ float factor[kMostWorkers];
     __shared__ v4f sums[SETS][LANES];
     __shared__ float red[2][4];
-    const int first = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
-    const AttentionCut cut = a.cuts[first];
-    if (cut.last <= first || row >= cut.rows) return;
-    const int parts = cut.last - first + 1;
-    // a part's row among the workers' sums: the first worker's second place, the others' first
-    auto place = [&](int p) { return (int64_t)(2 * (first + p) + (p == 0 ? 1 : 0)) * ROWS + row; };
+    const int row = blockIdx.y, tid = threadIdx.x;
+    const AttentionCut cut = cuts[blockIdx.x];
+    if (cut.parts <= 1 || row >= cut.rows) return;
+    const int parts = cut.parts;
+    auto place = [&](int p) { return (int64_t)(p == 0 ? cut.place0 : cut.place + p * cut.step) + row; };
     float top = -INFINITY;
     for (int p = tid; p < parts; p += 256) top = fmaxf(top, a.part_ml[place(p)].x);
     top = wave_max(top);
@@ -572,16 +437,23 @@ __global__ __launch_bounds__(256) void join_kernel(AttentionLaunch a) {
 }
 
 template <int D, int FMT, int TERMS, int RT>
-void launch_rows(const AttentionPlan &p, const AttentionLaunch &a, hipStream_t s) {
+void launch_rows(const AttentionLaunch &a, hipStream_t s) {
     hipLaunchKernelGGL((attention_kernel<D, FMT, TERMS, RT>), dim3(a.workers), dim3(64 * kWaves), 0, s, a);
-    if (!a.whole && a.workers > 1)
-        hipLaunchKernelGGL((join_kernel<D, TERMS == 3, 16 * RT>), dim3(a.workers - 1, p.live_rows), dim3(256), 0, s, a);
 }
 
 template <int D, int FMT>
 void launch_width(bool f32, const AttentionPlan &p, const AttentionLaunch &a, hipStream_t s) {
-    if (p.rows == 16) f32 ? launch_rows<D, FMT, 3, 1>(p, a, s) : launch_rows<D, FMT, 2, 1>(p, a, s);
-    else f32 ? launch_rows<D, FMT, 3, 2>(p, a, s) : launch_rows<D, FMT, 2, 2>(p, a, s);
+    if (p.workers > 0) {
+        if (p.rows == 16) f32 ? launch_rows<D, FMT, 3, 1>(a, s) : launch_rows<D, FMT, 2, 1>(a, s);
+        else f32 ? launch_rows<D, FMT, 3, 2>(a, s) : launch_rows<D, FMT, 2, 2>(a, s);
+    }
+    if (p.wide_units > 0) launch_wide(FMT, f32, D, a, s);
+    auto join = [&](const AttentionCut *cuts, int64_t entries, int rows) {
+        if (f32) hipLaunchKernelGGL((join_kernel<D, true>), dim3(entries, rows), dim3(256), 0, s, a, cuts);
+        else hipLaunchKernelGGL((join_kernel<D, false>), dim3(entries, rows), dim3(256), 0, s, a, cuts);
+    };
+    if (p.workers > 1 && !p.whole) join(a.cuts, p.workers - 1, p.live_rows);
+    if (p.wide_parts > 1) join(a.wide_cuts, p.wide_units, p.wide_rows);
 }
 
 template <int FMT>
@@ -600,30 +472,50 @@ int64_t row_tiles(int64_t sequences, int64_t tokens, int group, int rows) {
     return std::min((tokens * group + some * (rows - 1)) / rows, tokens * ((group + rows - 1) / rows));
 }
 
+constexpr int kWideItems = 512;    // (unit, head, part) workgroups that wide units are split for
+
 }  // namespace
 
 AttentionPlan attention_plan(int sequences, int tokens, int max_context, int kv_heads, int group, int head_dim) {
     AttentionPlan p = {};
     if (sequences == 0 || tokens == 0) return p;
-    p.rows = (int64_t)tokens * group <= 16 * (int64_t)sequences ? 16 : 32;
-    p.live_rows = (int)std::min<int64_t>(p.rows, (int64_t)tokens * group);
+    const int64_t all_rows = (int64_t)tokens * group;
     const int step = head_dim <= 128 ? 256 : 128;
-    p.whole = max_context <= step;
-    // as many workers as are resident at once
-    const int resident = p.rows == 32 ? 1 : head_dim == 64 ? 3 : 2;
-    const int64_t units = row_tiles(sequences, tokens, group, p.rows) * kv_heads;
-    if (p.whole) {
-        p.workers = (int)std::min<int64_t>(units, kMostWorkers);
-        return p;
+    const int64_t steps = ((int64_t)max_context + step - 1) / step + 1;
+
+    // Which sequences have few rows is known on the device alone: of several, some may
+    // have few and some many, and both kernels run, each with its own.
+    const bool wide = (tokens - std::min(sequences, tokens)) * (int64_t)group >= kWideFrom;
+    const bool few = !wide || sequences > 1;
+    p.few_rows = !wide ? INT32_MAX : few ? kFewRows : 0;
+    if (few) {
+        // 16 rows in a unit, or 32: as a sequence has on average, or of single tokens where that says nothing
+        p.rows = all_rows <= 16 * (int64_t)sequences || (all_rows > 32 * (int64_t)sequences && group <= 16) ? 16 : 32;
+        p.live_rows = (int)std::min<int64_t>(p.rows, all_rows);
+        const int64_t units = row_tiles(sequences, tokens, group, p.rows) * kv_heads;
+        // as many workers as are resident at once
+        const int resident = p.rows == 32 ? 1 : head_dim == 64 ? 3 : 2;
+        p.whole = max_context <= 2 * step;
+        p.workers = (int)std::min<int64_t>(p.whole ? kMostWorkers : 256 * resident, p.whole ? units : units * steps);
     }
-    p.workers = (int)std::min<int64_t>(256 * resident, units * (((int64_t)max_context + step - 1) / step + 1));
-    // the workspace of any plan of as many or fewer sequences, tokens and context
-    const int64_t most = std::min<int64_t>(
-        kMostWorkers, row_tiles(sequences, tokens, group, 16) * kv_heads * (((int64_t)max_context + step - 1) / step + 1));
-    const size_t slots = 2 * (size_t)most * ((int64_t)tokens * group <= 16 ? 16 : 32);
-    p.ml_at = slots * head_dim * sizeof(float);
-    p.cuts_at = p.ml_at + slots * sizeof(float2);
-    p.ws_bytes = p.cuts_at + (size_t)most * sizeof(AttentionCut);
+    if (wide) {
+        p.wide_rows = wide_rows(head_dim);
+        p.wide_units = row_tiles(sequences, tokens, group, p.wide_rows) * kv_heads;
+        p.wide_parts = (int)std::max<int64_t>(1, std::min<int64_t>(kWideItems / p.wide_units, (max_context + 1023) / 1024));
+    }
+    // The workspace of any plan of as many or fewer sequences, tokens and context
+    if (max_context > 2 * step) {               // else nothing is cut: a part has 1024 tokens at least
+        const int64_t few_most = std::min<int64_t>(kMostWorkers, row_tiles(sequences, tokens, group, 16) * kv_heads * steps);
+        const int64_t slots = few_most * 2 * (all_rows <= 16 ? 16 : 32);
+        const int64_t wide_most = std::min<int64_t>(kWideItems, row_tiles(sequences, tokens, group, 64) * kv_heads *
+                                                                    ((max_context + 1023) / 1024));
+        const int64_t wide_slots = (tokens - 1) * (int64_t)group >= kWideFrom ? wide_most * 128 : 0;
+        p.wide_place = slots;
+        p.ml_at = (size_t)(slots + wide_slots) * head_dim * sizeof(float);
+        p.cuts_at = p.ml_at + (size_t)(slots + wide_slots) * sizeof(float2);
+        p.wide_cuts_at = p.cuts_at + (size_t)few_most * sizeof(AttentionCut);
+        p.ws_bytes = p.wide_cuts_at + (wide_slots ? (size_t)wide_most * sizeof(AttentionCut) : 0);
+    }
     return p;
 }
 

@@ -199,15 +199,21 @@ struct RowsLaunch {            // append and read
 
 // How qlin_cache_attention runs (qlin_attention.hip).
 struct AttentionPlan {
-    int rows;                  // (token, head of the group) rows of a unit
+    int few_rows;              // sequences with at most so many (token, head of the group) rows: the first kernel's
+    int rows;                  // rows of its units
     int live_rows;             // of them, at most, there
     int workers, whole;        // workgroups; no unit is cut between them
-    size_t ml_at, cuts_at, ws_bytes;
+    int wide_rows;             // the second kernel's units: rows,
+    int64_t wide_units;        // row tiles of all heads, at most,
+    int wide_parts;            // parts of their tokens
+    int64_t wide_place;        // its first row among the sums of what was cut
+    size_t ml_at, cuts_at, wide_cuts_at, ws_bytes;
 };
 
-// A unit whose tokens are in the shares of several workers; in the entry of the first.
+// A unit of which several workgroups have a part each.
 struct AttentionCut {
-    int last;                  // worker that has its end; -1: the worker's last unit goes no further
+    int parts;                 // 0 or 1: nothing to join
+    int place0, place, step;   // their first rows among the sums: place0, then place + part step
     int head, first, row0, rows;
 };
 
@@ -219,12 +225,21 @@ struct AttentionLaunch {
     int64_t ldy;
     int group;                 // query heads of a key head
     int causal, window;
-    float scale;               // times log2(e)
+    float scale;               // its magnitude, times log2(e)
+    uint32_t flip;             // sign bits of two bf16 where the scale is negative
+    int few_rows;
     int workers, whole;
-    float *part_o;             // [worker][2][rows][D]: of the unit in the worker's share
-    float2 *part_ml;           // that began before it, and of the one that goes on: maximum (log2), sum
-    AttentionCut *cuts;        // [worker]
+    int64_t wide_units;
+    int wide_parts, wide_place;
+    float *part_o;             // [places][D]: sums of what was cut,
+    float2 *part_ml;           // [places]: with its maximum (log2) and sum of p
+    AttentionCut *cuts;        // [workers]: the unit that goes on behind a worker's share
+    AttentionCut *wide_cuts;   // [wide_units]
 };
+
+constexpr int kFewRows = 64;       // measured: see qlin_attention_wide.hip
+constexpr int kWideFrom = 512;     // rows beyond one token a sequence from which the second kernel runs too
+inline int wide_rows(int head_dim) { return head_dim <= 192 ? 128 : 64; }
 
 // Host-side selection table (qlin_table.cpp).
 qlin_status table_lookup(qlin_format fmt, int M, int N, int K, qlin_config *out, bool *found);
@@ -262,6 +277,7 @@ hipError_t launch_read(int fmt, bool f32, int head_dim, const RowsLaunch &a, hip
 AttentionPlan attention_plan(int sequences, int tokens, int max_context, int kv_heads, int group, int head_dim);
 hipError_t launch_attention(int fmt, bool f32, int head_dim, const AttentionPlan &p, const AttentionLaunch &a,
                             hipStream_t s);
+void launch_wide(int fmt, bool f32, int head_dim, const AttentionLaunch &a, hipStream_t s);
 bool gemm_variant_exists(int fmt, bool swap, int tile_m, int nr, int xc);
 // this device's static scratch array (kScratchBytes, zero between calls);
 // see qlin_linear_scratch

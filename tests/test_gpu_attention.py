@@ -60,18 +60,24 @@ def table_of(rng, lengths, page, pages, width=None):
     return table
 
 
-def tolerance(y, W, E, D, longest, out):
+def tolerance(y, W, E, F, D, longest, out, many):
     """E: the scores' errors, (D + 8) roundings of their terms, two of the exponent.
     W: each p has up to 8 roundings (its power of two, the page's scale, the joined
     waves and parts) and 4 for each time the maximum moves, at most once for the 64
     tokens of a step, and at most 40 times for scores in any order that fp32 powers
-    tell apart; its terms leave 2^-16 (2^-24 in fp32); the product's sum has a
-    rounding for each of the longest / 4 tokens of a wave.  y: the sum of p
-    likewise, the quotient, and the rounding of y."""
+    tell apart; its terms leave 2^-16 (three terms, where y is fp32: 2^-24; one fp16
+    number, where y is bf16 and the sequence has many rows: 2^-11 of a normal number,
+    and 2^-25 below them, where scales are at least 2^-4: F 2^-21); the product's sum
+    has a rounding for each of the longest / 4 tokens of a wave (each of all of them,
+    where there are many rows).  y: the sum of p likewise, the quotient, and the
+    rounding of y."""
     moves = 4 * min(40, longest // 64 + 1)
-    terms = 2.0 ** -24 if out == F32 else 2.0 ** -16
-    return E * U + W * (terms + (8 + moves + longest / 4 + 16) * U) + np.abs(y) * (
-        (longest / 4 + moves + 24) * U + (0 if out == F32 else 2.0 ** -8)) + 1e-30
+    many = np.asarray(many)[:, None, None]
+    terms = 2.0 ** -24 if out == F32 else np.where(many, 2.0 ** -11, 2.0 ** -16)
+    flat = 0.0 if out == F32 else np.where(many, 2.0 ** -21, 0.0)
+    adds = longest * np.where(many, 1.0, 0.25)
+    return E * U + W * (terms + (8 + moves + adds + 16) * U) + F * flat + np.abs(y) * (
+        (adds + moves + 24) * U + (0 if out == F32 else 2.0 ** -8)) + 1e-30
 
 
 class Call:
@@ -116,9 +122,10 @@ class Call:
             return 0.0
         got = full[:used, :n] if self.out == F32 else wl.bf16_bits_to_f32(full.view(np.uint16)[:used, :n])
         got = got.reshape(used, self.Hq, self.D).astype(np.float64)
-        y, W, E = oa.attention(self.ref, self.offsets, self.lengths, self.table, self.q_np[:used], self.scale,
+        y, W, E, F = oa.attention(self.ref, self.offsets, self.lengths, self.table, self.q_np[:used], self.scale,
                                bool(self.causal), self.window)
-        tol = tolerance(y, W, E, self.D, self.longest, self.out)
+        n = np.diff(self.offsets)
+        tol = tolerance(y, W, E, F, self.D, self.longest, self.out, np.repeat(n * (self.Hq // self.cache.kv_heads) > 64, n))
         assert np.isfinite(got).all(), f"{np.argwhere(~np.isfinite(got))[:3]} not finite"
         err = np.abs(got - y)
         at = np.unravel_index(np.argmax(err / tol), err.shape)
@@ -307,3 +314,58 @@ def test_pools_past_32_bits():
     table[table >= 0] += moved
     small.run()
     small.check()
+
+
+def scaled(c, kv, factor):
+    """The pages' scales times factor(page number in its sequence, sequence)."""
+    for s in range(len(c.lengths)):
+        for which in range(c.table.shape[1]):
+            p = c.ref.page_of(c.table, s, which * c.ref.page)
+            if p >= 0:
+                c.ref.scales[kv][p] *= np.float32(factor(which, s))
+    c.arrays[2 + kv].copy_(torch.from_numpy(c.ref.scales[kv]))
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("name,factor", [
+    ("growing", lambda w, s: 2.0 ** (3 * w)), ("falling", lambda w, s: 2.0 ** (-3 * w)),
+    ("far apart", lambda w, s: 2.0 ** (20 if w % 3 == 1 else 0)), ("zeros", lambda w, s: 0.0 if w % 2 else 1.0),
+    ("all zeros", lambda w, s: 0.0), ("tiny", lambda w, s: 2.0 ** -60), ("huge", lambda w, s: 2.0 ** 60)])
+def test_value_scales_of_any_size(name, factor, out):
+    for new, page in (([300, 20], 16), ([1, 3], 16), ([280, 70], 64)):
+        c = Call(FP8 if page == 16 else INT8, new, [400, 130], 8, 2, 64 if page == 16 else 128, page, out)
+        scaled(c, 1, factor)
+        c.run()
+        c.check()
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_key_scales_of_zero(out):
+    for new in ([300, 20], [1, 3]):
+        c = Call(FP8, new, [400, 130], 8, 2, 64, 16, out, window=200)
+        scaled(c, 0, lambda w, s: 0.0 if w % 2 else 1.0)
+        c.run()
+        c.check()
+
+
+@pytest.mark.parametrize("causal,window", [(1, 0), (0, 0), (1, 70), (0, 70), (1, 1)])
+def test_long_and_short_sequences_together(causal, window):
+    new, lengths = [1, 200, 0, 7, 1, 129, 33], [700, 200, 9, 1000, 3, 400, 33]
+    check(FP8, new, lengths, 8, 2, 64, 16, BF16, causal, window, extra=5)
+    check(INT8, new, lengths, 20, 2, 128, 32, F32, causal, window)
+    check(FP8, new, lengths, 6, 2, 192, 64, BF16, causal, window)
+    check(INT8, new, lengths, 6, 2, 256, 128, BF16, causal, window)
+
+
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+def test_long_contexts_of_many_rows(D):
+    """Units of many rows whose tokens several workgroups share."""
+    check(FP8, [130], [2500], 5, 1, D, 64, BF16)
+    check(INT8, [70, 1, 66], [2300, 40, 1100], 8, 1, D, 16, F32, window=1500)
+    check(FP8, [70, 66], [1 + 2300, 1100], 16, 1, D, 128, BF16, causal=0)
+
+
+def test_many_rows_that_see_nothing():
+    table = np.array([[-1] * 12, [0, 1, 2] + [-1] * 9, list(range(3, 15))])
+    check(FP8, [100, 200, 90], [150, 20, 180], 8, 1, 64, 16, F32, table=table, pages=16)
+    check(FP8, [100, 200, 90], [150, 20, 180], 8, 1, 64, 16, BF16, table=table, pages=16)

@@ -83,9 +83,10 @@ def filled(rng, fmt=oa.FP8, n=40, heads=2, D=64, page=16):
 def test_attention_of_equal_scores_is_the_mean_and_of_one_token_is_it():
     c, table = filled(np.random.default_rng(1))
     v = c.exact(1, table, 0, range(40))
-    y, W, E = oa.attention(c, [0, 2], [40], table, np.zeros((2, 4, 64)), 0.3)
+    y, W, E, F = oa.attention(c, [0, 2], [40], table, np.zeros((2, 4, 64)), 0.3)
     assert np.allclose(y[1], v.mean(0).repeat(2, 0)) and np.allclose(y[0], v[:39].mean(0).repeat(2, 0))
     assert np.allclose(W[1], np.abs(v).mean(0).repeat(2, 0)) and (E == 0).all()
+    assert np.allclose(F, W)                                         # all p are 1
     q = np.random.default_rng(2).normal(size=(2, 4, 64))
     y, *_ = oa.attention(c, [0, 2], [40], table, q, 0.3, window=1)
     assert np.allclose(y, v[38:40].repeat(2, 1))
