@@ -473,6 +473,7 @@ int64_t row_tiles(int64_t sequences, int64_t tokens, int group, int rows) {
 }
 
 constexpr int kWideItems = 512;    // (unit, head, part) workgroups that wide units are split for
+constexpr int kWideChunk = 1024;   // expected tokens of a part, at least
 
 }  // namespace
 
@@ -501,14 +502,14 @@ AttentionPlan attention_plan(int sequences, int tokens, int max_context, int kv_
     if (wide) {
         p.wide_rows = wide_rows(head_dim);
         p.wide_units = row_tiles(sequences, tokens, group, p.wide_rows) * kv_heads;
-        p.wide_parts = (int)std::max<int64_t>(1, std::min<int64_t>(kWideItems / p.wide_units, (max_context + 1023) / 1024));
+        p.wide_parts = (int)std::max<int64_t>(1, std::min<int64_t>(kWideItems / p.wide_units, (max_context + kWideChunk - 1) / kWideChunk));
     }
     // The workspace of any plan of as many or fewer sequences, tokens and context
-    if (max_context > 2 * step) {               // else nothing is cut: a part has 1024 tokens at least
+    if (max_context > std::min(2 * step, kWideChunk)) {      // else no unit is cut
         const int64_t few_most = std::min<int64_t>(kMostWorkers, row_tiles(sequences, tokens, group, 16) * kv_heads * steps);
         const int64_t slots = few_most * 2 * (all_rows <= 16 ? 16 : 32);
         const int64_t wide_most = std::min<int64_t>(kWideItems, row_tiles(sequences, tokens, group, 64) * kv_heads *
-                                                                    ((max_context + 1023) / 1024));
+                                                                    ((max_context + kWideChunk - 1) / kWideChunk));
         const int64_t wide_slots = (tokens - 1) * (int64_t)group >= kWideFrom ? wide_most * 128 : 0;
         p.wide_place = slots;
         p.ml_at = (size_t)(slots + wide_slots) * head_dim * sizeof(float);

@@ -101,7 +101,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void wide_kernel(AttentionLaunch a)
 
     v4f y[RT][DT];
     float m[RT], l[RT];
-    int base = 0;                               // y's sums are times 2^(127 - base)
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         m[rt] = -INFINITY;
@@ -110,67 +109,77 @@ __global__ __launch_bounds__(64 * kWaves, 2) void wide_kernel(AttentionLaunch a)
         for (int d = 0; d < DT; ++d) y[rt][d] = v4f{0, 0, 0, 0};
     }
 
-    // pages and scales of the next groups, a tile a lane; two sets, as loads run ahead of products
-    int page = -1, page_next = -1;
-    float ks = 0, vs = 0, ks_next = 0, vs_next = 0;
-    auto look_up = [&](int gi, int &pg, float &k, float &v) {
-        const int tile = tile_begin + gi * NT + lane;
-        pg = tile < tile_end ? pool_page(c, seq, tile >> tile_shift) : -1;
-        const int64_t slot = (int64_t)max(pg, 0) * c.heads + head;
-        k = c.k_scales[slot];
-        v = c.v_scales[slot];
+    // Pages and scales of AHEAD steps, a tile a lane: of the steps whose codes are on their way, and of
+    // those that are multiplied.
+    struct Pages {
+        int64_t at;                             // where the tile's codes are
+        uint64_t there;                         // lanes whose page is
+        float ks, vs;
     };
+    Pages next = {0, 0, 0, 0}, now = next;
+    auto look_up = [&](int gi) {
+        const int tile = tile_begin + gi * NT + lane;
+        const int page = tile < tile_end ? pool_page(c, seq, tile >> tile_shift) : -1;
+        const int64_t slot = (int64_t)max(page, 0) * c.heads + head;
+        next.there = __ballot(page >= 0);
+        next.ks = c.k_scales[slot] * a.scale;
+        next.vs = page >= 0 ? c.v_scales[slot] : 0.0f;
+        next.at = ((slot << tile_shift) + (tile & ((1 << tile_shift) - 1))) * (kTile * D);
+    };
+    auto lane_of = [&](int gi) { return gi % AHEAD * NT; };
     uint4 kc[KU], vc[VU][2];
     auto load = [&](int gi) {                   // a step's codes, this wave's pieces
-        if (gi % AHEAD == 0) look_up(gi, page_next, ks_next, vs_next);
+        if (gi % AHEAD == 0) look_up(gi);
         auto at = [&](const uint8_t *codes, int t, int j) {
-            const int p = __builtin_amdgcn_readlane(page_next, (gi % AHEAD) * NT + t);
-            const int64_t tile = (((int64_t)max(p, 0) * c.heads + head) << tile_shift) +
-                                 ((tile_begin + gi * NT + t) & ((1 << tile_shift) - 1));
-            return *(reinterpret_cast<const uint4 *>(codes + tile * (kTile * D) + 1024 * j) + lane);
+            const int lo = __builtin_amdgcn_readlane((int)next.at, lane_of(gi) + t);
+            const int hi = __builtin_amdgcn_readlane((int)(next.at >> 32), lane_of(gi) + t);
+            const int64_t tile = (int64_t)((uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
+            return *(reinterpret_cast<const uint4 *>(codes + tile + 1024 * j) + lane);
         };
 #pragma unroll
         for (int i = 0; i < KU; ++i) {
-            const int piece = wave + kWaves * i;
-            if (piece < NT * J) kc[i] = at(c.k, piece % NT, piece / NT);
+            const int piece = min(wave + kWaves * i, NT * J - 1);
+            kc[i] = at(c.k, piece % NT, piece / NT);
         }
 #pragma unroll
         for (int i = 0; i < VU; ++i) {
-            const int piece = wave + kWaves * i;
-            if (piece < NT / 2 * J) {
-                vc[i][0] = at(c.v, piece % (NT / 2) * 2, piece / (NT / 2));
-                vc[i][1] = at(c.v, piece % (NT / 2) * 2 + 1, piece / (NT / 2));
-            }
+            const int piece = min(wave + kWaves * i, NT / 2 * J - 1);
+            vc[i][0] = at(c.v, piece % (NT / 2) * 2, piece / (NT / 2));
+            vc[i][1] = at(c.v, piece % (NT / 2) * 2 + 1, piece / (NT / 2));
         }
     };
-    auto convert = [&](int gi) {                // what load() brought, into the buffer of step gi
+    constexpr uint64_t STEP = (1ull << NT) - 1;
+    auto pages_there = [&](const Pages &p, int gi) { return (p.there >> lane_of(gi) & STEP) == STEP; };
+    // Tokens that no row sees may hold anything: NaN codes must not meet the probability 0.
+    auto hide = [&](int gi) {
+        const int tile0 = tile_begin + gi * NT;
+        if (pages_there(next, gi) && tile0 * kTile >= u.lo && (tile0 + NT) * kTile <= u.up) return;
+#pragma unroll
+        for (int i = 0; i < VU; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int t = min(wave + kWaves * i, NT / 2 * J - 1) % (NT / 2) * 2 + h, token = (tile0 + t) * kTile + 4 * g;
+                const bool there = next.there >> (lane_of(gi) + t) & 1;
+                uint32_t keep = 0;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (there && token + r >= u.lo && token + r < u.up) keep |= 0xFFu << (8 * r);
+                vc[i][h].x &= keep; vc[i][h].y &= keep; vc[i][h].z &= keep; vc[i][h].w &= keep;
+            }
+    };
+    // What load() brought, as operands, into the buffer of step gi.  (A wave without a piece of
+    // its own repeats the last one.)
+    auto convert = [&](int gi) {
         const int b = gi & 1;
 #pragma unroll
         for (int i = 0; i < KU; ++i) {
-            const int piece = wave + kWaves * i;
-            if (piece >= NT * J) break;
-            const int t = piece % NT, j = piece / NT;
+            const int piece = min(wave + kWaves * i, NT * J - 1), t = piece % NT, j = piece / NT;
             keys[b][t * 2 * J + 2 * j][lane] = __builtin_bit_cast(v4u, operand<FMT>(kc[i].x, kc[i].y));
             keys[b][t * 2 * J + 2 * j + 1][lane] = __builtin_bit_cast(v4u, operand<FMT>(kc[i].z, kc[i].w));
         }
 #pragma unroll
         for (int i = 0; i < VU; ++i) {
-            const int piece = wave + kWaves * i;
-            if (piece >= NT / 2 * J) break;
-            const int t = piece % (NT / 2) * 2, j = piece / (NT / 2);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                // tokens that no row sees may hold anything: NaN codes must not meet the probability 0
-                const int token = (tile_begin + gi * NT + t + h) * kTile;
-                const bool there = __builtin_amdgcn_readlane(page_next, (gi % AHEAD) * NT + t + h) >= 0;
-                if (!there || token < u.lo || token + kTile > u.up) {
-                    uint32_t keep = 0;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (there && token + 4 * g + r >= u.lo && token + 4 * g + r < u.up) keep |= 0xFFu << (8 * r);
-                    vc[i][h].x &= keep; vc[i][h].y &= keep; vc[i][h].z &= keep; vc[i][h].w &= keep;
-                }
-            }
+            const int piece = min(wave + kWaves * i, NT / 2 * J - 1), t = piece % (NT / 2), j = piece / (NT / 2);
             const uint32_t w0[4] = {vc[i][0].x, vc[i][0].y, vc[i][0].z, vc[i][0].w};
             const uint32_t w1[4] = {vc[i][1].x, vc[i][1].y, vc[i][1].z, vc[i][1].w};
 #pragma unroll
@@ -182,7 +191,62 @@ __global__ __launch_bounds__(64 * kWaves, 2) void wide_kernel(AttentionLaunch a)
                     const uint2 lo = f16_codes<FMT>(w0[d]), hi = f16_codes<FMT>(w1[d]);
                     w = v4u{lo.x, lo.y, hi.x, hi.y};
                 }
-                values[b][t / 2 * DT + 4 * j + d][lane] = w;
+                values[b][t * DT + 4 * j + d][lane] = w;
+            }
+        }
+    };
+
+    // Base: a scale over 2^(base - 127) is between 2^-4 and 2^5, so a probability below fp16's
+    // normal numbers is off by 2^-21 of its value's magnitude at most.
+    int base = 0;                               // y's sums are times 2^(127 - base)
+    float weight = 0.0f;                        // a tile's scale in them
+    uint64_t valued = 0, plain = 0;             // lanes whose tiles have a scale that is not 0, and one near base
+    auto set_base = [&](int to) {
+        base = to;
+        weight = F32 ? now.vs : __builtin_ldexpf(now.vs, 127 - base);
+        valued = __ballot(now.vs != 0.0f);
+        plain = valued & __ballot((unsigned)(exponent(now.vs) - (base - 4)) <= 8u);
+    };
+    auto rebase = [&](int to) {
+        const int next_base = max(to, base - 80);       // sums of 2^30 tokens stay in fp32
+        const float f = __builtin_ldexpf(1.0f, max(base - next_base, -126));
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int d = 0; d < DT; ++d) y[rt][d] *= f;
+        set_base(next_base);
+    };
+    auto value = [&](int b, int t, int d) { return __builtin_bit_cast(v8h, values[b][t / 2 * DT + d][lane]); };
+    // y += V^T P^T of tiles t and t + 1, their probabilities times f0 and f1
+    auto multiply = [&](int b, int t, const v4f (&x)[RT][NT], float f0, float f1) {
+        if constexpr (F32) {
+            v8bf p[RT][TERMS];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) terms<TERMS>(x[rt][t] * f0, x[rt][t + 1] * f1, p[rt]);
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const v8bf v = __builtin_bit_cast(v8bf, value(b, t, d));
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int n = 0; n < TERMS; ++n)
+                        y[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[rt][n], y[rt][d], 0, 0, 0);
+            }
+        } else {
+            v8h p[RT];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    p[rt][i] = (_Float16)(x[rt][t][i] * f0);
+                    p[rt][4 + i] = (_Float16)(x[rt][t + 1][i] * f1);
+                }
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const v8h v = value(b, t, d);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+                    y[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p[rt], y[rt][d], 0, 0, 0);
             }
         }
     };
@@ -190,77 +254,90 @@ __global__ __launch_bounds__(64 * kWaves, 2) void wide_kernel(AttentionLaunch a)
     __syncthreads();                            // the buffers may still be read for the item before
     if (groups > 0) {
         load(0);
+        hide(0);
         convert(0);
-        page = page_next; ks = ks_next; vs = vs_next;
+        now = next;
+        set_base(base);
     }
     if (groups > 1) load(1);
     __syncthreads();
     for (int gi = 0; gi < groups; ++gi) {
-        const int b = gi & 1, tile0 = tile_begin + gi * NT;
-        int mine[NT];
-        float kf[NT], vf[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            mine[t] = __builtin_amdgcn_readlane(page, (gi % AHEAD) * NT + t);
-            kf[t] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), (gi % AHEAD) * NT + t)) * a.scale;
-            vf[t] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs), (gi % AHEAD) * NT + t));
-        }
-        if (gi + 1 < groups) {
-            convert(gi + 1);
-            if ((gi + 1) % AHEAD == 0) {
-                page = page_next; ks = ks_next; vs = vs_next;
-            }
-        }
-        if (gi + 2 < groups) load(gi + 2);
+        const int b = gi & 1, tile0 = tile_begin + gi * NT, lane0 = lane_of(gi);
         const bool needed = tile0 * kTile < any.up && (tile0 + NT) * kTile > any.lo;
-        if (needed) {
-            bool edge = tile0 * kTile < all.lo || (tile0 + NT) * kTile > all.up;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) edge |= mine[t] < 0;
-            v4f x[RT][NT];
+        const bool edge = tile0 * kTile < all.lo || (tile0 + NT) * kTile > all.up || !pages_there(now, gi);
+        v4f x[RT][NT];
+        if (gi + 1 < groups) hide(gi + 1);
+        // Scores: row token 4 g + r of tile t, column the lane's query row.  The next channels'
+        // operands are on their way from the LDS while these are multiplied, and the next step's
+        // codes are converted beside the products.
+        {
+            v8bf kk[2][NT];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
+                kk[0][t] = __builtin_bit_cast(v8bf, keys[b][t * 2 * J][lane]);
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) x[rt][t] = v4f{0, 0, 0, 0};
+            }
 #pragma unroll
-                for (int k = 0; k < 2 * J; ++k) {
-                    const v8bf kk = __builtin_bit_cast(v8bf, keys[b][t * 2 * J + k][lane]);
+            for (int k = 0; k < 2 * J; ++k) {
+                if (k + 1 < 2 * J) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        kk[(k + 1) & 1][t] = __builtin_bit_cast(v8bf, keys[b][t * 2 * J + k + 1][lane]);
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt)
-                        x[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk, q[rt][k], x[rt][t], 0, 0, 0);
-                }
+                        x[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kk[k & 1][t], q[rt][k], x[rt][t], 0, 0, 0);
             }
+            convert(gi + 1);                    // past the last step: what was there, into the free buffer
+        }
+        if (gi + 2 < groups) load(gi + 2);
+        if (needed) {
+            float kf[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) kf[t] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(now.ks), lane0 + t));
             if (edge) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     const int token = (tile0 + t) * kTile + 4 * g;
+                    const bool there = now.there >> (lane0 + t) & 1;
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
 #pragma unroll
                         for (int rt = 0; rt < RT; ++rt)
-                            x[rt][t][r] = mine[t] >= 0 && token + r >= seen[rt].lo && token + r < seen[rt].up
-                                              ? x[rt][t][r] * kf[t]
-                                              : -INFINITY;
+                            x[rt][t][r] = there && token + r >= seen[rt].lo && token + r < seen[rt].up ? x[rt][t][r] * kf[t]
+                                                                                                       : -INFINITY;
                     kf[t] = 1.0f;
-                    if (mine[t] < 0) vf[t] = 0.0f;       // the scale is another page's
+                }
+            }
+            // x kf is the score: the scale of a tile is one for its maximum, and enters each power's argument.
+            // The maximum that powers are taken from moves only when a score is 2^8 past it.
+            float top[RT];
+            bool moves = false;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                top[rt] = m[rt];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    top[rt] = fmaxf(top[rt], fmaxf(fmaxf(x[rt][t][0], x[rt][t][1]), fmaxf(x[rt][t][2], x[rt][t][3])) * kf[t]);
+                top[rt] = row_max(top[rt]);
+                moves |= top[rt] > m[rt] + 8.0f;
+            }
+            if (__any(moves)) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const float f = top[rt] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - top[rt]);
+                    l[rt] *= f;
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) y[rt][d] *= f;
+                    m[rt] = top[rt];
                 }
             }
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                // x kf is the score: the scale of a tile is one for its maximum, and enters each power's argument
-                float top = m[rt];
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    top = fmaxf(top, fmaxf(fmaxf(x[rt][t][0], x[rt][t][1]), fmaxf(x[rt][t][2], x[rt][t][3])) * kf[t]);
-                top = row_max(top);
-                const float from = top == -INFINITY ? 0.0f : top;
-                if (__any(top > m[rt])) {
-                    const float f = __builtin_amdgcn_exp2f(m[rt] - from);
-                    l[rt] *= f;
-#pragma unroll
-                    for (int d = 0; d < DT; ++d) y[rt][d] *= f;
-                    m[rt] = top;
-                }
+                const float from = m[rt] == -INFINITY ? 0.0f : m[rt];        // nothing seen yet: all p are 0
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -269,59 +346,28 @@ __global__ __launch_bounds__(64 * kWaves, 2) void wide_kernel(AttentionLaunch a)
                         l[rt] += x[rt][t][r];
                     }
             }
+            // The tiles whose scales are near base, which is nearly always all of them; then, for what is
+            // left, a base near the first of it.
+            uint64_t left = F32 ? STEP : valued >> lane0 & STEP;
+            while (left) {
+                if (!F32 && (plain >> lane0 & left) == 0)
+                    rebase(exponent(__uint_as_float(
+                        __builtin_amdgcn_readlane(__float_as_uint(now.vs), lane0 + __builtin_ctzll(left)))));
+                const uint64_t mine = F32 ? STEP : plain >> lane0 & left;
+                float f[NT];
 #pragma unroll
-            for (int t = 0; t < NT; t += 2) {
-                if constexpr (F32) {
-                    v8bf p[RT][TERMS];
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) terms<TERMS>(x[rt][t] * vf[t], x[rt][t + 1] * vf[t + 1], p[rt]);
-#pragma unroll
-                    for (int d = 0; d < DT; ++d) {
-                        const v8bf v = __builtin_bit_cast(v8bf, values[b][t / 2 * DT + d][lane]);
-#pragma unroll
-                        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                            for (int n = 0; n < TERMS; ++n)
-                                y[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[rt][n], y[rt][d], 0, 0, 0);
-                    }
-                } else {
-                    // Base: a scale over 2^(base - 127) is between 2^-4 and 2^5, so a probability below
-                    // fp16's normal numbers is off by 2^-21 of its value's magnitude at most.  A pair of tiles
-                    // whose scales are further apart is multiplied a tile at a time.
-                    const int e0 = vf[t] == 0.0f ? 0 : exponent(vf[t]), e1 = vf[t + 1] == 0.0f ? 0 : exponent(vf[t + 1]);
-                    const int high = max(e0, e1), low = min(e0 ? e0 : high, e1 ? e1 : high);
-                    const int rounds = high - low > 4 ? 2 : 1;
-                    for (int round = 0; round < rounds; ++round) {
-                        const int most = rounds == 1 ? high : round ? e1 : e0, least = rounds == 1 ? low : most;
-                        if (most && (most > base + 4 || least < base - 4)) {
-                            const int next = max(most, base - 80);      // sums of 2^30 tokens stay in fp32
-                            const float f = __builtin_ldexpf(1.0f, max(base - next, -126));
-#pragma unroll
-                            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                                for (int d = 0; d < DT; ++d) y[rt][d] *= f;
-                            base = next;
-                        }
-                        float f0 = __builtin_ldexpf(vf[t], 127 - base), f1 = __builtin_ldexpf(vf[t + 1], 127 - base);
-                        if (rounds == 2) (round ? f0 : f1) = 0.0f;
-                        v8h p[RT];
-#pragma unroll
-                        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                p[rt][i] = (_Float16)(x[rt][t][i] * f0);
-                                p[rt][4 + i] = (_Float16)(x[rt][t + 1][i] * f1);
-                            }
-#pragma unroll
-                        for (int d = 0; d < DT; ++d) {
-                            const v8h v = __builtin_bit_cast(v8h, values[b][t / 2 * DT + d][lane]);
-#pragma unroll
-                            for (int rt = 0; rt < RT; ++rt)
-                                y[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p[rt], y[rt][d], 0, 0, 0);
-                        }
-                    }
+                for (int t = 0; t < NT; ++t) {
+                    const uint32_t w = __builtin_amdgcn_readlane(__float_as_uint(weight), lane0 + t);
+                    f[t] = __uint_as_float(mine >> t & 1 ? w : 0u);
                 }
+#pragma unroll
+                for (int t = 0; t < NT; t += 2) multiply(b, t, x, f[t], f[t + 1]);
+                left &= ~mine;
             }
+        }
+        if ((gi + 1) % AHEAD == 0) {
+            now = next;
+            set_base(base);
         }
         __syncthreads();
     }
