@@ -44,13 +44,6 @@ __device__ __forceinline__ SequenceWork sequence_work(const AttentionLaunch &a, 
     return w;
 }
 
-template <int CTRL, int ROW_MASK>
-__device__ __forceinline__ int64_t add_dpp(int64_t v) {
-    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROW_MASK, 0xF, ROW_MASK == 0xF);
-    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(v >> 32), CTRL, ROW_MASK, 0xF, ROW_MASK == 0xF);
-    return v + (int64_t)((uint64_t)hi << 32 | lo);
-}
-
 // What the workgroups find their shares with.
 struct Shares {
     int64_t sums[256];             // steps (for one head) of the sequences up to and with each thread's
@@ -68,12 +61,7 @@ __device__ __forceinline__ void sum_steps(const AttentionLaunch &a, Shares &sh) 
         v += sequence_work<ROWS, STEP>(a, q).all();
         if (s == tid * per) sh.first[tid] = q;
     }
-    v = add_dpp<0x111, 0xF>(v);    // as wave_scan
-    v = add_dpp<0x112, 0xF>(v);
-    v = add_dpp<0x114, 0xF>(v);
-    v = add_dpp<0x118, 0xF>(v);
-    v = add_dpp<0x142, 0xA>(v);
-    v = add_dpp<0x143, 0xC>(v);
+    v = wave_scan(v);
     if ((tid & 63) == 63) sh.waves[tid >> 6] = v;
     __syncthreads();
     for (int w = 0; w < tid >> 6; ++w) v += sh.waves[w];

@@ -1,18 +1,28 @@
 // qlin_cache.hip -- keys and values into a paged 8-bit cache with one scale for
 // each page and head, and back out of it.
 //
-// One workgroup has one page and head of keys or of values, so the page's scale
-// needs no exchange between workgroups, and a call is one launch.  Rows are read
-// and written 16 consecutive bytes a lane; the tiles' order of bytes
-// (include/qlin.h) is made in the LDS.
+// One workgroup (or, for few tokens, one wave) has one page and head of keys or of
+// values, so the page's scale needs no exchange between workgroups, and a call is one
+// launch.  Rows are read and written 16 consecutive bytes a lane; the tiles' order of
+// bytes (include/qlin.h) is made in the LDS.  Bytes bound the large calls: prompts of
+// 11489 tokens (8 heads of 128, bf16, 70 MB) are stored in 21.3 us, 42974 tokens (264
+// MB) read back in 49.8, 5.3 TB/s; 63 without the non-temporal policy on what is
+// written, which nobody reads soon.  Small calls are a chain of dependent loads: offsets
+// and lengths, the page, its scale, 5.0 us with the launch.
 #include "qlin_sequences.h"
 
 namespace qlin {
 
 namespace {
 
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+
 constexpr int kTile = 16;                    // tokens of a tile
 constexpr int kRowPad = 16;                  // bytes behind each LDS row of codes
+// Tokens a sequence, on average, up to which a wave has a page and head, not a
+// workgroup.  32 sequences, us a call: 8 tokens each 5.0 and 5.0, 16 tokens 5.6 and 4.9,
+// 64 tokens 17.5 and 8.0; 256 sequences of one token 5.7 and 16.3.
+constexpr int kFewTokens = 8;
 
 // four codes of a word as fp32
 template <int FMT>
@@ -224,6 +234,90 @@ __global__ __launch_bounds__(256) void append_kernel(RowsLaunch a, int D) {
     }
 }
 
+// The same for few tokens a sequence: a wave has a page and head of keys or of
+// values, and nothing is exchanged.  A lane's eight codes go straight to their places:
+// eight bytes of a key's row, or eight single bytes of values.  Older codes that
+// change are written before them, by the same wave.
+template <int FMT, bool F32>
+__global__ __launch_bounds__(256) void append_few_kernel(RowsLaunch a, int D) {
+    constexpr int NI = 2;                        // passes whose rows stay in registers
+    const CacheArgs &c = a.c;
+    const int lane = threadIdx.x & 63;
+    const int item = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), head = item >> 1;
+    const bool values = item & 1;
+    if (head >= c.heads) return;
+    const PageWork w = page_work(c);
+    if (w.page < 0) return;
+    const int64_t slot = (int64_t)w.page * c.heads + head;
+    float *const scale_at = (values ? c.v_scales : c.k_scales) + slot;
+    uint8_t *const page = (values ? c.v : c.k) + slot * ((int64_t)D << c.page_shift);
+    const int shift = row_lanes_shift(D), ch = (lane & ((1 << shift) - 1)) * 8, row0 = lane >> shift, rows = 64 >> shift;
+    const void *src = values ? a.v : a.k;
+    const int64_t at = (int64_t)(w.row + row0) * (values ? a.ldv : a.ldk) + (int64_t)head * D + ch;
+    const int64_t step = (values ? a.ldv : a.ldk) * rows;
+    const bool live = ch < D;
+    v4f x[NI][2];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        x[i][0] = x[i][1] = v4f{0, 0, 0, 0};
+        if (row0 + i * rows < w.n && live) load_row8<F32>(src, at + i * step, x[i]);
+    }
+    const float was = w.had > 0 ? *scale_at : 0.0f;
+    auto most = [](const v4f (&v)[2]) {
+        float m = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e >> 2][e & 3]));
+        return m;
+    };
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) amax = fmaxf(amax, most(x[i]));
+    for (int i = NI; i * rows < w.n; ++i) {
+        v4f more[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        if (row0 + i * rows < w.n && live) load_row8<F32>(src, at + i * step, more);
+        amax = fmaxf(amax, most(more));
+    }
+    amax = wave_max(amax);
+    const float now = fmaxf(was, amax / qmax_of<FMT>());
+    const float y = recip_scale(now);
+    if (w.had > 0 && now > was) {
+        // pieces of 16 bytes: a key's 16 channels, or four tokens of four channels of values
+        uint4 *const pieces = reinterpret_cast<uint4 *>(page);
+        const int J = D / 64, tiles = (w.had + kTile - 1) / kTile;
+        for (int p = lane; p < tiles * D; p += 64) {
+            const int first = (p >> 6) / J * kTile + (values ? 4 * ((p >> 4) & 3) : p & 15);
+            if (first >= w.had) continue;
+            uint32_t older = 0xFFFFFFFFu;
+            if (values && first + 4 > w.had) older = 0xFFFFFFFFu >> (8 * (first + 4 - w.had));
+            const uint4 o = pieces[p];
+            auto again = [&](uint32_t v) { return (v & ~older) | (requant4<FMT>(v, was, now, y) & older); };
+            pieces[p] = make_uint4(again(o.x), again(o.y), again(o.z), again(o.w));
+        }
+        __threadfence_block();                   // before other lanes store new tokens into the same pieces
+    }
+    if (lane == 0) *scale_at = now;
+    auto store = [&](int r, const v4f (&v)[2]) {
+        const int t = w.had + r, d = ch;
+        const uint2 q = make_uint2(quant4<FMT>(v[0], now, y), quant4<FMT>(v[1], now, y));
+        uint8_t *to = page + (t / kTile) * (kTile * D) + 1024 * (d / 64);
+        if (!values) {
+            *reinterpret_cast<uint2 *>(to + 256 * (d % 64 / 16) + 16 * (t % kTile) + d % 16) = q;
+        } else {
+            to += 256 * (t % kTile / 4) + 16 * (d % 16) + 4 * (d % 64 / 16) + t % 4;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) to[16 * e] = (uint8_t)((e < 4 ? q.x : q.y) >> (8 * (e & 3)));
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+        if (row0 + i * rows < w.n && live) store(row0 + i * rows, x[i]);
+    for (int i = NI; row0 + i * rows < w.n && live; ++i) {
+        v4f more[2];
+        load_row8<F32>(src, at + i * step, more);
+        store(row0 + i * rows, more);
+    }
+}
+
 template <int FMT, bool F32>
 __global__ __launch_bounds__(256) void read_kernel(RowsLaunch a, int D) {
     extern __shared__ uint4 lds[];
@@ -277,12 +371,12 @@ __global__ __launch_bounds__(256) void read_kernel(RowsLaunch a, int D) {
         const int64_t at = (int64_t)(w.row + r) * ld + (int64_t)head * D + ch;
         if constexpr (F32) {
             v4f *to = reinterpret_cast<v4f *>(static_cast<float *>(dst) + at);
-            to[0] = x;
-            to[1] = z;
+            __builtin_nontemporal_store(x, to);
+            __builtin_nontemporal_store(z, to + 1);
         } else {
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(dst) + at) =
-                make_uint4(bf16_bits(x[0]) | (bf16_bits(x[1]) << 16), bf16_bits(x[2]) | (bf16_bits(x[3]) << 16),
-                           bf16_bits(z[0]) | (bf16_bits(z[1]) << 16), bf16_bits(z[2]) | (bf16_bits(z[3]) << 16));
+            const v4u b = {bf16_bits(x[0]) | (bf16_bits(x[1]) << 16), bf16_bits(x[2]) | (bf16_bits(x[3]) << 16),
+                           bf16_bits(z[0]) | (bf16_bits(z[1]) << 16), bf16_bits(z[2]) | (bf16_bits(z[3]) << 16)};
+            __builtin_nontemporal_store(b, reinterpret_cast<v4u *>(static_cast<uint16_t *>(dst) + at));
         }
     }
 }
@@ -291,8 +385,13 @@ size_t page_lds(const CacheArgs &c, int D) { return (size_t)(D + kRowPad) << c.p
 
 template <int FMT, bool F32>
 void launch_append_t(int D, const RowsLaunch &a, hipStream_t s) {
+    const dim3 block(256);
+    if (a.c.T <= kFewTokens * (int64_t)a.c.B) {
+        hipLaunchKernelGGL((append_few_kernel<FMT, F32>), dim3(a.units, (2 * a.c.heads + 3) / 4), block, 0, s, a, D);
+        return;
+    }
     const int rows = 256 >> row_lanes_shift(D), passes = ((1 << a.c.page_shift) + rows - 1) / rows;
-    const dim3 grid(a.units, 2 * a.c.heads), block(256);
+    const dim3 grid(a.units, 2 * a.c.heads);
     const size_t lds = page_lds(a.c, D);
 #define QLIN_APPEND(NI) hipLaunchKernelGGL((append_kernel<FMT, F32, NI>), grid, block, lds, s, a, D)
     if (passes <= 1) QLIN_APPEND(1);

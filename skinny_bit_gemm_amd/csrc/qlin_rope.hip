@@ -5,7 +5,10 @@
 // Each element is read and written once and takes some ten operations, so the
 // memory bounds it.  A head has 8, 16 or 32 lanes of 8 channels each, chosen so
 // that both members of a rotated pair are one lane's: the only exchange is the
-// sum of the squares.
+// sum of the squares.  From 1024 tokens on a workgroup has all heads of its token, so
+// the angles are read once, and writes with the non-temporal policy: 8192 tokens of
+// 72 heads of 128, bf16, 71.7 -> 62.3 -> 59.4 us (5.2 TB/s); with that policy on the
+// reads instead 61.7.
 #include "qlin_device.h"
 
 namespace qlin {
@@ -23,13 +26,17 @@ __device__ __forceinline__ v4f load4(const void *base, int64_t at) {
 
 typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
 
-template <bool F32>
+template <bool F32, bool STREAM>
 __device__ __forceinline__ void store4(void *base, int64_t at, v4f x) {
     if constexpr (F32) {
-        *reinterpret_cast<v4f *>(static_cast<float *>(base) + at) = x;
+        v4f *to = reinterpret_cast<v4f *>(static_cast<float *>(base) + at);
+        if constexpr (STREAM) __builtin_nontemporal_store(x, to);
+        else *to = x;
     } else {
         const v4bf b = {(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3]};   // nearest even
-        *reinterpret_cast<v4bf *>(static_cast<uint16_t *>(base) + at) = b;
+        v4bf *to = reinterpret_cast<v4bf *>(static_cast<uint16_t *>(base) + at);
+        if constexpr (STREAM) __builtin_nontemporal_store(b, to);
+        else *to = b;
     }
 }
 
@@ -41,7 +48,7 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return v;
 }
 
-template <int LANES, bool IN32, bool OUT32>
+template <int LANES, bool IN32, bool OUT32, bool STREAM>
 __global__ __launch_bounds__(256) void rope_kernel(RopeLaunch a) {
     constexpr int HEADS = 256 / LANES;      // heads of a step
     const int t = blockIdx.x;
@@ -104,22 +111,34 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeLaunch a) {
         }
         if (on) {
             void *dst = is_k ? a.k_out : a.q_out;
-            store4<OUT32>(dst, to + at0, x);
-            store4<OUT32>(dst, to + at1, y);
+            store4<OUT32, STREAM>(dst, to + at0, x);
+            store4<OUT32, STREAM>(dst, to + at1, y);
         }
     }
+}
+
+constexpr int kStreamTokens = 1024;
+
+template <int LANES, bool STREAM>
+void launch_types(bool in32, bool out32, const RopeLaunch &a, dim3 grid, hipStream_t s) {
+    const dim3 block(256);
+    if (in32 && out32) hipLaunchKernelGGL((rope_kernel<LANES, true, true, STREAM>), grid, block, 0, s, a);
+    else if (in32) hipLaunchKernelGGL((rope_kernel<LANES, true, false, STREAM>), grid, block, 0, s, a);
+    else if (out32) hipLaunchKernelGGL((rope_kernel<LANES, false, true, STREAM>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((rope_kernel<LANES, false, false, STREAM>), grid, block, 0, s, a);
 }
 
 template <int LANES>
 void launch_lanes(bool in32, bool out32, RopeLaunch a, hipStream_t s) {
     constexpr int HEADS = 256 / LANES;
     const int groups = (a.q_heads + a.kv_heads + HEADS - 1) / HEADS;
-    a.steps = 1;
-    const dim3 grid(a.T, (groups + a.steps - 1) / a.steps), block(256);
-    if (in32 && out32) hipLaunchKernelGGL((rope_kernel<LANES, true, true>), grid, block, 0, s, a);
-    else if (in32) hipLaunchKernelGGL((rope_kernel<LANES, true, false>), grid, block, 0, s, a);
-    else if (out32) hipLaunchKernelGGL((rope_kernel<LANES, false, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((rope_kernel<LANES, false, false>), grid, block, 0, s, a);
+    if (a.T >= kStreamTokens) {
+        a.steps = groups;
+        launch_types<LANES, true>(in32, out32, a, dim3(a.T, 1), s);
+    } else {
+        a.steps = 1;
+        launch_types<LANES, false>(in32, out32, a, dim3(a.T, groups), s);
+    }
 }
 
 }  // namespace

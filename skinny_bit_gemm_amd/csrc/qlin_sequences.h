@@ -25,37 +25,74 @@ __device__ __forceinline__ Sequence sequence_at(const CacheArgs &c, int s) {
     return q;
 }
 
+// v and the one that a lane permutation brings (0 where it brings none)
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ int64_t add_dpp(int64_t v) {
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROW_MASK, 0xF, ROW_MASK == 0xF);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(v >> 32), CTRL, ROW_MASK, 0xF, ROW_MASK == 0xF);
+    return v + (int64_t)((uint64_t)hi << 32 | lo);
+}
+
 // sum of v over the lanes up to and with this one
+__device__ __forceinline__ int64_t wave_scan(int64_t v) {
+    v = add_dpp<0x111, 0xF>(v);    // row_shr:1
+    v = add_dpp<0x112, 0xF>(v);    // row_shr:2
+    v = add_dpp<0x114, 0xF>(v);    // row_shr:4
+    v = add_dpp<0x118, 0xF>(v);    // row_shr:8
+    v = add_dpp<0x142, 0xA>(v);    // row_bcast:15 into rows 1 and 3
+    return add_dpp<0x143, 0xC>(v); // row_bcast:31 into rows 2 and 3
+}
 __device__ __forceinline__ int wave_scan(int v) {
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);    // row_shr:1
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);    // row_shr:2
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);    // row_shr:4
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);    // row_shr:8
-    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast:15 into rows 1 and 3
-    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast:31 into rows 2 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
     return v;
 }
 
-// The sequence that unit u belongs to, where sequence s has count(s) units, and
-// u's number among its units (in *within); -1: u is past the last.  One pass of a
-// wave over 64 sequences at a time: a load, a scan of six steps and a ballot.
-template <typename F>
-__device__ __forceinline__ int unit_sequence(const CacheArgs &c, int u, F count, int *within) {
+// A wave takes 64 PER sequences at a time, PER a lane: their loads together, a scan
+// of six steps and a ballot.  A call has fewer than 2^24 units, so larger counts are
+// of offsets that are none, and sums stay in 32 bits.
+template <int PER, typename F>
+__device__ __forceinline__ int unit_sequence_by(const CacheArgs &c, int64_t u, F count, int *within) {
     const int lane = threadIdx.x & 63;
     int64_t base = 0;                              // units before sequence s0
-    for (int s0 = 0; s0 < c.B; s0 += 64) {
-        const int s = s0 + lane;
-        const int n = s < c.B ? min(count(sequence_at(c, s)), 1 << 24) : 0;   // 64 of them stay in 32 bits
-        const int upto = wave_scan(n);
+    for (int s0 = 0; s0 < c.B; s0 += 64 * PER) {
+        int n[PER], all = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int s = s0 + PER * lane + i;
+            n[i] = s < c.B ? min((int64_t)count(sequence_at(c, s)), (int64_t)(1 << 24) / PER) : 0;
+            all += n[i];
+        }
+        const int upto = wave_scan(all);
         const uint64_t past = __ballot(base + upto > u);
         if (past) {
             const int l = __builtin_ctzll(past);
-            *within = u - (int)base - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(n, l));
-            return s0 + l;
+            int rest = (int)(u - base) - __builtin_amdgcn_readlane(upto, l) + __builtin_amdgcn_readlane(all, l);
+            int s = s0 + PER * l;
+#pragma unroll
+            for (int i = 0; i + 1 < PER; ++i) {
+                const int here = __builtin_amdgcn_readlane(n[i], l);
+                if (rest < here) break;
+                rest -= here;
+                ++s;
+            }
+            *within = rest;
+            return s;
         }
         base += __builtin_amdgcn_readlane(upto, 63);
     }
     return -1;
+}
+
+// The sequence that unit u belongs to, where sequence s has count(s) units, and
+// u's number among its units (in *within); -1: u is past the last.
+template <typename F>
+__device__ __forceinline__ int unit_sequence(const CacheArgs &c, int64_t u, F count, int *within) {
+    return c.B <= 64 ? unit_sequence_by<1>(c, u, count, within) : unit_sequence_by<4>(c, u, count, within);
 }
 
 // pages that a sequence's own tokens of the call touch, and the first of them

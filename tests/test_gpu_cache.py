@@ -174,6 +174,23 @@ def test_many_sequences():
     b.read(new, lengths, table, F32, extra=3)
 
 
+@pytest.mark.parametrize("fmt", [FP8, INT8])
+@pytest.mark.parametrize("type_", [BF16, F32])
+@pytest.mark.parametrize("D,page", [(64, 32), (128, 128), (192, 16), (256, 64)])
+def test_few_tokens_beside_many(fmt, type_, D, page):
+    """Calls on both sides of the average at which a wave has a page, not a workgroup."""
+    b = Both(fmt, 3, D, page, 100)
+    lengths = np.array([50, 3, 90, 20, 1, 0])
+    table = table_of(b.rng, lengths + 60, page, 100)
+    b.append(lengths, lengths, table, type_)
+    for new, amplitude in (([40, 0, 1, 3, 2, 1], 5.0), ([1, 1, 0, 1, 1, 1], 2.0), ([0, 2, 3, 1, 0, 1], 20.0),
+                           ([9, 9, 9, 9, 9, 9], 50.0)):
+        lengths = lengths + new
+        b.append(new, lengths, table, type_, amplitude)
+    b.append([2, 30, 2, 2, 2, 2], lengths, table, type_, 60.0)       # stored over
+    b.read(lengths, lengths, table, type_)
+
+
 def test_absent_tokens_and_bad_tables():
     b = Both(FP8, 2, 64, 16, 8)
     table = np.array([[3, -1, 5], [8, 1 << 30, -(1 << 31)], [1, 2, 4], [0, 7, 6]], dtype=np.int32)

@@ -103,7 +103,7 @@ def test_types(it, ot):
     check(5, 5, 5, 64, 64, 1, it, ot)
 
 
-@pytest.mark.parametrize("T,Hq,Hk", [(1, 16, 8), (1, 1, 1), (2, 64, 8), (61, 32, 4), (300, 7, 1), (1000, 64, 8), (5, 0, 3),
+@pytest.mark.parametrize("T,Hq,Hk", [(1, 16, 8), (1, 1, 1), (2, 64, 8), (61, 32, 4), (300, 7, 1), (1000, 64, 8), (1024, 9, 2), (1500, 3, 3), (5, 0, 3),
                                      (5, 9, 0), (2, 1024, 1024)])
 def test_tokens_and_heads(T, Hq, Hk):
     check(T, Hq, Hk, 128, 128)
@@ -119,6 +119,7 @@ def test_norms_and_no_rotation(norm, R):
 def test_in_place(it):
     check(70, 8, 4, 128, 128, 0, it, it, in_place=True)
     check(70, 8, 4, 128, 96, 1, it, it, in_place=True)
+    check(1100, 2, 1, 64, 64, 0, it, it, in_place=True)
 
 
 def test_amplitudes():
