@@ -248,35 +248,32 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 2 : 1) void attention_kernel
                 for (int j = 0; j < J; ++j) {
                     vc[t][j].x &= keep; vc[t][j].y &= keep; vc[t][j].z &= keep; vc[t][j].w &= keep;
                 }
+                kf[t] = 1.0f;
                 if (mine[t] < 0) vf[t] = 0.0f;       // the scale is another page's
             }
-        } else {
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) x[rt][t] *= kf[t];
         }
+        // x kf is the score: the scale of a tile is one for its maximum, and enters each power's argument.
+        // The maximum that powers are taken from moves only when a score is 2^8 past it.
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
             float top = m[rt];
 #pragma unroll
             for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) top = fmaxf(top, x[rt][t][r]);
+                top = fmaxf(top, fmaxf(fmaxf(x[rt][t][0], x[rt][t][1]), fmaxf(x[rt][t][2], x[rt][t][3])) * kf[t]);
             top = row_max(top);
-            const float from = top == -INFINITY ? 0.0f : top;    // nothing seen yet: all p are 0
-            if (__any(top > m[rt])) {
-                const float f = __builtin_amdgcn_exp2f(m[rt] - from);
+            if (__any(top > m[rt] + 8.0f)) {
+                const float f = top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - top);
                 l[rt] *= f;
 #pragma unroll
                 for (int d = 0; d < DT; ++d) y[rt][d] *= f;
                 m[rt] = top;
             }
+            const float from = m[rt] == -INFINITY ? 0.0f : m[rt];    // nothing seen yet: all p are 0
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    x[rt][t][r] = __builtin_amdgcn_exp2f(x[rt][t][r] - from);
+                    x[rt][t][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[rt][t][r], kf[t], -from));
                     l[rt] += x[rt][t][r];
                     x[rt][t][r] *= vf[t];
                 }
