@@ -13,11 +13,12 @@ namespace qlin {
 namespace {
 
 constexpr int kMostWorkers = 768;
+constexpr int kStep = 128;         // tokens: two tiles of 16 for each wave
 
 // ------------------------------------------------------------ few rows a sequence
 //
 // The cached tokens of every unit, for every key head, are one long line of steps
-// of STEP tokens, and each workgroup takes an equal share of it: the codes are
+// of kStep tokens, and each workgroup takes an equal share of it: the codes are
 // what bounds the call, so all compute units read the same number of them,
 // however the lengths differ.  A unit that lies in one share is written at once;
 // of one that is cut, each workgroup leaves its sums, and join_kernel adds them.
@@ -33,14 +34,14 @@ struct SequenceWork {
     int tiles, tile0, steps;       // row tiles; first tile of 16 tokens, and steps of each
     __device__ __forceinline__ int64_t all() const { return (int64_t)tiles * steps; }
 };
-template <int ROWS, int STEP>
+template <int ROWS>
 __device__ __forceinline__ SequenceWork sequence_work(const AttentionLaunch &a, const Sequence &q) {
     SequenceWork w = {0, 0, 0};
     if (q.n == 0 || (int64_t)q.n * a.group > a.few_rows) return w;
     const Seen first = seen_by(a, q, 0), last = seen_by(a, q, q.n - 1);
     w.tiles = (q.n * a.group + ROWS - 1) / ROWS;
     w.tile0 = first.lo / kTile;
-    w.steps = last.up > first.lo && !a.whole ? (last.up - w.tile0 * kTile + STEP - 1) / STEP : 1;
+    w.steps = last.up > first.lo && !a.whole ? (last.up - w.tile0 * kTile + kStep - 1) / kStep : 1;
     return w;
 }
 
@@ -52,13 +53,13 @@ struct Shares {
 };
 
 // Threads have B / 256 sequences each, in order.
-template <int ROWS, int STEP>
+template <int ROWS>
 __device__ __forceinline__ void sum_steps(const AttentionLaunch &a, Shares &sh) {
     const int tid = threadIdx.x, per = (a.c.B + 255) / 256;
     int64_t v = 0;
     for (int s = tid * per; s < min(a.c.B, (tid + 1) * per); ++s) {
         const Sequence q = sequence_at(a.c, s);
-        v += sequence_work<ROWS, STEP>(a, q).all();
+        v += sequence_work<ROWS>(a, q).all();
         if (s == tid * per) sh.first[tid] = q;
     }
     v = wave_scan(v);
@@ -72,9 +73,8 @@ __device__ __forceinline__ void sum_steps(const AttentionLaunch &a, Shares &sh) 
 // RT: tiles of 16 query rows; all waves have the same rows and take groups of NT
 // tiles of tokens in turn, so a code is read and converted once for all rows.
 template <int D, int FMT, int TERMS, int RT>
-__global__ __launch_bounds__(64 * kWaves, RT == 1 ? 2 : 1) void attention_kernel(AttentionLaunch a) {
-    constexpr int ROWS = 16 * RT, J = D / 64, DT = D / 16, NT = D <= 128 ? 4 : 2;
-    constexpr int STEP = kWaves * NT * kTile;
+__global__ __launch_bounds__(64 * kWaves, RT == 1 || D <= 128 ? 2 : 1) void attention_kernel(AttentionLaunch a) {
+    constexpr int ROWS = 16 * RT, J = D / 64, DT = D / 16, NT = kStep / (kWaves * kTile);
     constexpr int AHEAD = 64 / NT;              // groups whose pages a wave looks up at once
     constexpr bool F32 = TERMS == 3;
     __shared__ float merge[kWaves][16][D + 4];
@@ -87,7 +87,7 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 2 : 1) void attention_kernel
     // this worker's share
     Shares &sh = *reinterpret_cast<Shares *>(merge);
     static_assert(sizeof(Shares) <= sizeof(merge), "they share the LDS");
-    sum_steps<ROWS, STEP>(a, sh);
+    sum_steps<ROWS>(a, sh);
     const int64_t per_head = uniform(sh.sums[255]), steps = per_head * c.heads;
     const int64_t share = quotient(steps + a.workers - 1, a.workers);
     int64_t at = worker * share;
@@ -106,11 +106,11 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 2 : 1) void attention_kernel
         sq = uniform(sh.first[block]);
     }
     __syncthreads();                            // their place is used again
-    SequenceWork sw = sequence_work<ROWS, STEP>(a, sq);
+    SequenceWork sw = sequence_work<ROWS>(a, sq);
     while (begin + sw.all() <= at) {
         begin += sw.all();
         sq = sequence_at(c, ++seq);
-        sw = sequence_work<ROWS, STEP>(a, sq);
+        sw = sequence_work<ROWS>(a, sq);
     }
     int tile = sw.tiles > 1 ? (int)quotient(at - begin, sw.steps) : 0;
     begin += (int64_t)tile * sw.steps;
@@ -120,9 +120,9 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 2 : 1) void attention_kernel
     const int64_t unit_end = begin + sw.steps, stop = min(unit_end, end);
     const bool starts = at == begin, whole = starts && stop == unit_end;
     // tiles of 16 tokens that this worker has of the unit, and that any row sees
-    const int tile_begin = max(sw.tile0 + (int)(at - begin) * (STEP / kTile), u.lo / kTile);
+    const int tile_begin = max(sw.tile0 + (int)(at - begin) * (kStep / kTile), u.lo / kTile);
     int tile_end = u.up > u.lo ? (u.up + kTile - 1) / kTile : 0;
-    if (!a.whole) tile_end = min(tile_end, sw.tile0 + (int)(stop - begin) * (STEP / kTile));
+    if (!a.whole) tile_end = min(tile_end, sw.tile0 + (int)(stop - begin) * (kStep / kTile));
 
     v8bf q[RT][2 * J];
     Seen seen[RT];
@@ -365,7 +365,7 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 ? 2 : 1) void attention_kernel
                 ++head;
             }
             sq = sequence_at(c, seq);
-            sw = sequence_work<ROWS, STEP>(a, sq);
+            sw = sequence_work<ROWS>(a, sq);
         } while (sw.tiles == 0);
     }
     }
@@ -466,8 +466,9 @@ AttentionPlan attention_plan(int sequences, int tokens, int max_context, int kv_
     AttentionPlan p = {};
     if (sequences == 0 || tokens == 0) return p;
     const int64_t all_rows = (int64_t)tokens * group;
-    const int step = head_dim <= 128 ? 256 : 128;
-    const int64_t steps = ((int64_t)max_context + step - 1) / step + 1;
+    const int64_t steps = ((int64_t)max_context + kStep - 1) / kStep + 1;
+    // a unit of so few tokens is read as fast by one workgroup as cut and joined
+    const int whole = head_dim <= 128 ? 4 * kStep : 2 * kStep;
 
     // Which sequences have few rows is known on the device alone: of several, some may
     // have few and some many, and both kernels run, each with its own.
@@ -479,10 +480,12 @@ AttentionPlan attention_plan(int sequences, int tokens, int max_context, int kv_
         p.rows = all_rows <= 16 * (int64_t)sequences || (all_rows > 32 * (int64_t)sequences && group <= 16) ? 16 : 32;
         p.live_rows = (int)std::min<int64_t>(p.rows, all_rows);
         const int64_t units = row_tiles(sequences, tokens, group, p.rows) * kv_heads;
-        // as many workers as are resident at once
-        const int resident = p.rows == 32 ? 1 : head_dim == 64 ? 3 : 2;
-        p.whole = max_context <= 2 * step;
-        p.workers = (int)std::min<int64_t>(p.whole ? kMostWorkers : 256 * resident, p.whole ? units : units * steps);
+        p.whole = max_context <= whole;
+        // As many workers as are resident at once.  (Registers: 122 for heads of 64, 161 of 128, up to 241 of 256;
+        // of 32 rows 204, 256, and over 256 for wider heads.)  With fewer, ragged lengths take longer, 64
+        // contexts of up to 8192 for heads of 64 42.9 us with 512 and 40.4 with 768; with more, they wait.
+        const int64_t most = 256 * (p.rows == 32 && head_dim > 128 ? 1 : head_dim == 64 && p.rows == 16 ? 3 : 2);
+        p.workers = (int)(p.whole ? std::min<int64_t>(units, kMostWorkers) : std::min(most, units * steps));
     }
     if (wide) {
         p.wide_rows = wide_rows(head_dim);
@@ -490,7 +493,7 @@ AttentionPlan attention_plan(int sequences, int tokens, int max_context, int kv_
         p.wide_parts = (int)std::max<int64_t>(1, std::min<int64_t>(kWideItems / p.wide_units, (max_context + kWideChunk - 1) / kWideChunk));
     }
     // The workspace of any plan of as many or fewer sequences, tokens and context
-    if (max_context > std::min(2 * step, kWideChunk)) {      // else no unit is cut
+    if (max_context > std::min(whole, kWideChunk)) {      // else no unit is cut
         const int64_t few_most = std::min<int64_t>(kMostWorkers, row_tiles(sequences, tokens, group, 16) * kv_heads * steps);
         const int64_t slots = few_most * 2 * (all_rows <= 16 ? 16 : 32);
         const int64_t wide_most = std::min<int64_t>(kWideItems, row_tiles(sequences, tokens, group, 64) * kv_heads *
