@@ -458,7 +458,7 @@ int64_t row_tiles(int64_t sequences, int64_t tokens, int group, int rows) {
 }
 
 constexpr int kWideItems = 512;    // (unit, head, part) workgroups that wide units are split for
-constexpr int kWideChunk = 1024;   // expected tokens of a part, at least
+constexpr int kWideChunk = 256;    // expected tokens of a part, at least
 
 }  // namespace
 
@@ -472,12 +472,13 @@ AttentionPlan attention_plan(int sequences, int tokens, int max_context, int kv_
 
     // Which sequences have few rows is known on the device alone: of several, some may
     // have few and some many, and both kernels run, each with its own.
-    const bool wide = (tokens - std::min(sequences, tokens)) * (int64_t)group >= kWideFrom;
+    const bool wide = sequences == 1 ? all_rows >= kWideFromAlone
+                                     : (tokens - std::min(sequences, tokens)) * (int64_t)group >= kWideFrom;
     const bool few = !wide || sequences > 1;
     p.few_rows = !wide ? INT32_MAX : few ? kFewRows : 0;
     if (few) {
-        // 16 rows in a unit, or 32: as a sequence has on average, or of single tokens where that says nothing
-        p.rows = all_rows <= 16 * (int64_t)sequences || (all_rows > 32 * (int64_t)sequences && group <= 16) ? 16 : 32;
+        // 16 rows in a unit, or 32: as a sequence has on average, or a single token beside sequences with many
+        p.rows = all_rows <= 16 * (int64_t)sequences || (wide && group <= 16) ? 16 : 32;
         p.live_rows = (int)std::min<int64_t>(p.rows, all_rows);
         const int64_t units = row_tiles(sequences, tokens, group, p.rows) * kv_heads;
         p.whole = max_context <= whole;
@@ -490,7 +491,8 @@ AttentionPlan attention_plan(int sequences, int tokens, int max_context, int kv_
     if (wide) {
         p.wide_rows = wide_rows(head_dim);
         p.wide_units = row_tiles(sequences, tokens, group, p.wide_rows) * kv_heads;
-        p.wide_parts = (int)std::max<int64_t>(1, std::min<int64_t>(kWideItems / p.wide_units, (max_context + kWideChunk - 1) / kWideChunk));
+        p.wide_parts = (int)std::max<int64_t>(
+            1, std::min<int64_t>(kWideItems / p.wide_units, (max_context + kWideChunk - 1) / kWideChunk));
     }
     // The workspace of any plan of as many or fewer sequences, tokens and context
     if (max_context > std::min(whole, kWideChunk)) {      // else no unit is cut
@@ -498,7 +500,7 @@ AttentionPlan attention_plan(int sequences, int tokens, int max_context, int kv_
         const int64_t slots = few_most * 2 * (all_rows <= 16 ? 16 : 32);
         const int64_t wide_most = std::min<int64_t>(kWideItems, row_tiles(sequences, tokens, group, 64) * kv_heads *
                                                                     ((max_context + kWideChunk - 1) / kWideChunk));
-        const int64_t wide_slots = (tokens - 1) * (int64_t)group >= kWideFrom ? wide_most * 128 : 0;
+        const int64_t wide_slots = all_rows >= kWideFromAlone ? wide_most * 128 : 0;
         p.wide_place = slots;
         p.ml_at = (size_t)(slots + wide_slots) * head_dim * sizeof(float);
         p.cuts_at = p.ml_at + (size_t)(slots + wide_slots) * sizeof(float2);

@@ -237,8 +237,14 @@ struct AttentionLaunch {
     AttentionCut *wide_cuts;   // [wide_units]
 };
 
-constexpr int kFewRows = 64;       // measured: see qlin_attention_wide.hip
-constexpr int kWideFrom = 512;     // rows beyond one token a sequence from which the second kernel runs too
+// Which kernel a sequence is for.  Of several, one with more than kFewRows rows has the wide one (16 sequences of
+// 128 rows over 2000 tokens 80 us, 104 in the other; of 64 rows 61 and 68 the other way round), where the call's rows
+// beyond a token for each are kWideFrom or more: below, the second launch costs more (4 sequences of 128 rows over
+// 4000 tokens 47 us with it, 36 without).  A sequence alone needs no second kernel, only the other one (over 8000 tokens,
+// 128 rows 25.6 and 30.0 us, 512 rows 45 and 58; 64 rows the other way round).
+constexpr int kFewRows = 64;
+constexpr int kWideFrom = 512;
+constexpr int kWideFromAlone = 96;
 inline int wide_rows(int head_dim) { return head_dim <= 192 ? 128 : 64; }
 
 // Host-side selection table (qlin_table.cpp).
