@@ -627,10 +627,13 @@ typedef struct {
  *   q   bf16 [T, ldq], head h at columns h D ..
  *   y   [T, ldy] of out_type (QLIN_OUT_BF16 or QLIN_OUT_F32_ACC); not q.  A
  *       token that sees nothing gets zeros
- * Products with the codes are exact, sums and the softmax are fp32; the
- * probabilities enter the second product with 16 bits of mantissa (24 where y is
- * fp32); y is rounded once.  What lies in absent or unseen tokens' places, NaN
- * codes among it, does not matter.
+ * Products with the codes are exact, sums and the softmax are fp32.  The
+ * probabilities enter the second product with 24 bits of mantissa where y is
+ * fp32; where it is bf16, with 16, or 11 in sequences of many rows (tokens times
+ * q_heads / kv_heads: over 64).  y is rounded once.  What lies in absent or unseen
+ * tokens' places, NaN codes among it, does not matter.
+ * One call takes prompts and single tokens together; its time is best where
+ * max_context is near the longest sequence.
  *   workspace  qlin_cache_attention_workspace_bytes(...) bytes (may be 0), of
  *              counts and max_context only: as any of sequences, tokens and
  *              max_context grows it never shrinks.  Needs no initial value.
