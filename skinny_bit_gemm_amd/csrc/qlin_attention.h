@@ -143,6 +143,11 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
                      (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32);
 }
 
+__device__ __forceinline__ int64_t readlane(int64_t v, int lane) {
+    return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)v, lane) |
+                     (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32);
+}
+
 __device__ __forceinline__ Sequence uniform(const Sequence &q) {
     Sequence r;
     r.first = __builtin_amdgcn_readfirstlane(q.first);

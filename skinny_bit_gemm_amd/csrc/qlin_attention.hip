@@ -57,11 +57,14 @@ template <int ROWS>
 __device__ __forceinline__ void sum_steps(const AttentionLaunch &a, Shares &sh) {
     const int tid = threadIdx.x, per = (a.c.B + 255) / 256;
     int64_t v = 0;
-    for (int s = tid * per; s < min(a.c.B, (tid + 1) * per); ++s) {
-        const Sequence q = sequence_at(a.c, s);
-        v += sequence_work<ROWS>(a, q).all();
-        if (s == tid * per) sh.first[tid] = q;
+    const int from = tid * per, to = min(a.c.B, from + per);
+    if (from < to) {
+        const Sequence q = sequence_at(a.c, from);
+        sh.first[tid] = q;
+        v = sequence_work<ROWS>(a, q).all();
     }
+#pragma unroll 4
+    for (int s = from + 1; s < to; ++s) v += sequence_work<ROWS>(a, sequence_at(a.c, s)).all();
     v = wave_scan(v);
     if ((tid & 63) == 63) sh.waves[tid >> 6] = v;
     __syncthreads();
@@ -101,17 +104,30 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 || D <= 128 ? 2 : 1) void atte
         int block = 0;                          // the thread whose sequences have it
 #pragma unroll
         for (int i = 0; i < 4; ++i) block += __popcll(__ballot(sh.sums[64 * i + lane] <= at - begin));
-        seq = block * ((c.B + 255) / 256);
         begin += block ? uniform(sh.sums[block - 1]) : 0;
+        const int per = (c.B + 255) / 256;
+        seq = block * per;
         sq = uniform(sh.first[block]);
+        if (per > 1) {
+            for (int from = seq;; from += 64) {
+                const int s = from + lane;
+                Sequence q = {};
+                if (s < c.B) q = sequence_at(c, s);
+                const int64_t mine = sequence_work<ROWS>(a, q).all(), upto = wave_scan(mine);
+                const uint64_t past = __ballot(begin + upto > at);
+                if (past) {
+                    const int l = __builtin_ctzll(past);
+                    begin += readlane(upto - mine, l);
+                    seq = from + l;
+                    sq = lane_of(q, l);
+                    break;
+                }
+                begin += readlane(upto, 63);
+            }
+        }
     }
     __syncthreads();                            // their place is used again
     SequenceWork sw = sequence_work<ROWS>(a, sq);
-    while (begin + sw.all() <= at) {
-        begin += sw.all();
-        sq = sequence_at(c, ++seq);
-        sw = sequence_work<ROWS>(a, sq);
-    }
     int tile = sw.tiles > 1 ? (int)quotient(at - begin, sw.steps) : 0;
     begin += (int64_t)tile * sw.steps;
 
@@ -359,14 +375,25 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 || D <= 128 ? 2 : 1) void atte
     at = begin = unit_end;
     if (++tile == sw.tiles) {
         tile = 0;
-        do {
-            if (++seq == c.B) {
-                seq = 0;
+        // 64 at a time: a padded batch may have hundreds without tokens
+        for (int from = seq + 1;;) {
+            const int s = from + lane;
+            Sequence q = {};
+            if (s < c.B) q = sequence_at(c, s);
+            const uint64_t some = __ballot(sequence_work<ROWS>(a, q).tiles > 0);
+            if (some) {
+                const int l = __builtin_ctzll(some);
+                seq = from + l;
+                sq = lane_of(q, l);
+                break;
+            }
+            from += 64;
+            if (from >= c.B) {
+                from = 0;
                 ++head;
             }
-            sq = sequence_at(c, seq);
-            sw = sequence_work<ROWS>(a, sq);
-        } while (sw.tiles == 0);
+        }
+        sw = sequence_work<ROWS>(a, sq);
     }
     }
 }

@@ -52,6 +52,12 @@ __device__ __forceinline__ int wave_scan(int v) {
     return v;
 }
 
+// the sequence that a lane has, in scalar registers
+__device__ __forceinline__ Sequence lane_of(const Sequence &q, int lane) {
+    return Sequence{__builtin_amdgcn_readlane(q.first, lane), __builtin_amdgcn_readlane(q.n, lane),
+                    __builtin_amdgcn_readlane(q.start, lane), __builtin_amdgcn_readlane(q.length, lane)};
+}
+
 // A wave takes 64 PER sequences at a time, PER a lane: their loads together, a scan
 // of six steps and a ballot.  A call has fewer than 2^24 units, so larger counts are
 // of offsets that are none, and sums stay in 32 bits.

@@ -103,7 +103,7 @@ class Call:
                                           to_dev(self.table), self.table.shape[1], context or self.longest)
         self.work = guarded((q.qlin_cache_attention_workspace_bytes(self.attention, self.cache, self.sequences),),
                             torch.uint8, 0xFF)
-        print(f"[attention] fmt={fmt} new={list(new)[:8]} lengths={list(lengths)[:8]} heads={Hq}/{Hk} D={D} page={page} "
+        print(f"[attention] fmt={fmt} new={[int(v) for v in new[:8]]} lengths={[int(v) for v in lengths[:8]]} heads={Hq}/{Hk} D={D} page={page} "
               f"out={out} causal={causal} window={window} context={context}", flush=True)
 
     def run(self, stream=None):
@@ -239,6 +239,19 @@ def test_many_sequences():
     new = np.minimum(rng.integers(0, 3, 200), lengths)
     check(FP8, new, lengths, 2, 1, 64, 16)
     check(INT8, [1] * 200, lengths, 2, 1, 64, 16, F32)
+
+
+def test_padded_batches():
+    """Hundreds of sequences without tokens between and behind the others."""
+    rng = np.random.default_rng(9)
+    for B, live in ((300, [0, 7, 299]), (300, [150]), (700, [3, 64, 65, 690]), (5000, [17, 2400, 4999])):
+        new, lengths = np.zeros(B, int), np.zeros(B, int)
+        lengths[rng.integers(0, B, 20)] = 30
+        for s in live:
+            new[s], lengths[s] = 1 + s % 3, 600 + s % 7
+        check(FP8, new, lengths, 8, 4, 64, 16, F32, extra=4)
+        new[live[0]] = 200
+        check(FP8, new, lengths, 8, 4, 64, 16, BF16)
 
 
 def test_offsets_are_clamped():
