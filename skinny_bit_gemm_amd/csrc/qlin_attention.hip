@@ -22,9 +22,15 @@ constexpr int kStep = 128;         // tokens: two tiles of 16 for each wave
 // what bounds the call, so all compute units read the same number of them,
 // however the lengths differ.  A unit that lies in one share is written at once;
 // of one that is cut, each workgroup leaves its sums, and join_kernel adds them.
-// Where a context is expected to be no longer than a step, a unit is one step of
-// any length: none is cut, and the second launch is left out.
-
+// Where contexts are expected to be short, a unit is one step of any length: none
+// is cut, and the second launch is left out (one sequence of 500 tokens 7.7 us, 9.8
+// with it; of 1000 the other way round, 12.2 and 10.5).
+//
+// 64 sequences of 300 to 16384 tokens, 64 query heads over 8 of 128, e4m3 (534 MB of
+// codes): 100 us, 92 of them this kernel, 5.8 TB/s; equal parts of each sequence
+// instead, 164.  131071 tokens of one sequence, 269 MB: 51 us.  What the steps
+// measured: codes of the next step asked for while this one is multiplied, and their
+// stream with the non-temporal policy, each 10 %.
 // a / b, both not negative; 64-bit divisions take some 100 instructions
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     return (a | b) >> 32 == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
@@ -398,7 +404,9 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 || D <= 128 ? 2 : 1) void atte
     }
 }
 
-// The sums of a unit that was cut.  A workgroup has a row.
+// The sums of a unit that was cut.  A workgroup has a row, its parts in sets beside
+// each other: 4.6 us for 64 parts of 4 rows (one set after another 13.7), most of it
+// three dependent loads.
 template <int D, bool F32>
 __global__ __launch_bounds__(256) void join_kernel(AttentionLaunch a, const AttentionCut *cuts) {
     constexpr int LANES = D / 4, SETS = 256 / LANES;
@@ -494,7 +502,7 @@ AttentionPlan attention_plan(int sequences, int tokens, int max_context, int kv_
     if (sequences == 0 || tokens == 0) return p;
     const int64_t all_rows = (int64_t)tokens * group;
     const int64_t steps = ((int64_t)max_context + kStep - 1) / kStep + 1;
-    // a unit of so few tokens is read as fast by one workgroup as cut and joined
+    // a unit of so few tokens is read as fast by one workgroup as cut and joined (see above)
     const int whole = head_dim <= 128 ? 4 * kStep : 2 * kStep;
 
     // Which sequences have few rows is known on the device alone: of several, some may

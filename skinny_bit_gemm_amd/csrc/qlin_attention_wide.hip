@@ -13,6 +13,17 @@
 // holds them exactly.  The scales of the values would leave its range, so they enter
 // relative to a power of two that the sums are kept in, and that follows the scales
 // (Base).  Where y is fp32: three bf16 terms, 24 bits.
+//
+// 3558 tokens of three prompts over up to 8192, 32 query heads over 8 of 128, e4m3, y
+// bf16 (370 GFLOP): 498 us, 740 TFLOP/s.  Of a step's 6800 cycles for the two waves of a
+// SIMD the matrix cores work 2050 (32 and 32 products a wave), the vector ALUs some 3200
+// (300 instructions and 34 powers a wave), the LDS 2560; with two waves what is left
+// are the waits between them.  Without conversions it takes 425 us, without powers 35
+// less, without either product about as long.  Measured and slower: 16 rows a wave and
+// eight waves (674), eight waves of 32 rows (545), steps of 32 tokens (604; with three
+// waves a SIMD 734, spilled), the two tiles of rows one behind the other so that
+// powers and products share a stretch (740: each reads the LDS for itself, and
+// spills), 635 with maxima that move each time and a branch for each tile's edge and scale.
 #include "qlin_attention.h"
 
 namespace qlin {
