@@ -13,6 +13,7 @@ namespace qlin {
 namespace {
 
 constexpr int kMostWorkers = 768;
+constexpr int64_t kMostSteps = (int64_t)1 << 51;
 constexpr int kStep = 128;         // tokens: two tiles of 16 for each wave
 
 // ------------------------------------------------------------ few rows a sequence
@@ -58,7 +59,8 @@ struct Shares {
     Sequence first[256];           // each thread's first sequence
 };
 
-// Threads have B / 256 sequences each, in order.
+// Threads have B / 256 sequences each, in order.  Sums over 2^51 are of offsets that go back;
+// as clamped, products with the heads stay in 64 bits, and a search ends.
 template <int ROWS>
 __device__ __forceinline__ void sum_steps(const AttentionLaunch &a, Shares &sh) {
     const int tid = threadIdx.x, per = (a.c.B + 255) / 256;
@@ -70,12 +72,12 @@ __device__ __forceinline__ void sum_steps(const AttentionLaunch &a, Shares &sh) 
         v = sequence_work<ROWS>(a, q).all();
     }
 #pragma unroll 4
-    for (int s = from + 1; s < to; ++s) v += sequence_work<ROWS>(a, sequence_at(a.c, s)).all();
+    for (int s = from + 1; s < to; ++s) v = min(v + sequence_work<ROWS>(a, sequence_at(a.c, s)).all(), kMostSteps);
     v = wave_scan(v);
     if ((tid & 63) == 63) sh.waves[tid >> 6] = v;
     __syncthreads();
     for (int w = 0; w < tid >> 6; ++w) v += sh.waves[w];
-    sh.sums[tid] = v;
+    sh.sums[tid] = min(v, kMostSteps);
     __syncthreads();
 }
 

@@ -59,8 +59,9 @@ __device__ __forceinline__ Sequence lane_of(const Sequence &q, int lane) {
 }
 
 // A wave takes 64 PER sequences at a time, PER a lane: their loads together, a scan
-// of six steps and a ballot.  A call has fewer than 2^24 units, so larger counts are
-// of offsets that are none, and sums stay in 32 bits.
+// of six steps and a ballot.  A call has fewer than 2^24 units, so larger sums are of
+// offsets that go back; as clamped they stay in 32 bits, and a unit among its
+// sequence's.
 template <int PER, typename F>
 __device__ __forceinline__ int unit_sequence_by(const CacheArgs &c, int64_t u, F count, int *within) {
     const int lane = threadIdx.x & 63;
@@ -70,9 +71,10 @@ __device__ __forceinline__ int unit_sequence_by(const CacheArgs &c, int64_t u, F
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int s = s0 + PER * lane + i;
-            n[i] = s < c.B ? min((int64_t)count(sequence_at(c, s)), (int64_t)(1 << 24) / PER) : 0;
+            n[i] = s < c.B ? min((int)count(sequence_at(c, s)), 1 << 24) : 0;
             all += n[i];
         }
+        all = min(all, 1 << 24);
         const int upto = wave_scan(all);
         const uint64_t past = __ballot(base + upto > u);
         if (past) {

@@ -267,6 +267,23 @@ def test_offsets_are_clamped():
     assert torch.equal(c.y, want)
 
 
+def test_offsets_that_go_back():
+    """Sequences that overlap in their rows: whose result stays is open, but nothing else is written."""
+    for B, T in ((100, 50), (300, 200), (40, 7)):
+        new = np.zeros(B, int)
+        new[0] = T
+        c = Call(FP8, new, np.full(B, 230), 16, 4, 64, 16, extra=5)
+        offsets = torch.tensor([0, T] * (B // 2) + [0], dtype=torch.int32)
+        c.sequences.tensors[0].copy_(offsets)
+        c.run()
+        torch.cuda.synchronize()
+        check_guards(c.y, c.work, what="qlin_cache_attention")
+        full = c.y.cpu().numpy()
+        assert (full[T:] == 9).all() and (full[:, c.Hq * c.D:] == 9).all()
+        got = wl.bf16_bits_to_f32(full.view(np.uint16)[:T, :c.Hq * c.D])
+        assert np.isfinite(got).all()
+
+
 def test_the_same_bits_every_time_and_with_other_sequences_beside():
     c = Call(FP8, [1, 1], [3000, 1200], 8, 2, 128, 64, F32)
     c.run()

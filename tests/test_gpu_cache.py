@@ -215,6 +215,21 @@ def test_offsets_are_clamped():
     b.check("append")
 
 
+def test_offsets_that_go_back():
+    """Two sequences that take the same rows, into pages of their own."""
+    b = Both(FP8, 2, 64, 16, 12)
+    table = np.arange(12, dtype=np.int32).reshape(3, 4)
+    dev, x, ld = b.rows(40, BF16)
+    s = q.make_sequences(3, 40, to_dev(np.array([0, 40, 0, 40], np.int32)), to_dev(np.array([40, 9, 40], np.int32)),
+                         to_dev(table), 4, 40)
+    q.qlin_cache_append(b.cache, s, dev[0], ld, dev[1], ld)
+    torch.cuda.synchronize()
+    for i in (0, 2):
+        b.ref.append([0, 40], [40], table[i:i + 1], *x)
+    # a call of 40 tokens has 40 / 16 + 2 x 3 page places at most: the second's six fit too
+    b.check("append")
+
+
 def test_rows_past_the_last_sequence_and_empty_calls():
     b = Both(FP8, 2, 64, 16, 8)
     table = table_of(b.rng, [20, 20], 16, 8)
