@@ -95,11 +95,22 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 || D <= 128 ? 2 : 1) void atte
     const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-    // this worker's share
+    // this worker's share: of up to 64 sequences each wave finds it by itself, a sequence a lane
     Shares &sh = *reinterpret_cast<Shares *>(merge);
     static_assert(sizeof(Shares) <= sizeof(merge), "they share the LDS");
-    sum_steps<ROWS>(a, sh);
-    const int64_t per_head = uniform(sh.sums[255]), steps = per_head * c.heads;
+    const bool by_wave = c.B <= 64;
+    Sequence lane_q = {};
+    int64_t lane_all = 0, lane_upto = 0, per_head;
+    if (by_wave) {
+        if (lane < c.B) lane_q = sequence_at(c, lane);
+        lane_all = sequence_work<ROWS>(a, lane_q).all();
+        lane_upto = wave_scan(lane_all);
+        per_head = readlane(lane_upto, 63);
+    } else {
+        sum_steps<ROWS>(a, sh);
+        per_head = uniform(sh.sums[255]);
+    }
+    const int64_t steps = per_head * c.heads;
     const int64_t share = quotient(steps + a.workers - 1, a.workers);
     int64_t at = worker * share;
     const int64_t end = min(steps, at + share);
@@ -108,7 +119,22 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 || D <= 128 ? 2 : 1) void atte
     int head = (int)quotient(at, per_head), seq;
     int64_t begin = (int64_t)head * per_head;   // of the sequence, and then of the unit
     Sequence sq;
-    {
+    // among 64 sequences from `from` on, a lane each, the one that has step `at`
+    auto find_lane = [&](int from, const Sequence &q, int64_t all, int64_t upto) {
+        const uint64_t past = __ballot(begin + upto > at);
+        if (past == 0) {
+            begin += readlane(upto, 63);
+            return false;
+        }
+        const int l = __builtin_ctzll(past);
+        begin += readlane(upto - all, l);
+        seq = from + l;
+        sq = lane_of(q, l);
+        return true;
+    };
+    if (by_wave) {
+        find_lane(0, lane_q, lane_all, lane_upto);
+    } else {
         int block = 0;                          // the thread whose sequences have it
 #pragma unroll
         for (int i = 0; i < 4; ++i) block += __popcll(__ballot(sh.sums[64 * i + lane] <= at - begin));
@@ -116,25 +142,15 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 || D <= 128 ? 2 : 1) void atte
         const int per = (c.B + 255) / 256;
         seq = block * per;
         sq = uniform(sh.first[block]);
-        if (per > 1) {
-            for (int from = seq;; from += 64) {
-                const int s = from + lane;
-                Sequence q = {};
-                if (s < c.B) q = sequence_at(c, s);
-                const int64_t mine = sequence_work<ROWS>(a, q).all(), upto = wave_scan(mine);
-                const uint64_t past = __ballot(begin + upto > at);
-                if (past) {
-                    const int l = __builtin_ctzll(past);
-                    begin += readlane(upto - mine, l);
-                    seq = from + l;
-                    sq = lane_of(q, l);
-                    break;
-                }
-                begin += readlane(upto, 63);
-            }
+        for (int from = seq; per > 1; from += 64) {
+            const int s = from + lane;
+            Sequence q = {};
+            if (s < c.B) q = sequence_at(c, s);
+            const int64_t all = sequence_work<ROWS>(a, q).all();
+            if (find_lane(from, q, all, wave_scan(all))) break;
         }
+        __syncthreads();                        // their place is used again
     }
-    __syncthreads();                            // their place is used again
     SequenceWork sw = sequence_work<ROWS>(a, sq);
     int tile = sw.tiles > 1 ? (int)quotient(at - begin, sw.steps) : 0;
     begin += (int64_t)tile * sw.steps;
