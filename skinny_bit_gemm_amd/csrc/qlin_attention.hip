@@ -156,269 +156,269 @@ __global__ __launch_bounds__(64 * kWaves, RT == 1 || D <= 128 ? 2 : 1) void atte
     begin += (int64_t)tile * sw.steps;
 
     while (true) {
-    const Unit u = unit_at(a, seq, sq, tile, ROWS);
-    const int64_t unit_end = begin + sw.steps, stop = min(unit_end, end);
-    const bool starts = at == begin, whole = starts && stop == unit_end;
-    // tiles of 16 tokens that this worker has of the unit, and that any row sees
-    const int tile_begin = max(sw.tile0 + (int)(at - begin) * (kStep / kTile), u.lo / kTile);
-    int tile_end = u.up > u.lo ? (u.up + kTile - 1) / kTile : 0;
-    if (!a.whole) tile_end = min(tile_end, sw.tile0 + (int)(stop - begin) * (kStep / kTile));
+        const Unit u = unit_at(a, seq, sq, tile, ROWS);
+        const int64_t unit_end = begin + sw.steps, stop = min(unit_end, end);
+        const bool starts = at == begin, whole = starts && stop == unit_end;
+        // tiles of 16 tokens that this worker has of the unit, and that any row sees
+        const int tile_begin = max(sw.tile0 + (int)(at - begin) * (kStep / kTile), u.lo / kTile);
+        int tile_end = u.up > u.lo ? (u.up + kTile - 1) / kTile : 0;
+        if (!a.whole) tile_end = min(tile_end, sw.tile0 + (int)(stop - begin) * (kStep / kTile));
 
-    v8bf q[RT][2 * J];
-    Seen seen[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const int row = min(rt * 16 + col, u.rows - 1);
-        const uint16_t *from = a.q + row_at(a, u, row, a.ldq, head, D);
-#pragma unroll
-        for (int k = 0; k < 2 * J; ++k)
-            q[rt][k] = query(a, from, k, g);
-        seen[rt] = seen_by(a, u.q, (u.row0 + row) / a.group);
-    }
-
-    v4f y[RT][DT];
-    float m[RT], l[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        m[rt] = -INFINITY;
-        l[rt] = 0.0f;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) y[rt][d] = v4f{0, 0, 0, 0};
-    }
-
-    const int tile_shift = c.page_shift - 4;    // tiles of a page, log2
-    const int groups = tile_end > tile_begin ? (tile_end - tile_begin + NT - 1) / NT : 0;
-    int page = -1;
-    float ks = 0.0f, vs = 0.0f;
-    int there[NT];                              // pages of the tiles whose codes are on their way
-    float kf[NT], vf[NT];
-    int64_t tile_at[NT];                        // where they are, in tiles
-    // a group's pages: every AHEAD groups a wave looks them up, a tile a lane
-    auto find = [&](int gi, int k) {
-        if (k % AHEAD == 0) {
-            const int tile = tile_begin + (gi + kWaves * (lane / NT)) * NT + lane % NT;
-            page = tile < tile_end ? pool_page(c, u.seq, tile >> tile_shift) : -1;
-            const int64_t slot = (int64_t)max(page, 0) * c.heads + head;
-            ks = c.k_scales[slot];
-            vs = c.v_scales[slot];
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            there[t] = __builtin_amdgcn_readlane(page, (k % AHEAD) * NT + t);
-            tile_at[t] = (((int64_t)max(there[t], 0) * c.heads + head) << tile_shift) +
-                         ((tile_begin + gi * NT + t) & ((1 << tile_shift) - 1));
-        }
-    };
-    auto find_scales = [&](int k) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            kf[t] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), (k % AHEAD) * NT + t)) * a.scale;
-            vf[t] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs), (k % AHEAD) * NT + t));
-        }
-    };
-    uint4 kc[NT][J], vc[NT][J];
-    auto load = [&](uint4 (&to)[NT][J], const uint8_t *codes) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const v4u *p = reinterpret_cast<const v4u *>(codes + tile_at[t] * (kTile * D)) + lane;
-#pragma unroll
-            for (int j = 0; j < J; ++j) to[t][j] = __builtin_bit_cast(uint4, __builtin_nontemporal_load(p + 64 * j));
-        }
-    };
-    if (wave < groups) {
-        find(wave, 0);
-        load(kc, c.k);
-        __builtin_amdgcn_sched_barrier(0);      // in this order the keys can be waited for alone
-        load(vc, c.v);
-    }
-    for (int gi = wave, k = 0; gi < groups; gi += kWaves, ++k) {
-        const int tile0 = tile_begin + gi * NT;
-        find_scales(k);
-        bool edge = tile0 * kTile < u.all_lo || (tile0 + NT) * kTile > u.all_up;
-        int mine[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            mine[t] = there[t];
-            edge |= mine[t] < 0;
-        }
-        const bool more = gi + kWaves < groups;
-        // scores: row token 4 g + r of tile t, column the lane's query row.  The
-        // barriers keep conversions beside the products that take them: hoisted over
-        // them, they double the registers.
-        v4f x[RT][NT];
-#pragma unroll
-        for (int t = 0; t < NT; t += 2) {
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) x[rt][t] = x[rt][t + 1] = v4f{0, 0, 0, 0};
-#pragma unroll
-            for (int k = 0; k < 2 * J; ++k) {
-                const uint4 &c0 = kc[t][k >> 1], &c1 = kc[t + 1][k >> 1];
-                const v8bf k0 = k & 1 ? operand<FMT>(c0.z, c0.w) : operand<FMT>(c0.x, c0.y);
-                const v8bf k1 = k & 1 ? operand<FMT>(c1.z, c1.w) : operand<FMT>(c1.x, c1.y);
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    x[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q[rt][k], x[rt][t], 0, 0, 0);
-                    x[rt][t + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, q[rt][k], x[rt][t + 1], 0, 0, 0);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        }
-        // the next keys, while these scores become probabilities and meet the values
-        if (more) {
-            find(gi + kWaves, k + 1);
-            load(kc, c.k);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        if (edge) {
-            // tokens that no row sees may hold anything: NaN codes must not meet the probability 0
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int token = (tile0 + t) * kTile + 4 * g;
-                uint32_t keep = 0;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const bool any = mine[t] >= 0 && token + r >= u.lo && token + r < u.up;
-                    if (any) keep |= 0xFFu << (8 * r);
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-                        x[rt][t][r] = any && token + r >= seen[rt].lo && token + r < seen[rt].up ? x[rt][t][r] * kf[t]
-                                                                                                 : -INFINITY;
-                }
-#pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    vc[t][j].x &= keep; vc[t][j].y &= keep; vc[t][j].z &= keep; vc[t][j].w &= keep;
-                }
-                kf[t] = 1.0f;
-                if (mine[t] < 0) vf[t] = 0.0f;       // the scale is another page's
-            }
-        }
-        // x kf is the score: the scale of a tile is one for its maximum, and enters each power's argument.
-        // The maximum that powers are taken from moves only when a score is 2^8 past it.
+        v8bf q[RT][2 * J];
+        Seen seen[RT];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            float top = m[rt];
+            const int row = min(rt * 16 + col, u.rows - 1);
+            const uint16_t *from = a.q + row_at(a, u, row, a.ldq, head, D);
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-                top = fmaxf(top, fmaxf(fmaxf(x[rt][t][0], x[rt][t][1]), fmaxf(x[rt][t][2], x[rt][t][3])) * kf[t]);
-            top = row_max(top);
-            if (__any(top > m[rt] + 8.0f)) {
-                const float f = top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - top);
-                l[rt] *= f;
-#pragma unroll
-                for (int d = 0; d < DT; ++d) y[rt][d] *= f;
-                m[rt] = top;
-            }
-            const float from = m[rt] == -INFINITY ? 0.0f : m[rt];    // nothing seen yet: all p are 0
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    x[rt][t][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[rt][t][r], kf[t], -from));
-                    l[rt] += x[rt][t][r];
-                    x[rt][t][r] *= vf[t];
-                }
+            for (int k = 0; k < 2 * J; ++k)
+                q[rt][k] = query(a, from, k, g);
+            seen[rt] = seen_by(a, u.q, (u.row0 + row) / a.group);
         }
-        __builtin_amdgcn_sched_barrier(0);
-        // second product, 32 tokens and 32 channels at a time
-#pragma unroll
-        for (int t = 0; t < NT; t += 2) {
-            v8bf p[RT][TERMS];
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) terms<TERMS>(x[rt][t], x[rt][t + 1], p[rt]);
-#pragma unroll
-            for (int d = 0; d < DT; d += 2) {
-                const uint4 &c0 = vc[t][d >> 2], &c1 = vc[t + 1][d >> 2];
-                const v8bf v0 = d & 2 ? operand<FMT>(c0.z, c1.z) : operand<FMT>(c0.x, c1.x);
-                const v8bf v1 = d & 2 ? operand<FMT>(c0.w, c1.w) : operand<FMT>(c0.y, c1.y);
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int n = 0; n < TERMS; ++n) {
-                        y[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, p[rt][n], y[rt][d], 0, 0, 0);
-                        y[rt][d + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, p[rt][n], y[rt][d + 1], 0, 0, 0);
-                    }
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        }
-        if (more) load(vc, c.v);
-    }
 
-    // the waves' sums together, 16 rows at a time
-    const int64_t slot = 2 * worker + (starts ? 1 : 0);
+        v4f y[RT][DT];
+        float m[RT], l[RT];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        __syncthreads();                        // the last ones are read
-        const float sum = row_sum(l[rt]);
-        if (g == 0) merge_ml[wave][col] = make_float2(m[rt], sum);
+        for (int rt = 0; rt < RT; ++rt) {
+            m[rt] = -INFINITY;
+            l[rt] = 0.0f;
 #pragma unroll
-        for (int d = 0; d < DT; ++d) *reinterpret_cast<v4f *>(&merge[wave][col][16 * d + 4 * g]) = y[rt][d];
-        __syncthreads();
-        const int r = threadIdx.x >> 4, row = rt * 16 + r;
-        if (row >= u.rows) continue;
-        float2 ml[kWaves];
-        float top = -INFINITY, total = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            ml[w] = merge_ml[w][r];
-            top = fmaxf(top, ml[w].x);
+            for (int d = 0; d < DT; ++d) y[rt][d] = v4f{0, 0, 0, 0};
         }
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            ml[w].x = ml[w].x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml[w].x - top);
-            total += ml[w].x * ml[w].y;
-        }
-        const float by = total > 0.0f ? 1.0f / total : 0.0f;
-        const int64_t to = row_at(a, u, row, a.ldy, head, D);
-#pragma unroll
-        for (int k = 0; k < J; ++k) {
-            const int d = 64 * k + 4 * (threadIdx.x & 15);
-            v4f v = {0, 0, 0, 0};
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) v += *reinterpret_cast<const v4f *>(&merge[w][r][d]) * ml[w].x;
-            if (whole) store_y4<F32>(a.y, to + d, v * by);
-            else *reinterpret_cast<v4f *>(a.part_o + (slot * ROWS + row) * D + d) = v;
-        }
-        if (!whole && (threadIdx.x & 15) == 0) a.part_ml[slot * ROWS + row] = make_float2(top, total);
-    }
-    if (stop == end) {
-        if (threadIdx.x == 0 && starts && !whole) {      // the unit goes on in other shares
-            AttentionCut cut;
-            cut.parts = (int)quotient(unit_end - 1, share) - worker + 1;
-            cut.place0 = (2 * worker + 1) * ROWS;
-            cut.place = 2 * worker * ROWS;
-            cut.step = 2 * ROWS;
-            cut.head = head;
-            cut.first = u.q.first;
-            cut.row0 = u.row0;
-            cut.rows = u.rows;
-            a.cuts[worker] = cut;
-        }
-        return;
-    }
-    // the next unit: the sequence's next row tile, the next sequence, the next head
-    at = begin = unit_end;
-    if (++tile == sw.tiles) {
-        tile = 0;
-        // 64 at a time: a padded batch may have hundreds without tokens
-        for (int from = seq + 1;;) {
-            const int s = from + lane;
-            Sequence q = {};
-            if (s < c.B) q = sequence_at(c, s);
-            const uint64_t some = __ballot(sequence_work<ROWS>(a, q).tiles > 0);
-            if (some) {
-                const int l = __builtin_ctzll(some);
-                seq = from + l;
-                sq = lane_of(q, l);
-                break;
+
+        const int tile_shift = c.page_shift - 4;    // tiles of a page, log2
+        const int groups = tile_end > tile_begin ? (tile_end - tile_begin + NT - 1) / NT : 0;
+        int page = -1;
+        float ks = 0.0f, vs = 0.0f;
+        int there[NT];                              // pages of the tiles whose codes are on their way
+        float kf[NT], vf[NT];
+        int64_t tile_at[NT];                        // where they are, in tiles
+        // a group's pages: every AHEAD groups a wave looks them up, a tile a lane
+        auto find = [&](int gi, int k) {
+            if (k % AHEAD == 0) {
+                const int tile = tile_begin + (gi + kWaves * (lane / NT)) * NT + lane % NT;
+                page = tile < tile_end ? pool_page(c, u.seq, tile >> tile_shift) : -1;
+                const int64_t slot = (int64_t)max(page, 0) * c.heads + head;
+                ks = c.k_scales[slot];
+                vs = c.v_scales[slot];
             }
-            from += 64;
-            if (from >= c.B) {
-                from = 0;
-                ++head;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                there[t] = __builtin_amdgcn_readlane(page, (k % AHEAD) * NT + t);
+                tile_at[t] = (((int64_t)max(there[t], 0) * c.heads + head) << tile_shift) +
+                             ((tile_begin + gi * NT + t) & ((1 << tile_shift) - 1));
             }
+        };
+        auto find_scales = [&](int k) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                kf[t] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), (k % AHEAD) * NT + t)) * a.scale;
+                vf[t] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs), (k % AHEAD) * NT + t));
+            }
+        };
+        uint4 kc[NT][J], vc[NT][J];
+        auto load = [&](uint4 (&to)[NT][J], const uint8_t *codes) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const v4u *p = reinterpret_cast<const v4u *>(codes + tile_at[t] * (kTile * D)) + lane;
+#pragma unroll
+                for (int j = 0; j < J; ++j) to[t][j] = __builtin_bit_cast(uint4, __builtin_nontemporal_load(p + 64 * j));
+            }
+        };
+        if (wave < groups) {
+            find(wave, 0);
+            load(kc, c.k);
+            __builtin_amdgcn_sched_barrier(0);      // in this order the keys can be waited for alone
+            load(vc, c.v);
         }
-        sw = sequence_work<ROWS>(a, sq);
-    }
+        for (int gi = wave, k = 0; gi < groups; gi += kWaves, ++k) {
+            const int tile0 = tile_begin + gi * NT;
+            find_scales(k);
+            bool edge = tile0 * kTile < u.all_lo || (tile0 + NT) * kTile > u.all_up;
+            int mine[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                mine[t] = there[t];
+                edge |= mine[t] < 0;
+            }
+            const bool more = gi + kWaves < groups;
+            // scores: row token 4 g + r of tile t, column the lane's query row.  The
+            // barriers keep conversions beside the products that take them: hoisted over
+            // them, they double the registers.
+            v4f x[RT][NT];
+#pragma unroll
+            for (int t = 0; t < NT; t += 2) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) x[rt][t] = x[rt][t + 1] = v4f{0, 0, 0, 0};
+#pragma unroll
+                for (int k = 0; k < 2 * J; ++k) {
+                    const uint4 &c0 = kc[t][k >> 1], &c1 = kc[t + 1][k >> 1];
+                    const v8bf k0 = k & 1 ? operand<FMT>(c0.z, c0.w) : operand<FMT>(c0.x, c0.y);
+                    const v8bf k1 = k & 1 ? operand<FMT>(c1.z, c1.w) : operand<FMT>(c1.x, c1.y);
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        x[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q[rt][k], x[rt][t], 0, 0, 0);
+                        x[rt][t + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, q[rt][k], x[rt][t + 1], 0, 0, 0);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            // the next keys, while these scores become probabilities and meet the values
+            if (more) {
+                find(gi + kWaves, k + 1);
+                load(kc, c.k);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if (edge) {
+                // tokens that no row sees may hold anything: NaN codes must not meet the probability 0
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const int token = (tile0 + t) * kTile + 4 * g;
+                    uint32_t keep = 0;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const bool any = mine[t] >= 0 && token + r >= u.lo && token + r < u.up;
+                        if (any) keep |= 0xFFu << (8 * r);
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt)
+                            x[rt][t][r] = any && token + r >= seen[rt].lo && token + r < seen[rt].up ? x[rt][t][r] * kf[t]
+                                                                                                     : -INFINITY;
+                    }
+#pragma unroll
+                    for (int j = 0; j < J; ++j) {
+                        vc[t][j].x &= keep; vc[t][j].y &= keep; vc[t][j].z &= keep; vc[t][j].w &= keep;
+                    }
+                    kf[t] = 1.0f;
+                    if (mine[t] < 0) vf[t] = 0.0f;       // the scale is another page's
+                }
+            }
+            // x kf is the score: the scale of a tile is one for its maximum, and enters each power's argument.
+            // The maximum that powers are taken from moves only when a score is 2^8 past it.
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                float top = m[rt];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    top = fmaxf(top, fmaxf(fmaxf(x[rt][t][0], x[rt][t][1]), fmaxf(x[rt][t][2], x[rt][t][3])) * kf[t]);
+                top = row_max(top);
+                if (__any(top > m[rt] + 8.0f)) {
+                    const float f = top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - top);
+                    l[rt] *= f;
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) y[rt][d] *= f;
+                    m[rt] = top;
+                }
+                const float from = m[rt] == -INFINITY ? 0.0f : m[rt];    // nothing seen yet: all p are 0
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        x[rt][t][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[rt][t][r], kf[t], -from));
+                        l[rt] += x[rt][t][r];
+                        x[rt][t][r] *= vf[t];
+                    }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            // second product, 32 tokens and 32 channels at a time
+#pragma unroll
+            for (int t = 0; t < NT; t += 2) {
+                v8bf p[RT][TERMS];
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) terms<TERMS>(x[rt][t], x[rt][t + 1], p[rt]);
+#pragma unroll
+                for (int d = 0; d < DT; d += 2) {
+                    const uint4 &c0 = vc[t][d >> 2], &c1 = vc[t + 1][d >> 2];
+                    const v8bf v0 = d & 2 ? operand<FMT>(c0.z, c1.z) : operand<FMT>(c0.x, c1.x);
+                    const v8bf v1 = d & 2 ? operand<FMT>(c0.w, c1.w) : operand<FMT>(c0.y, c1.y);
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                        for (int n = 0; n < TERMS; ++n) {
+                            y[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, p[rt][n], y[rt][d], 0, 0, 0);
+                            y[rt][d + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, p[rt][n], y[rt][d + 1], 0, 0, 0);
+                        }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            if (more) load(vc, c.v);
+        }
+
+        // the waves' sums together, 16 rows at a time
+        const int64_t slot = 2 * worker + (starts ? 1 : 0);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            __syncthreads();                        // the last ones are read
+            const float sum = row_sum(l[rt]);
+            if (g == 0) merge_ml[wave][col] = make_float2(m[rt], sum);
+#pragma unroll
+            for (int d = 0; d < DT; ++d) *reinterpret_cast<v4f *>(&merge[wave][col][16 * d + 4 * g]) = y[rt][d];
+            __syncthreads();
+            const int r = threadIdx.x >> 4, row = rt * 16 + r;
+            if (row >= u.rows) continue;
+            float2 ml[kWaves];
+            float top = -INFINITY, total = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                ml[w] = merge_ml[w][r];
+                top = fmaxf(top, ml[w].x);
+            }
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                ml[w].x = ml[w].x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml[w].x - top);
+                total += ml[w].x * ml[w].y;
+            }
+            const float by = total > 0.0f ? 1.0f / total : 0.0f;
+            const int64_t to = row_at(a, u, row, a.ldy, head, D);
+#pragma unroll
+            for (int k = 0; k < J; ++k) {
+                const int d = 64 * k + 4 * (threadIdx.x & 15);
+                v4f v = {0, 0, 0, 0};
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) v += *reinterpret_cast<const v4f *>(&merge[w][r][d]) * ml[w].x;
+                if (whole) store_y4<F32>(a.y, to + d, v * by);
+                else *reinterpret_cast<v4f *>(a.part_o + (slot * ROWS + row) * D + d) = v;
+            }
+            if (!whole && (threadIdx.x & 15) == 0) a.part_ml[slot * ROWS + row] = make_float2(top, total);
+        }
+        if (stop == end) {
+            if (threadIdx.x == 0 && starts && !whole) {      // the unit goes on in other shares
+                AttentionCut cut;
+                cut.parts = (int)quotient(unit_end - 1, share) - worker + 1;
+                cut.place0 = (2 * worker + 1) * ROWS;
+                cut.place = 2 * worker * ROWS;
+                cut.step = 2 * ROWS;
+                cut.head = head;
+                cut.first = u.q.first;
+                cut.row0 = u.row0;
+                cut.rows = u.rows;
+                a.cuts[worker] = cut;
+            }
+            return;
+        }
+        // the next unit: the sequence's next row tile, the next sequence, the next head
+        at = begin = unit_end;
+        if (++tile == sw.tiles) {
+            tile = 0;
+            // 64 at a time: a padded batch may have hundreds without tokens
+            for (int from = seq + 1;;) {
+                const int s = from + lane;
+                Sequence q = {};
+                if (s < c.B) q = sequence_at(c, s);
+                const uint64_t some = __ballot(sequence_work<ROWS>(a, q).tiles > 0);
+                if (some) {
+                    const int l = __builtin_ctzll(some);
+                    seq = from + l;
+                    sq = lane_of(q, l);
+                    break;
+                }
+                from += 64;
+                if (from >= c.B) {
+                    from = 0;
+                    ++head;
+                }
+            }
+            sw = sequence_work<ROWS>(a, sq);
+        }
     }
 }
 

@@ -11,19 +11,23 @@
 // Where y is bf16, probabilities enter the second product as one fp16 number (11
 // bits of mantissa, 2^-11 against 2^-8 of y's own rounding), and codes as fp16, which
 // holds them exactly.  The scales of the values would leave its range, so they enter
-// relative to a power of two that the sums are kept in, and that follows the scales
-// (Base).  Where y is fp32: three bf16 terms, 24 bits.
+// relative to a power of two for each part of a unit, which looks at all its pages'
+// scales first: over 2^(base - 127) they are between 2^-4 and 2^7, so no probability
+// times its scale is past fp16's range, and one below fp16's normal numbers is off by
+// 2^-21 of its value's magnitude at most.  A part whose scales differ by more than 2^10,
+// which is rare, takes two bf16 terms.  Where y is fp32: three, 24 bits.
 //
 // 3558 tokens of three prompts over up to 8192, 32 query heads over 8 of 128, e4m3, y
-// bf16 (370 GFLOP): 498 us, 740 TFLOP/s.  Of a step's 6800 cycles for the two waves of a
-// SIMD the matrix cores work 2050 (32 and 32 products a wave), the vector ALUs some 3200
-// (300 instructions and 34 powers a wave), the LDS 2560; with two waves what is left
-// are the waits between them.  Without conversions it takes 425 us, without powers 35
-// less, without either product about as long.  Measured and slower: 16 rows a wave and
-// eight waves (674), eight waves of 32 rows (545), steps of 32 tokens (604; with three
-// waves a SIMD 734, spilled), the two tiles of rows one behind the other so that
-// powers and products share a stretch (740: each reads the LDS for itself, and
-// spills), 635 with maxima that move each time and a branch for each tile's edge and scale.
+// bf16 (370 GFLOP): 442 us, 840 TFLOP/s.  The powers of two tiles are computed beside the
+// products of the two before, whose operands are read from the LDS a while before: 499 us with
+// all powers first, 491 with reads next to their products.  With two waves a SIMD (of a
+// step, 2050 cycles of the matrix cores, some 3200 of the vector ALUs and 2560 of the LDS)
+// what is left are the waits between them.  Measured and slower: 16 rows a wave and
+// eight waves (674 where this was 500), eight waves of 32 rows (545), steps of 32 tokens
+// (604; with three waves a SIMD 734, spilled), the two tiles of rows one behind the other
+// (740: each reads the LDS for itself, and spills), a base that moves with the scales
+// (557: its path costs the registers of the other), maxima that move each time and a branch for
+// each tile's edge and scale (635), waves of a higher priority in the products (523).
 #include "qlin_attention.h"
 
 namespace qlin {
@@ -52,42 +56,31 @@ __device__ __forceinline__ uint2 f16_codes(uint32_t w) {
 // exponent of a scale's power of two, in fp32's bias; of those too small for it, the lowest
 __device__ __forceinline__ int exponent(float v) { return max((int)(__float_as_uint(v) >> 23 & 0xFFu), 1); }
 
-template <int D, int FMT, bool F32, int RT>
-__global__ __launch_bounds__(64 * kWaves, 2) void wide_kernel(AttentionLaunch a) {
-    constexpr int WROWS = 16 * RT, ROWS = kWaves * WROWS, J = D / 64, DT = D / 16, NT = D <= 128 ? 4 : 2;
-    constexpr int AHEAD = 64 / NT, TERMS = F32 ? 3 : 1;
-    constexpr int KU = (NT * J + kWaves - 1) / kWaves, VU = (NT / 2 * J + kWaves - 1) / kWaves;   // a wave's pieces of a step
-    __shared__ v4u keys[2][NT * 2 * J][64];
-    __shared__ v4u values[2][NT / 2 * DT][64];
+// A step's tiles, and its operands in the LDS.
+constexpr int tiles_of_step(int D) { return D <= 128 ? 4 : 2; }
+
+template <int D>
+struct Operands {
+    v4u keys[2][tiles_of_step(D) * (D / 32)][64];
+    v4u values[2][tiles_of_step(D) / 2 * (D / 16)][64];
+};
+
+// A part of a unit: what its tokens of tiles tile_begin to tile_end add.  TERMS: bf16 terms of a
+// probability, or 0 for one fp16 number.
+template <int D, int FMT, bool F32, int RT, int TERMS>
+__device__ __forceinline__ void unit_part(const AttentionLaunch &a, Operands<D> &sh, const Unit &u, int seq, int head,
+                                          int tile_begin, int tile_end, int base, int64_t place, int part) {
+    constexpr int WROWS = 16 * RT, ROWS = kWaves * WROWS, J = D / 64, DT = D / 16, NT = tiles_of_step(D);
+    constexpr int AHEAD = 64 / NT;
+    constexpr int PRE = NT / 2 * DT < 8 ? NT / 2 * DT : 8;
+    // a wave's pieces of a step
+    constexpr int KU = (NT * J + kWaves - 1) / kWaves, VU = (NT / 2 * J + kWaves - 1) / kWaves;
+    auto &keys = sh.keys;
+    auto &values = sh.values;
     const CacheArgs &c = a.c;
     const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tile_shift = c.page_shift - 4;
-
-    const int64_t items = a.wide_units * a.wide_parts;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int part = (int)(item / a.wide_units);
-    const int64_t place = item - part * a.wide_units;       // (unit, head): heads beside each other
-    const int unit = (int)(place / c.heads), head = (int)(place - (int64_t)unit * c.heads);
-    int within;
-    auto tiles_of = [&](const Sequence &q) {
-        return (int64_t)q.n * a.group > a.few_rows ? (q.n * a.group + ROWS - 1) / ROWS : 0;
-    };
-    const int seq = unit_sequence(c, unit, tiles_of, &within);
-    if (seq < 0) {
-        if (a.wide_parts > 1 && part == 0 && threadIdx.x == 0) a.wide_cuts[place].parts = 0;
-        continue;
-    }
-    const Sequence sq = sequence_at(c, seq);
-    // the last rows first: of a prompt, they see the most
-    const Unit u = unit_at(a, seq, sq, tiles_of(sq) - 1 - within, ROWS);
-    int tile_begin = u.lo / kTile, tile_end = u.up > u.lo ? (u.up + kTile - 1) / kTile : tile_begin;
-    if (a.wide_parts > 1) {
-        // whole steps of the unit's tokens in each part
-        const int steps = (tile_end - tile_begin + NT - 1) / NT, from = tile_begin, all = tile_end;
-        tile_begin = from + (int)((int64_t)steps * part / a.wide_parts) * NT;
-        tile_end = min(all, from + (int)((int64_t)steps * (part + 1) / a.wide_parts) * NT);
-    }
     const int groups = tile_end > tile_begin ? (tile_end - tile_begin + NT - 1) / NT : 0;
 
     // this wave's rows, and what they see
@@ -125,7 +118,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void wide_kernel(AttentionLaunch a)
     struct Pages {
         int64_t at;                             // where the tile's codes are
         uint64_t there;                         // lanes whose page is
-        float ks, vs;
+        float ks, weight;                       // of keys, and of values times 2^(127 - base)
     };
     Pages next = {0, 0, 0, 0}, now = next;
     auto look_up = [&](int gi) {
@@ -134,7 +127,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void wide_kernel(AttentionLaunch a)
         const int64_t slot = (int64_t)max(page, 0) * c.heads + head;
         next.there = __ballot(page >= 0);
         next.ks = c.k_scales[slot] * a.scale;
-        next.vs = page >= 0 ? c.v_scales[slot] : 0.0f;
+        next.weight = page >= 0 ? __builtin_ldexpf(c.v_scales[slot], 127 - base) : 0.0f;
         next.at = ((slot << tile_shift) + (tile & ((1 << tile_shift) - 1))) * (kTile * D);
     };
     auto lane_of = [&](int gi) { return gi % AHEAD * NT; };
@@ -169,7 +162,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void wide_kernel(AttentionLaunch a)
         for (int i = 0; i < VU; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int t = min(wave + kWaves * i, NT / 2 * J - 1) % (NT / 2) * 2 + h, token = (tile0 + t) * kTile + 4 * g;
+                const int t = min(wave + kWaves * i, NT / 2 * J - 1) % (NT / 2) * 2 + h;
+                const int token = (tile0 + t) * kTile + 4 * g;
                 const bool there = next.there >> (lane_of(gi) + t) & 1;
                 uint32_t keep = 0;
 #pragma unroll
@@ -196,7 +190,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void wide_kernel(AttentionLaunch a)
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
                 v4u w;
-                if constexpr (F32) {
+                if constexpr (TERMS > 0) {
                     w = __builtin_bit_cast(v4u, operand<FMT>(w0[d], w1[d]));
                 } else {
                     const uint2 lo = f16_codes<FMT>(w0[d]), hi = f16_codes<FMT>(w1[d]);
@@ -207,36 +201,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void wide_kernel(AttentionLaunch a)
         }
     };
 
-    // Base: a scale over 2^(base - 127) is between 2^-4 and 2^5, so a probability below fp16's
-    // normal numbers is off by 2^-21 of its value's magnitude at most.
-    int base = 0;                               // y's sums are times 2^(127 - base)
-    float weight = 0.0f;                        // a tile's scale in them
-    uint64_t valued = 0, plain = 0;             // lanes whose tiles have a scale that is not 0, and one near base
-    auto set_base = [&](int to) {
-        base = to;
-        weight = F32 ? now.vs : __builtin_ldexpf(now.vs, 127 - base);
-        valued = __ballot(now.vs != 0.0f);
-        plain = valued & __ballot((unsigned)(exponent(now.vs) - (base - 4)) <= 8u);
-    };
-    auto rebase = [&](int to) {
-        const int next_base = max(to, base - 80);       // sums of 2^30 tokens stay in fp32
-        const float f = __builtin_ldexpf(1.0f, max(base - next_base, -126));
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int d = 0; d < DT; ++d) y[rt][d] *= f;
-        set_base(next_base);
-    };
-    auto value = [&](int b, int t, int d) { return __builtin_bit_cast(v8h, values[b][t / 2 * DT + d][lane]); };
     // y += V^T P^T of tiles t and t + 1, their probabilities times f0 and f1
-    auto multiply = [&](int b, int t, const v4f (&x)[RT][NT], float f0, float f1) {
-        if constexpr (F32) {
+    auto multiply = [&](int t, const v4f (&x)[RT][NT], float f0, float f1, auto &&value) {
+        if constexpr (TERMS > 0) {
             v8bf p[RT][TERMS];
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) terms<TERMS>(x[rt][t] * f0, x[rt][t + 1] * f1, p[rt]);
 #pragma unroll
             for (int d = 0; d < DT; ++d) {
-                const v8bf v = __builtin_bit_cast(v8bf, value(b, t, d));
+                const v8bf v = __builtin_bit_cast(v8bf, value(d));
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -254,7 +227,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void wide_kernel(AttentionLaunch a)
                 }
 #pragma unroll
             for (int d = 0; d < DT; ++d) {
-                const v8h v = value(b, t, d);
+                const v8h v = __builtin_bit_cast(v8h, value(d));
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt)
                     y[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p[rt], y[rt][d], 0, 0, 0);
@@ -268,7 +241,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void wide_kernel(AttentionLaunch a)
         hide(0);
         convert(0);
         now = next;
-        set_base(base);
     }
     if (groups > 1) load(1);
     __syncthreads();
@@ -306,10 +278,16 @@ __global__ __launch_bounds__(64 * kWaves, 2) void wide_kernel(AttentionLaunch a)
         }
         if (gi + 2 < groups) load(gi + 2);
         if (needed) {
+            // the first values, a while before they are multiplied
+            v4u ready[PRE];
+#pragma unroll
+            for (int i = 0; i < PRE; ++i) ready[i] = values[b][i][lane];
+            __builtin_amdgcn_sched_barrier(0);
             float kf[NT];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) kf[t] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(now.ks), lane0 + t));
-            if (edge) {
+            for (int t = 0; t < NT; ++t)
+                kf[t] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(now.ks), lane0 + t));
+            if (__builtin_expect(edge, 0)) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     const int token = (tile0 + t) * kTile + 4 * g;
@@ -317,9 +295,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void wide_kernel(AttentionLaunch a)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
 #pragma unroll
-                        for (int rt = 0; rt < RT; ++rt)
-                            x[rt][t][r] = there && token + r >= seen[rt].lo && token + r < seen[rt].up ? x[rt][t][r] * kf[t]
-                                                                                                       : -INFINITY;
+                        for (int rt = 0; rt < RT; ++rt) {
+                            const bool sees = there && token + r >= seen[rt].lo && token + r < seen[rt].up;
+                            x[rt][t][r] = sees ? x[rt][t][r] * kf[t] : -INFINITY;
+                        }
                     kf[t] = 1.0f;
                 }
             }
@@ -331,12 +310,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void wide_kernel(AttentionLaunch a)
             for (int rt = 0; rt < RT; ++rt) {
                 top[rt] = m[rt];
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    top[rt] = fmaxf(top[rt], fmaxf(fmaxf(x[rt][t][0], x[rt][t][1]), fmaxf(x[rt][t][2], x[rt][t][3])) * kf[t]);
+                for (int t = 0; t < NT; ++t) {
+                    const v4f &s = x[rt][t];
+                    top[rt] = fmaxf(top[rt], fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])) * kf[t]);
+                }
                 top[rt] = row_max(top[rt]);
                 moves |= top[rt] > m[rt] + 8.0f;
             }
-            if (__any(moves)) {
+            if (__builtin_expect(__any(moves), 0)) {
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
                     const float f = top[rt] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - top[rt]);
@@ -346,44 +327,39 @@ __global__ __launch_bounds__(64 * kWaves, 2) void wide_kernel(AttentionLaunch a)
                     m[rt] = top[rt];
                 }
             }
+            float from[RT];                         // where nothing is seen yet, all p are 0
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                const float from = m[rt] == -INFINITY ? 0.0f : m[rt];        // nothing seen yet: all p are 0
+            for (int rt = 0; rt < RT; ++rt) from[rt] = m[rt] == -INFINITY ? 0.0f : m[rt];
+            auto powers = [&](int t) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        x[rt][t][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[rt][t][r], kf[t], -from));
-                        l[rt] += x[rt][t][r];
+                    for (int i = 0; i < 8; ++i) {
+                        const float p = x[rt][t + i / 4][i % 4];
+                        x[rt][t + i / 4][i % 4] = __builtin_amdgcn_exp2f(__builtin_fmaf(p, kf[t + i / 4], -from[rt]));
+                        l[rt] += x[rt][t + i / 4][i % 4];
                     }
-            }
-            // The tiles whose scales are near base, which is nearly always all of them; then, for what is
-            // left, a base near the first of it.
-            uint64_t left = F32 ? STEP : valued >> lane0 & STEP;
-            while (left) {
-                if (!F32 && (plain >> lane0 & left) == 0)
-                    rebase(exponent(__uint_as_float(
-                        __builtin_amdgcn_readlane(__float_as_uint(now.vs), lane0 + __builtin_ctzll(left)))));
-                const uint64_t mine = F32 ? STEP : plain >> lane0 & left;
-                float f[NT];
+            };
+            auto weight_of = [&](int t) {
+                return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(now.weight), lane0 + t));
+            };
+            // powers of two tiles beside the products of the two before
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const uint32_t w = __builtin_amdgcn_readlane(__float_as_uint(weight), lane0 + t);
-                    f[t] = __uint_as_float(mine >> t & 1 ? w : 0u);
-                }
-#pragma unroll
-                for (int t = 0; t < NT; t += 2) multiply(b, t, x, f[t], f[t + 1]);
-                left &= ~mine;
+            for (int t = 0; t < NT; t += 2) {
+                powers(t);
+                multiply(t, x, weight_of(t), weight_of(t + 1), [&](int d) {
+                    const int piece = t / 2 * DT + d;
+                    const v4u v = ready[piece % PRE];
+                    if (piece + PRE < NT / 2 * DT) ready[piece % PRE] = values[b][piece + PRE][lane];
+                    return v;
+                });
             }
         }
-        if ((gi + 1) % AHEAD == 0) {
-            now = next;
-            set_base(base);
-        }
+        if ((gi + 1) % AHEAD == 0) now = next;
         __syncthreads();
     }
 
-    const float unit_of_y = F32 ? 1.0f : __builtin_ldexpf(1.0f, base - 127);
+    const float unit_of_y = __builtin_ldexpf(1.0f, base - 127);
     const int64_t first_place = a.wide_place + (place * a.wide_parts + part) * ROWS;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -402,17 +378,74 @@ __global__ __launch_bounds__(64 * kWaves, 2) void wide_kernel(AttentionLaunch a)
             for (int d = 0; d < DT; ++d) store_y4<F32>(a.y, to + 16 * d + 4 * g, y[rt][d] * by);
         }
     }
-    if (a.wide_parts > 1 && part == 0 && threadIdx.x == 0) {
-        AttentionCut cut;
-        cut.parts = a.wide_parts;
-        cut.place0 = cut.place = (int)first_place;
-        cut.step = ROWS;
-        cut.head = head;
-        cut.first = u.q.first;
-        cut.row0 = u.row0;
-        cut.rows = u.rows;
-        a.wide_cuts[place] = cut;
-    }
+}
+
+template <int D, int FMT, bool F32, int RT>
+__global__ __launch_bounds__(64 * kWaves, 2) void wide_kernel(AttentionLaunch a) {
+    constexpr int ROWS = kWaves * 16 * RT, NT = tiles_of_step(D);
+    __shared__ Operands<D> sh;
+    const CacheArgs &c = a.c;
+    const int lane = threadIdx.x & 63, tile_shift = c.page_shift - 4;
+
+    const int64_t items = a.wide_units * a.wide_parts;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int part = (int)(item / a.wide_units);
+        const int64_t place = item - part * a.wide_units;       // (unit, head): heads beside each other
+        const int unit = (int)(place / c.heads), head = (int)(place - (int64_t)unit * c.heads);
+        int within;
+        auto tiles_of = [&](const Sequence &q) {
+            return (int64_t)q.n * a.group > a.few_rows ? (q.n * a.group + ROWS - 1) / ROWS : 0;
+        };
+        const int seq = unit_sequence(c, unit, tiles_of, &within);
+        if (seq < 0) {
+            if (a.wide_parts > 1 && part == 0 && threadIdx.x == 0) a.wide_cuts[place].parts = 0;
+            continue;
+        }
+        const Sequence sq = sequence_at(c, seq);
+        // the last rows first: of a prompt, they see the most
+        const Unit u = unit_at(a, seq, sq, tiles_of(sq) - 1 - within, ROWS);
+        int tile_begin = u.lo / kTile, tile_end = u.up > u.lo ? (u.up + kTile - 1) / kTile : tile_begin;
+        if (a.wide_parts > 1) {
+            // whole steps of the unit's tokens in each part
+            const int steps = (tile_end - tile_begin + NT - 1) / NT, from = tile_begin, all = tile_end;
+            tile_begin = from + (int)((int64_t)steps * part / a.wide_parts) * NT;
+            tile_end = min(all, from + (int)((int64_t)steps * (part + 1) / a.wide_parts) * NT);
+        }
+
+        if constexpr (F32) {
+            unit_part<D, FMT, true, RT, 3>(a, sh, u, seq, head, tile_begin, tile_end, 127, place, part);
+        } else {
+            // the largest and the smallest scale of the part's values, but for 0
+            int high = 0, low = 255;
+            const int pages = (tile_end + (1 << tile_shift) - 1) >> tile_shift;
+            for (int from = tile_begin >> tile_shift; from < pages; from += 64) {
+                const int page = from + lane < pages ? pool_page(c, seq, from + lane) : -1;
+                const float scale = page >= 0 ? c.v_scales[(int64_t)page * c.heads + head] : 0.0f;
+                high = max(high, scale != 0.0f ? exponent(scale) : 0);
+                low = min(low, scale != 0.0f ? exponent(scale) : 255);
+            }
+#pragma unroll
+            for (int i = 1; i < 64; i <<= 1) {
+                high = max(high, __shfl_xor(high, i));
+                low = min(low, __shfl_xor(low, i));
+            }
+            high = __builtin_amdgcn_readfirstlane(high);
+            low = __builtin_amdgcn_readfirstlane(low);
+            const int base = max(high - 6, 1);
+            if (high - low <= 10) unit_part<D, FMT, false, RT, 0>(a, sh, u, seq, head, tile_begin, tile_end, base, place, part);
+            else unit_part<D, FMT, false, RT, 2>(a, sh, u, seq, head, tile_begin, tile_end, base, place, part);
+        }
+        if (a.wide_parts > 1 && part == 0 && threadIdx.x == 0) {
+            AttentionCut cut;
+            cut.parts = a.wide_parts;
+            cut.place0 = cut.place = (int)(a.wide_place + place * a.wide_parts * ROWS);
+            cut.step = ROWS;
+            cut.head = head;
+            cut.first = u.q.first;
+            cut.row0 = u.row0;
+            cut.rows = u.rows;
+            a.wide_cuts[place] = cut;
+        }
     }
 }
 

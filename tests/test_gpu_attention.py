@@ -370,6 +370,19 @@ def test_value_scales_of_any_size(name, factor, out):
 
 
 @pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("name,factor", [
+    ("small between", lambda w, s: 2.0 ** (-110 if w % 3 == 1 else 0)), ("small first", lambda w, s: 2.0 ** (-110 if w == 0 else 0)),
+    ("large last", lambda w, s: 2.0 ** (100 if w == 3 else 0)), ("both ends", lambda w, s: 2.0 ** (-90 if w % 2 else 60)),
+    ("steps of 2^40", lambda w, s: 2.0 ** (90 - 40 * (w % 5)))])
+def test_value_scales_over_the_whole_range(name, factor, out):
+    for new, page in (([300, 20], 16), ([280, 70], 64)):
+        c = Call(FP8 if page == 16 else INT8, new, [400, 330], 8, 2, 64 if page == 16 else 128, page, out)
+        scaled(c, 1, factor)
+        c.run()
+        c.check()
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
 def test_key_scales_of_zero(out):
     for new in ([300, 20], [1, 3]):
         c = Call(FP8, new, [400, 130], 8, 2, 64, 16, out, window=200)
