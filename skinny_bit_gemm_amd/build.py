@@ -24,7 +24,8 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-munsafe-fp-a
 SOURCES = ["qlin_gemm_fp8.hip", "qlin_gemm_i8.hip", "qlin_gemm_block.hip", "qlin_kernels.hip",
            "qlin_route.hip", "qlin_expert_rows.hip", "qlin_lora.hip", "qlin_rope.hip",
            "qlin_cache.hip", "qlin_attention.hip", "qlin_attention_wide.hip", "qlin_api.cpp", "qlin_table.cpp"]
-FLAGS = {"qlin_route.hip": ["-fno-honor-nans"]}   # why: see the file
+# why: see the files
+FLAGS = {"qlin_route.hip": ["-fno-honor-nans"], "qlin_attention_wide.hip": ["-fno-honor-nans"]}
 PROBE_SOURCES = ["qlin_probe.hip"]
 
 

@@ -18,16 +18,21 @@
 // which is rare, takes two bf16 terms.  Where y is fp32: three, 24 bits.
 //
 // 3558 tokens of three prompts over up to 8192, 32 query heads over 8 of 128, e4m3, y
-// bf16 (370 GFLOP): 442 us, 840 TFLOP/s.  The powers of two tiles are computed beside the
-// products of the two before, whose operands are read from the LDS a while before: 499 us with
-// all powers first, 491 with reads next to their products.  With two waves a SIMD (of a
-// step, 2050 cycles of the matrix cores, some 3200 of the vector ALUs and 2560 of the LDS)
+// bf16 (370 GFLOP): 420 us, 880 TFLOP/s.  The powers of two tiles are computed beside the
+// products of the two before, whose operands are read from the LDS a while before: 499 us
+// (where this was 442) with all powers first, 491 with reads next to their products.  With two waves a SIMD (of a
+// step's 5700 cycles 2050 of the matrix cores, 2300 of the vector ALUs, 2560 of the LDS)
 // what is left are the waits between them.  Measured and slower: 16 rows a wave and
 // eight waves (674 where this was 500), eight waves of 32 rows (545), steps of 32 tokens
 // (604; with three waves a SIMD 734, spilled), the two tiles of rows one behind the other
 // (740: each reads the LDS for itself, and spills), a base that moves with the scales
 // (557: its path costs the registers of the other), maxima that move each time and a branch for
-// each tile's edge and scale (635), waves of a higher priority in the products (523).
+// each tile's edge and scale (635), waves of a higher priority in the products (523); and
+// where this is 424, a barrier in the middle of a step with three buffers of values (433), and
+// four or twelve reads of values ahead (440, 443).
+//
+// Built with -fno-honor-nans, without which each fmaxf quiets its operands first (436 us,
+// 24 of 267 instructions of a step): what may be NaN in hidden places is replaced as bits.
 #include "qlin_attention.h"
 
 namespace qlin {
@@ -276,13 +281,11 @@ __device__ __forceinline__ void unit_part(const AttentionLaunch &a, Operands<D> 
             }
             convert(gi + 1);                    // past the last step: what was there, into the free buffer
         }
-        if (gi + 2 < groups) load(gi + 2);
         if (needed) {
             // the first values, a while before they are multiplied
             v4u ready[PRE];
 #pragma unroll
             for (int i = 0; i < PRE; ++i) ready[i] = values[b][i][lane];
-            __builtin_amdgcn_sched_barrier(0);
             float kf[NT];
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -297,7 +300,8 @@ __device__ __forceinline__ void unit_part(const AttentionLaunch &a, Operands<D> 
 #pragma unroll
                         for (int rt = 0; rt < RT; ++rt) {
                             const bool sees = there && token + r >= seen[rt].lo && token + r < seen[rt].up;
-                            x[rt][t][r] = sees ? x[rt][t][r] * kf[t] : -INFINITY;
+                            const uint32_t score = __float_as_uint(x[rt][t][r] * kf[t]);
+                            x[rt][t][r] = __uint_as_float(sees ? score : 0xFF800000u);
                         }
                     kf[t] = 1.0f;
                 }
@@ -337,8 +341,12 @@ __device__ __forceinline__ void unit_part(const AttentionLaunch &a, Operands<D> 
                     for (int i = 0; i < 8; ++i) {
                         const float p = x[rt][t + i / 4][i % 4];
                         x[rt][t + i / 4][i % 4] = __builtin_amdgcn_exp2f(__builtin_fmaf(p, kf[t + i / 4], -from[rt]));
-                        l[rt] += x[rt][t + i / 4][i % 4];
                     }
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const v4f s = x[rt][t] + x[rt][t + 1];
+                    l[rt] += (s[0] + s[1]) + (s[2] + s[3]);
+                }
             };
             auto weight_of = [&](int t) {
                 return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(now.weight), lane0 + t));
@@ -355,6 +363,7 @@ __device__ __forceinline__ void unit_part(const AttentionLaunch &a, Operands<D> 
                 });
             }
         }
+        if (gi + 2 < groups) load(gi + 2);
         if ((gi + 1) % AHEAD == 0) now = next;
         __syncthreads();
     }
