@@ -513,6 +513,25 @@ int64_t row_tiles(int64_t sequences, int64_t tokens, int group, int rows) {
 constexpr int kWideItems = 512;    // (unit, head, part) workgroups that wide units are split for
 constexpr int kWideChunk = 256;    // expected tokens of a part, at least
 
+// Parts of a wide unit: the time of a part's steps, 1.5 us each or 2.4 where two workgroups share a
+// compute unit, and of the join: a launch, and partial sums written and read at 4 TB/s.  512 tokens alone
+// (32 / 8 heads of 128) take 20.0 us with one part and 31.3 with two; 512 after 3600, 65 with four and 70
+// with two; 32 tokens of 16 sequences of 2000, 61 with one and 71 with two; 64 over 8000, 27.6
+// with 16 and 30.6 with 32; 100 over 2000 (heads of 64), 18.7 with eight and 31.5 with two.
+int wide_parts(int64_t units, int64_t most, int max_context, int head_dim) {
+    const double steps = max_context / (head_dim <= 128 ? 64.0 : 32.0);
+    const double sums = units * wide_rows(head_dim) * head_dim * 8 / 4e6;
+    int best = 1;
+    double least = 0.0;
+    for (int64_t parts = 1; parts <= std::max<int64_t>(1, std::min(kWideItems / units, most)); ++parts) {
+        const double us = steps / parts * (units * parts > 256 ? 2.4 : 1.5) + (parts > 1 ? 5.0 + sums * parts : 0.0);
+        if (parts > 1 && us >= least) continue;
+        least = us;
+        best = (int)parts;
+    }
+    return best;
+}
+
 }  // namespace
 
 AttentionPlan attention_plan(int sequences, int tokens, int max_context, int kv_heads, int group, int head_dim) {
@@ -544,8 +563,7 @@ AttentionPlan attention_plan(int sequences, int tokens, int max_context, int kv_
     if (wide) {
         p.wide_rows = wide_rows(head_dim);
         p.wide_units = row_tiles(sequences, tokens, group, p.wide_rows) * kv_heads;
-        p.wide_parts = (int)std::max<int64_t>(
-            1, std::min<int64_t>(kWideItems / p.wide_units, (max_context + kWideChunk - 1) / kWideChunk));
+        p.wide_parts = wide_parts(p.wide_units, (max_context + kWideChunk - 1) / kWideChunk, max_context, head_dim);
     }
     // The workspace of any plan of as many or fewer sequences, tokens and context
     if (max_context > std::min(whole, kWideChunk)) {      // else no unit is cut
