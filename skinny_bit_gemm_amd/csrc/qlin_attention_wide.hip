@@ -18,18 +18,19 @@
 // which is rare, takes two bf16 terms.  Where y is fp32: three, 24 bits.
 //
 // 3558 tokens of three prompts over up to 8192, 32 query heads over 8 of 128, e4m3, y
-// bf16 (370 GFLOP): 420 us, 880 TFLOP/s.  The powers of two tiles are computed beside the
-// products of the two before, whose operands are read from the LDS a while before: 499 us
-// (where this was 442) with all powers first, 491 with reads next to their products.  With two waves a SIMD (of a
-// step's 5700 cycles 2050 of the matrix cores, 2300 of the vector ALUs, 2560 of the LDS)
-// what is left are the waits between them.  Measured and slower: 16 rows a wave and
-// eight waves (674 where this was 500), eight waves of 32 rows (545), steps of 32 tokens
-// (604; with three waves a SIMD 734, spilled), the two tiles of rows one behind the other
-// (740: each reads the LDS for itself, and spills), a base that moves with the scales
-// (557: its path costs the registers of the other), maxima that move each time and a branch for
-// each tile's edge and scale (635), waves of a higher priority in the products (523); and
-// where this is 424, a barrier in the middle of a step with three buffers of values (433), and
-// four or twelve reads of values ahead (440, 443).
+// bf16 (370 GFLOP): 424 us, 870 TFLOP/s.  The powers of two tiles are computed beside the
+// products of the two before, whose operands are read from the LDS a while before:
+// where this was 442, 499 us with all powers first, 491 with reads next to their
+// products.  With two waves a SIMD (of a step's 5700 cycles 2050 of the matrix cores, 2300
+// of the vector ALUs, 2560 of the LDS) what is left are the waits between them.
+// Measured and slower: 16 rows a wave and eight waves (674 where this was 500), eight
+// waves of 32 rows (545), steps of 32 tokens (604; with three waves a SIMD 734, spilled),
+// the two tiles of rows one behind the other (740: each reads the LDS for itself, and
+// spills), a base that moves with the scales (557: its path costs the registers of the
+// other), maxima that move each time and a branch for each tile's edge and scale (635),
+// waves of a higher priority in the products (523); and where this is 424, a barrier in
+// the middle of a step with three buffers of values (433), and four or twelve reads of
+// values ahead (440, 443).
 //
 // Built with -fno-honor-nans, without which each fmaxf quiets its operands first (436 us,
 // 24 of 267 instructions of a step): what may be NaN in hidden places is replaced as bits.
