@@ -238,10 +238,11 @@ struct AttentionLaunch {
 };
 
 // Which kernel a sequence is for.  Of several, one with more than kFewRows rows has the wide one (16 sequences of
-// 128 rows over 2000 tokens 80 us, 104 in the other; of 64 rows 61 and 68 the other way round), where the call's rows
-// beyond a token for each are kWideFrom or more: below, the second launch costs more (4 sequences of 128 rows over
-// 4000 tokens 47 us with it, 36 without).  A sequence alone needs no second kernel, only the other one (over 8000 tokens,
-// 128 rows 25.6 and 30.0 us, 512 rows 45 and 58; 64 rows the other way round).
+// 128 rows over 2000 tokens 61 us, 104 in the other; of 64 rows 58 and 51), where the call's rows beyond a token for
+// each are kWideFrom or more: below, the second launch costs more (4 sequences of 128 rows over 4000 tokens 44.7 us
+// with it, 35.7 without).  A sequence alone needs no second kernel, only the other one (128 rows over 8000 tokens 22.7
+// and 30.0 us; 64 rows over 500 tokens 16.3 and 11.9, over 8000 19.9 and 24.6, but with one fp16 number where the
+// other has two bf16 terms, and with those 21.6, and 58.7 and 55.0 over 60000).
 constexpr int kFewRows = 64;
 constexpr int kWideFrom = 512;
 constexpr int kWideFromAlone = 96;

@@ -408,6 +408,13 @@ def test_long_contexts_of_many_rows(D):
     check(FP8, [70, 66], [1 + 2300, 1100], 16, 1, D, 128, BF16, causal=0)
 
 
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_one_sequence_of_some_rows_over_many_tokens(out):
+    for fmt, new, page in ((FP8, 9, 64), (INT8, 16, 16), (FP8, 8, 128)):
+        check(fmt, [new], [5100], 32, 8, 64, page, out)
+        check(fmt, [new], [5100], 32, 8, 128, page, out, window=2000)
+
+
 def test_many_rows_that_see_nothing():
     table = np.array([[-1] * 12, [0, 1, 2] + [-1] * 9, list(range(3, 15))])
     check(FP8, [100, 200, 90], [150, 20, 180], 8, 1, 64, 16, F32, table=table, pages=16)
