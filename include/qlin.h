@@ -629,9 +629,9 @@ typedef struct {
  *       token that sees nothing gets zeros
  * Products with the codes are exact, sums and the softmax are fp32.  The
  * probabilities enter the second product with 24 bits of mantissa where y is
- * fp32; where it is bf16, with 16, or 11 in sequences of many rows (tokens times
- * q_heads / kv_heads: over 64).  y is rounded once.  What lies in absent or unseen
- * tokens' places, NaN codes among it, does not matter.
+ * fp32, with 16 where it is bf16, whatever their size and however many rows a
+ * sequence has.  y is rounded once.  What lies in absent or unseen tokens'
+ * places, NaN codes among it, does not matter.
  * One call takes prompts and single tokens together; its time is best where
  * max_context is near the longest sequence.
  *   workspace  qlin_cache_attention_workspace_bytes(...) bytes (may be 0), of

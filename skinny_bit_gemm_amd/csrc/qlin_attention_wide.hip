@@ -8,59 +8,33 @@
 // consecutive bytes); two buffers, so that the next step is converted while this one
 // is multiplied, and the one behind it is on its way from memory.
 //
-// Where y is bf16, probabilities enter the second product as one fp16 number (11
-// bits of mantissa, 2^-11 against 2^-8 of y's own rounding), and codes as fp16, which
-// holds them exactly.  The scales of the values would leave its range, so they enter
-// relative to a power of two for each part of a unit, which looks at all its pages'
-// scales first: over 2^(base - 127) they are between 2^-4 and 2^7, so no probability
-// times its scale is past fp16's range, and one below fp16's normal numbers is off by
-// 2^-21 of its value's magnitude at most.  A part whose scales differ by more than 2^10,
-// which is rare, takes two bf16 terms.  Where y is fp32: three, 24 bits.
+// Probabilities, times their page's scale, enter the second product as two bf16 terms where y
+// is bf16 (16 bits of mantissa) and three where it is fp32 (24), as in the kernel for few rows, so
+// that a query's result does not depend on how many rows its sequence brings.  One fp16 number (11
+// bits, and fewer below its normal range: a first token with nearly all the weight and a value of 0
+// leaves the others there, and the scales of a unit's pages have to fit its range) takes 424 us
+// where this takes 530.
 //
 // 3558 tokens of three prompts over up to 8192, 32 query heads over 8 of 128, e4m3, y
-// bf16 (370 GFLOP): 424 us, 870 TFLOP/s.  The powers of two tiles are computed beside the
-// products of the two before, whose operands are read from the LDS a while before:
-// where this was 442, 499 us with all powers first, 491 with reads next to their
-// products.  With two waves a SIMD (of a step's 5700 cycles 2050 of the matrix cores, 2300
-// of the vector ALUs, 2560 of the LDS) what is left are the waits between them.
-// Measured and slower: 16 rows a wave and eight waves (674 where this was 500), eight
-// waves of 32 rows (545), steps of 32 tokens (604; with three waves a SIMD 734, spilled),
-// the two tiles of rows one behind the other (740: each reads the LDS for itself, and
-// spills), a base that moves with the scales (557: its path costs the registers of the
-// other), maxima that move each time and a branch for each tile's edge and scale (635),
-// waves of a higher priority in the products (523); and where this is 424, a barrier in
-// the middle of a step with three buffers of values (433), and four or twelve reads of
-// values ahead (440, 443).
+// bf16 (370 GFLOP): 530 us, 700 TFLOP/s; y fp32: 662 us, 560 TFLOP/s.  The powers of two tiles are
+// computed beside the products of the two before, whose operands are read from the LDS a while
+// before.  Two waves a SIMD.  What was measured with one fp16 number, where this was
+// 500 us: all powers first (499), reads next to their products (491) and both as now (442); slower:
+// 16 rows a wave and eight waves (674), eight waves of 32 rows (545), steps of 32 tokens
+// (604; with three waves a SIMD 734, spilled), the two tiles of rows one behind the other (740:
+// each reads the LDS for itself, and spills), maxima that move each time and a branch for each
+// tile's edge and scale (635), waves of a higher priority in the products (523); and where it was
+// 424, a barrier in the middle of a step with three buffers of values (433), and four or twelve
+// reads of values ahead (440, 443).  With two terms the order of the terms' products and a first
+// term that is cut instead of rounded change nothing (526, 526).
 //
-// Built with -fno-honor-nans, without which each fmaxf quiets its operands first (436 us,
-// 24 of 267 instructions of a step): what may be NaN in hidden places is replaced as bits.
+// Built with -fno-honor-nans, without which each fmaxf quiets its operands first (436 us
+// where it was 424, 24 of 267 instructions of a step): what may be NaN in hidden places is replaced as bits.
 #include "qlin_attention.h"
 
 namespace qlin {
 
 namespace {
-
-typedef _Float16 v2h __attribute__((ext_vector_type(2)));
-typedef _Float16 v8h __attribute__((ext_vector_type(8)));
-typedef uint32_t v2u __attribute__((ext_vector_type(2)));
-
-// four codes of a word as fp16 (exact)
-template <int FMT>
-__device__ __forceinline__ uint2 f16_codes(uint32_t w) {
-    if constexpr (FMT == FMT_I8) {
-        // 1024 + (code + 128) is the fp16 number 0x6400 + code + 128
-        const uint32_t u = w ^ 0x80808080u;
-        const v2h off = {(_Float16)1152.0f, (_Float16)1152.0f};
-        const v2h lo = __builtin_bit_cast(v2h, __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u)) - off;
-        const v2h hi = __builtin_bit_cast(v2h, __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u)) - off;
-        return make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
-    }
-    return make_uint2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false)),
-                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true)));
-}
-
-// exponent of a scale's power of two, in fp32's bias; of those too small for it, the lowest
-__device__ __forceinline__ int exponent(float v) { return max((int)(__float_as_uint(v) >> 23 & 0xFFu), 1); }
 
 // A step's tiles, and its operands in the LDS.
 constexpr int tiles_of_step(int D) { return D <= 128 ? 4 : 2; }
@@ -71,12 +45,12 @@ struct Operands {
     v4u values[2][tiles_of_step(D) / 2 * (D / 16)][64];
 };
 
-// A part of a unit: what its tokens of tiles tile_begin to tile_end add.  TERMS: bf16 terms of a
-// probability, or 0 for one fp16 number.
-template <int D, int FMT, bool F32, int RT, int TERMS>
+// A part of a unit: what its tokens of tiles tile_begin to tile_end add.
+template <int D, int FMT, bool F32, int RT>
 __device__ __forceinline__ void unit_part(const AttentionLaunch &a, Operands<D> &sh, const Unit &u, int seq, int head,
-                                          int tile_begin, int tile_end, int base, int64_t place, int part) {
+                                          int tile_begin, int tile_end, int64_t place, int part) {
     constexpr int WROWS = 16 * RT, ROWS = kWaves * WROWS, J = D / 64, DT = D / 16, NT = tiles_of_step(D);
+    constexpr int TERMS = F32 ? 3 : 2;          // of a probability
     constexpr int AHEAD = 64 / NT;
     constexpr int PRE = NT / 2 * DT < 8 ? NT / 2 * DT : 8;
     // a wave's pieces of a step
@@ -124,7 +98,7 @@ __device__ __forceinline__ void unit_part(const AttentionLaunch &a, Operands<D> 
     struct Pages {
         int64_t at;                             // where the tile's codes are
         uint64_t there;                         // lanes whose page is
-        float ks, weight;                       // of keys, and of values times 2^(127 - base)
+        float ks, vs;                           // scales of keys, times the scores', and of values
     };
     Pages next = {0, 0, 0, 0}, now = next;
     auto look_up = [&](int gi) {
@@ -133,7 +107,7 @@ __device__ __forceinline__ void unit_part(const AttentionLaunch &a, Operands<D> 
         const int64_t slot = (int64_t)max(page, 0) * c.heads + head;
         next.there = __ballot(page >= 0);
         next.ks = c.k_scales[slot] * a.scale;
-        next.weight = page >= 0 ? __builtin_ldexpf(c.v_scales[slot], 127 - base) : 0.0f;
+        next.vs = page >= 0 ? c.v_scales[slot] : 0.0f;
         next.at = ((slot << tile_shift) + (tile & ((1 << tile_shift) - 1))) * (kTile * D);
     };
     auto lane_of = [&](int gi) { return gi % AHEAD * NT; };
@@ -194,50 +168,24 @@ __device__ __forceinline__ void unit_part(const AttentionLaunch &a, Operands<D> 
             const uint32_t w0[4] = {vc[i][0].x, vc[i][0].y, vc[i][0].z, vc[i][0].w};
             const uint32_t w1[4] = {vc[i][1].x, vc[i][1].y, vc[i][1].z, vc[i][1].w};
 #pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                v4u w;
-                if constexpr (TERMS > 0) {
-                    w = __builtin_bit_cast(v4u, operand<FMT>(w0[d], w1[d]));
-                } else {
-                    const uint2 lo = f16_codes<FMT>(w0[d]), hi = f16_codes<FMT>(w1[d]);
-                    w = v4u{lo.x, lo.y, hi.x, hi.y};
-                }
-                values[b][t * DT + 4 * j + d][lane] = w;
-            }
+            for (int d = 0; d < 4; ++d)
+                values[b][t * DT + 4 * j + d][lane] = __builtin_bit_cast(v4u, operand<FMT>(w0[d], w1[d]));
         }
     };
 
     // y += V^T P^T of tiles t and t + 1, their probabilities times f0 and f1
     auto multiply = [&](int t, const v4f (&x)[RT][NT], float f0, float f1, auto &&value) {
-        if constexpr (TERMS > 0) {
-            v8bf p[RT][TERMS];
+        v8bf p[RT][TERMS];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) terms<TERMS>(x[rt][t] * f0, x[rt][t + 1] * f1, p[rt]);
+        for (int rt = 0; rt < RT; ++rt) terms<TERMS>(x[rt][t] * f0, x[rt][t + 1] * f1, p[rt]);
 #pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                const v8bf v = __builtin_bit_cast(v8bf, value(d));
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int n = 0; n < TERMS; ++n)
-                        y[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[rt][n], y[rt][d], 0, 0, 0);
-            }
-        } else {
-            v8h p[RT];
+        for (int d = 0; d < DT; ++d) {
+            const v8bf v = __builtin_bit_cast(v8bf, value(d));
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    p[rt][i] = (_Float16)(x[rt][t][i] * f0);
-                    p[rt][4 + i] = (_Float16)(x[rt][t + 1][i] * f1);
-                }
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                const v8h v = __builtin_bit_cast(v8h, value(d));
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-                    y[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p[rt], y[rt][d], 0, 0, 0);
-            }
+                for (int n = 0; n < TERMS; ++n)
+                    y[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[rt][n], y[rt][d], 0, 0, 0);
         }
     };
 
@@ -349,14 +297,14 @@ __device__ __forceinline__ void unit_part(const AttentionLaunch &a, Operands<D> 
                     l[rt] += (s[0] + s[1]) + (s[2] + s[3]);
                 }
             };
-            auto weight_of = [&](int t) {
-                return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(now.weight), lane0 + t));
+            auto vs_of = [&](int t) {
+                return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(now.vs), lane0 + t));
             };
             // powers of two tiles beside the products of the two before
 #pragma unroll
             for (int t = 0; t < NT; t += 2) {
                 powers(t);
-                multiply(t, x, weight_of(t), weight_of(t + 1), [&](int d) {
+                multiply(t, x, vs_of(t), vs_of(t + 1), [&](int d) {
                     const int piece = t / 2 * DT + d;
                     const v4u v = ready[piece % PRE];
                     if (piece + PRE < NT / 2 * DT) ready[piece % PRE] = values[b][piece + PRE][lane];
@@ -369,7 +317,6 @@ __device__ __forceinline__ void unit_part(const AttentionLaunch &a, Operands<D> 
         __syncthreads();
     }
 
-    const float unit_of_y = __builtin_ldexpf(1.0f, base - 127);
     const int64_t first_place = a.wide_place + (place * a.wide_parts + part) * ROWS;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -379,10 +326,10 @@ __device__ __forceinline__ void unit_part(const AttentionLaunch &a, Operands<D> 
         if (a.wide_parts > 1) {
 #pragma unroll
             for (int d = 0; d < DT; ++d)
-                *reinterpret_cast<v4f *>(a.part_o + (first_place + row) * D + 16 * d + 4 * g) = y[rt][d] * unit_of_y;
+                *reinterpret_cast<v4f *>(a.part_o + (first_place + row) * D + 16 * d + 4 * g) = y[rt][d];
             if (g == 0) a.part_ml[first_place + row] = make_float2(m[rt], total);
         } else {
-            const float by = total > 0.0f ? unit_of_y / total : 0.0f;
+            const float by = total > 0.0f ? 1.0f / total : 0.0f;
             const int64_t to = row_at(a, u, row, a.ldy, head, D);
 #pragma unroll
             for (int d = 0; d < DT; ++d) store_y4<F32>(a.y, to + 16 * d + 4 * g, y[rt][d] * by);
@@ -395,7 +342,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void wide_kernel(AttentionLaunch a)
     constexpr int ROWS = kWaves * 16 * RT, NT = tiles_of_step(D);
     __shared__ Operands<D> sh;
     const CacheArgs &c = a.c;
-    const int lane = threadIdx.x & 63, tile_shift = c.page_shift - 4;
 
     const int64_t items = a.wide_units * a.wide_parts;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
@@ -422,29 +368,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void wide_kernel(AttentionLaunch a)
             tile_end = min(all, from + (int)((int64_t)steps * (part + 1) / a.wide_parts) * NT);
         }
 
-        if constexpr (F32) {
-            unit_part<D, FMT, true, RT, 3>(a, sh, u, seq, head, tile_begin, tile_end, 127, place, part);
-        } else {
-            // the largest and the smallest scale of the part's values, but for 0
-            int high = 0, low = 255;
-            const int pages = (tile_end + (1 << tile_shift) - 1) >> tile_shift;
-            for (int from = tile_begin >> tile_shift; from < pages; from += 64) {
-                const int page = from + lane < pages ? pool_page(c, seq, from + lane) : -1;
-                const float scale = page >= 0 ? c.v_scales[(int64_t)page * c.heads + head] : 0.0f;
-                high = max(high, scale != 0.0f ? exponent(scale) : 0);
-                low = min(low, scale != 0.0f ? exponent(scale) : 255);
-            }
-#pragma unroll
-            for (int i = 1; i < 64; i <<= 1) {
-                high = max(high, __shfl_xor(high, i));
-                low = min(low, __shfl_xor(low, i));
-            }
-            high = __builtin_amdgcn_readfirstlane(high);
-            low = __builtin_amdgcn_readfirstlane(low);
-            const int base = max(high - 6, 1);
-            if (high - low <= 10) unit_part<D, FMT, false, RT, 0>(a, sh, u, seq, head, tile_begin, tile_end, base, place, part);
-            else unit_part<D, FMT, false, RT, 2>(a, sh, u, seq, head, tile_begin, tile_end, base, place, part);
-        }
+        unit_part<D, FMT, F32, RT>(a, sh, u, seq, head, tile_begin, tile_end, place, part);
         if (a.wide_parts > 1 && part == 0 && threadIdx.x == 0) {
             AttentionCut cut;
             cut.parts = a.wide_parts;

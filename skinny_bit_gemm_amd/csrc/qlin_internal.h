@@ -240,9 +240,8 @@ struct AttentionLaunch {
 // Which kernel a sequence is for.  Of several, one with more than kFewRows rows has the wide one (16 sequences of
 // 128 rows over 2000 tokens 61 us, 104 in the other; of 64 rows 58 and 51), where the call's rows beyond a token for
 // each are kWideFrom or more: below, the second launch costs more (4 sequences of 128 rows over 4000 tokens 44.7 us
-// with it, 35.7 without).  A sequence alone needs no second kernel, only the other one (128 rows over 8000 tokens 22.7
-// and 30.0 us; 64 rows over 500 tokens 16.3 and 11.9, over 8000 19.9 and 24.6, but with one fp16 number where the
-// other has two bf16 terms, and with those 21.6, and 58.7 and 55.0 over 60000).
+// with it, 35.7 without).  A sequence alone needs no second kernel, only the other one (128 rows over 8000 tokens 23.5
+// and 29.0 us, over 600 19.1 and 13.4; 64 rows over 8000 20.2 and 24.3, over 600 16.8 and 12.0).
 constexpr int kFewRows = 64;
 constexpr int kWideFrom = 512;
 constexpr int kWideFromAlone = 96;
