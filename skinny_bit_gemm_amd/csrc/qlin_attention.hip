@@ -547,10 +547,15 @@ AttentionPlan attention_plan(int sequences, int tokens, int max_context, int kv_
     const bool wide = sequences == 1 ? all_rows >= kWideFromAlone
                                      : (tokens - std::min(sequences, tokens)) * (int64_t)group >= kWideFrom;
     const bool few = !wide || sequences > 1;
-    p.few_rows = !wide ? INT32_MAX : few ? kFewRows : 0;
+    p.few_rows = !wide ? INT32_MAX : few ? few_rows(head_dim) : 0;
     if (few) {
-        // 16 rows in a unit, or 32: as a sequence has on average, or a single token beside sequences with many
-        p.rows = all_rows <= 16 * (int64_t)sequences || (wide && group <= 16) ? 16 : 32;
+        // 16 rows in a unit, or 32: as a sequence has on average.  An average beyond this kernel's sequences says that
+        // some have many rows, and then 16 for the others, single tokens for the most part.  Between 16 and that it is
+        // drafts (4 tokens of 64 sequences of 4096, 8 query heads a key head: 98 us with 32 rows, 175 with 16, which read all
+        // codes twice), or single tokens beside a prompt that draws the average up, which lose less (400 tokens beside 63
+        // single ones over 2000, 4 query heads a key head: 112.6 with 32 rows, 109 with 16; 1000 of 128 over 1000: 92.6 and 87.5).
+        const bool prompts = wide && all_rows > few_rows(head_dim) * (int64_t)sequences;
+        p.rows = all_rows <= 16 * (int64_t)sequences || (prompts && group <= 16) ? 16 : 32;
         p.live_rows = (int)std::min<int64_t>(p.rows, all_rows);
         const int64_t units = row_tiles(sequences, tokens, group, p.rows) * kv_heads;
         p.whole = max_context <= whole;
