@@ -594,7 +594,8 @@ qlin_status qlin_cache_bytes(const qlin_cache *cache, size_t *code_bytes, size_t
  * behind a sequence's last (a draft that was not taken) can be stored over: give
  * the shorter length; the scale does not shrink until the page starts anew.
  * A page may be in several sequences' tables (a shared prefix) as long as no
- * call stores into it; into one page, only one sequence of a call may store.
+ * call stores into it; into one page, only one sequence of a call may store, and
+ * only by one entry of its table.
  * Keys and values are finite.
  * Errors: QLIN_ERR_INVALID_ARG (a null pointer, a field or type out of range),
  * QLIN_ERR_SHAPE (a count out of range), QLIN_ERR_ALIGNMENT. */
@@ -630,8 +631,10 @@ typedef struct {
  * Products with the codes are exact, sums and the softmax are fp32.  The
  * probabilities enter the second product with 24 bits of mantissa where y is
  * fp32, with 16 where it is bf16, whatever their size and however many rows a
- * sequence has.  y is rounded once.  What lies in absent or unseen tokens'
- * places, NaN codes among it, does not matter.
+ * sequence has.  y is rounded once.  Sums of values are kept times up to 2^8:
+ * values of a channel whose magnitudes sum to less than 2^119 over the tokens do
+ * not overflow.  What lies in absent or unseen tokens' places, NaN codes among
+ * it, does not matter.
  * One call takes prompts and single tokens together; its time is best where
  * max_context is near the longest sequence.
  *   workspace  qlin_cache_attention_workspace_bytes(...) bytes (may be 0), of

@@ -116,3 +116,15 @@ def test_rows_that_see_small_scales_alone(out, small, large):
         c = Call(fmt, [200, 90], [200, 90], 8, 2, 64, page, out, seed=4)
         scaled(c, 1, lambda w, s: 2.0 ** (small if w == 0 else large if w == 2 else 0))
         check(c)
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_large_values(out):
+    """Values whose magnitudes sum to nearly 2^119 over the tokens."""
+    for fmt, new, lengths in ((FP8, [300], [400]), (INT8, [1, 2], [700, 30]), (FP8, [130, 1], [1500, 40])):
+        c = Call(fmt, new, lengths, 8, 2, 64, 64, out, seed=5)
+        most = max(np.abs(c.ref.exact(1, c.table, s, range(n))).sum(0).max() for s, n in enumerate(lengths))
+        factor = 2.0 ** np.floor(119 - np.log2(most))
+        assert factor * most < 2.0 ** 119
+        scaled(c, 1, lambda w, s: factor)
+        check(c)
