@@ -28,7 +28,7 @@ constexpr int kStep = 128;         // tokens: two tiles of 16 for each wave
 // with it; of 1000 the other way round, 12.2 and 10.5).
 //
 // 64 sequences of 300 to 16384 tokens, 64 query heads over 8 of 128, e4m3 (534 MB of
-// codes): 100 us, 92 of them this kernel, 5.8 TB/s; equal parts of each sequence
+// codes): 100 us a call, 93 traced for this kernel, 5.7 TB/s; equal parts of each sequence
 // instead, 164.  131071 tokens of one sequence, 269 MB: 51 us.  What the steps
 // measured: codes of the next step asked for while this one is multiplied, and their
 // stream with the non-temporal policy, each 10 %.
@@ -515,9 +515,10 @@ constexpr int kWideChunk = 256;    // expected tokens of a part, at least
 
 // Parts of a wide unit: the time of a part's steps, 1.5 us each or 2.4 where two workgroups share a
 // compute unit, and of the join: a launch, and partial sums written and read at 4 TB/s.  512 tokens alone
-// (32 / 8 heads of 128) take 20.0 us with one part and 31.3 with two; 512 after 3600, 65 with four and 70
-// with two; 32 tokens of 16 sequences of 2000, 61 with one and 71 with two; 64 over 8000, 27.6
-// with 16 and 30.6 with 32; 100 over 2000 (heads of 64), 18.7 with eight and 31.5 with two.
+// (32 / 8 heads of 128) take 21.9 us with one part and 32.9 with two; 512 after 3600, 73 with four and 81
+// with two; 64 over 8000, 29.0 with 16, 31.4 with 32 and 40.6 with eight; 100 over 2000 (heads of 64),
+// 19.0 with eight and 23.8 with four.  (Steps are 1.7 and 3.0 us with two terms; chosen by those, 192 rows
+// alone over 30000 tokens take 66 us for 58, 512 rows 105 for 112, and most calls the same.)
 int wide_parts(int64_t units, int64_t most, int max_context, int head_dim) {
     const double steps = max_context / (head_dim <= 128 ? 64.0 : 32.0);
     const double sums = units * wide_rows(head_dim) * head_dim * 8 / 4e6;

@@ -5,8 +5,8 @@
 // values, so the page's scale needs no exchange between workgroups, and a call is one
 // launch.  Rows are read and written 16 consecutive bytes a lane; the tiles' order of
 // bytes (include/qlin.h) is made in the LDS.  Bytes bound the large calls: prompts of
-// 11489 tokens (8 heads of 128, bf16, 70 MB) are stored in 21.3 us, 42974 tokens (264
-// MB) read back in 49.8, 5.3 TB/s; 63 without the non-temporal policy on what is
+// 11489 tokens (8 heads of 128, bf16, 70 MB) are stored in 23 us, 42974 tokens (264
+// MB) read back in 50.4, 5.2 TB/s; 63 without the non-temporal policy on what is
 // written, which nobody reads soon.  Small calls are a chain of dependent loads: offsets
 // and lengths, the page, its scale, 5.0 us with the launch.
 #include "qlin_sequences.h"
@@ -21,7 +21,11 @@ constexpr int kTile = 16;                    // tokens of a tile
 constexpr int kRowPad = 16;                  // bytes behind each LDS row of codes
 // Tokens a sequence, on average, up to which a wave has a page and head, not a
 // workgroup.  32 sequences, us a call: 8 tokens each 5.0 and 5.0, 16 tokens 5.6 and 4.9,
-// 64 tokens 17.5 and 8.0; 256 sequences of one token 5.7 and 16.3.
+// 64 tokens 17.5 and 8.0; 256 sequences of one token 5.7 and 16.3.  The host knows counts alone, so a
+// long prompt beside many slots without tokens is the waves' too: one of 2000 tokens in 251 slots, 8
+// heads of 128, pages of 64, 19.8 us where workgroups take 13.5; 8 of 256, pages of 128, 94 and 31.
+// (A wave with eight loads on their way, 21.8 and 69; long pages by four waves together through
+// the LDS, 19.8 and 53, but 512 sequences of one token with pages of 128 then take 16.6 for 9.8.)
 constexpr int kFewTokens = 8;
 
 // four codes of a word as fp32

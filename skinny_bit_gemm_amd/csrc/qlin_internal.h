@@ -242,7 +242,7 @@ struct AttentionLaunch {
 // of 128 rows over 4000 tokens, 32 query heads over 8 of 128: 40.2 us with them, 34.9 without).  us a call with both
 // kernels launched, in the wide and in the other, 16 sequences of some rows over some tokens, the same heads:
 //   128 wide: 128 rows over 600 32 and 28, over 2000 70 and 58, over 8000 210 and 190; 96 rows over 600 31 and 41,
-//             over 2000 69 and 61, over 8000 201 and 165; 192 rows over 2000 68 and 96, over 8000 247 and 305
+//             over 2000 69 and 61, over 8000 201 and 165; 192 rows over 2000 68 and 90, over 8000 249 and 298
 //   256 wide: 128 rows over 2000 98 and 109, over 8000 343 and 373; 96 rows 95 and 92, 331 and 303; 64 rows 98 and 57
 // A sequence alone needs no second kernel, only the other one (128 rows over 8000 tokens 23.5
 // and 29.0 us, over 600 19.1 and 13.4; 64 rows over 8000 20.2 and 24.3, over 600 16.8 and 12.0).
