@@ -18,15 +18,15 @@
 // 3558 tokens of three prompts over up to 8192, 32 query heads over 8 of 128, e4m3, y
 // bf16 (370 GFLOP): 530 us, 700 TFLOP/s; y fp32: 662 us, 560 TFLOP/s.  The powers of two tiles are
 // computed beside the products of the two before, whose operands are read from the LDS a while
-// before.  Two waves a SIMD.  What was measured with one fp16 number, where this was
-// 500 us: all powers first (499), reads next to their products (491) and both as now (442); slower:
-// 16 rows a wave and eight waves (674), eight waves of 32 rows (545), steps of 32 tokens
-// (604; with three waves a SIMD 734, spilled), the two tiles of rows one behind the other (740:
-// each reads the LDS for itself, and spills), maxima that move each time and a branch for each
-// tile's edge and scale (635), waves of a higher priority in the products (523); and where it was
-// 424, a barrier in the middle of a step with three buffers of values (433), and four or twelve
-// reads of values ahead (440, 443).  With two terms the order of the terms' products and a first
-// term that is cut instead of rounded change nothing (526, 526).
+// before.  Two waves a SIMD.  Chosen while probabilities were one fp16 number, by us of the same
+// call: where it took 500, all powers first 499, reads next to their products 491, both as
+// now 442; 16 rows a wave and eight waves 674, eight waves of 32 rows 545, steps of 32 tokens
+// 604 (with three waves a SIMD 734, spilled), the two tiles of rows one behind the other 740
+// (each reads the LDS for itself, and spills), maxima that move each time and a branch for each
+// tile's edge and scale 635, waves of a higher priority in the products 523; where it took
+// 424, a barrier in the middle of a step with three buffers of values 433, four or twelve
+// reads of values ahead 440, 443.  With two terms, the order of the terms' products and a first
+// term that is cut instead of rounded change nothing (526 each).
 //
 // Built with -fno-honor-nans, without which each fmaxf quiets its operands first (436 us
 // where it was 424, 24 of 267 instructions of a step): what may be NaN in hidden places is replaced as bits.
