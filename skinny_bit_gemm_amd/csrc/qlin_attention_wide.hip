@@ -10,7 +10,7 @@
 //
 // Probabilities, times their page's scale, enter the second product as two bf16 terms where y
 // is bf16 (16 bits of mantissa) and three where it is fp32 (24), as in the kernel for few rows, so
-// that a query's result does not depend on how many rows its sequence brings.  One fp16 number (11
+// that a query's result is as exact however many rows its sequence brings.  One fp16 number (11
 // bits, and fewer below its normal range: a first token with nearly all the weight and a value of 0
 // leaves the others there, and the scales of a unit's pages have to fit its range) takes 424 us
 // where this takes 530.
@@ -29,7 +29,8 @@
 // term that is cut instead of rounded change nothing (526 each).
 //
 // Built with -fno-honor-nans, without which each fmaxf quiets its operands first (436 us
-// where it was 424, 24 of 267 instructions of a step): what may be NaN in hidden places is replaced as bits.
+// where it was 424, 24 of 267 instructions of a step): what may be NaN in hidden places is
+// replaced as bits.
 #include "qlin_attention.h"
 
 namespace qlin {
